@@ -354,6 +354,107 @@ mamba_status mamba_ssd_scan_fwd(const void *x, const void *dt, const float *dt_b
                                 int64_t G, int64_t N, mamba_dtype io, void *stream);
 
 /*
+ * Root-mean-square norm with the residual's addition, the step in front of a
+ * block's in-projection.  Per row of D elements, in fp32:
+ *   h = x + residual                       (residual NULL: h = x)
+ *   residual_out = h                       rounded to the residual's type
+ *   out = h / sqrt(mean(h^2) + eps) * weight   rounded to x's type
+ * out is formed from the unrounded h.
+ *   x, out                 : [M, D] of `io`
+ *   residual, residual_out : [M, D] of `residual_type`, which is fp32 or `io`;
+ *                            residual may be NULL (then residual_out must be,
+ *                            and residual_type is ignored), residual_out may
+ *                            be NULL (not returned) or the same buffer as
+ *                            residual (updated in place)
+ *   weight                 : [D] float, required
+ *   eps                    : finite, >= 0 (else MAMBA_ERR_SHAPE)
+ * D in 1..32768 (MAMBA_MAX_NORM_WIDTH), M < 2^22.  The square sum is an fp32
+ * sum: rows whose sum of squares passes the fp32 range give zeros or NaN.
+ * Except for that in-place update, outputs must not overlap inputs or each
+ * other.
+ */
+#define MAMBA_MAX_NORM_WIDTH 32768
+mamba_status mamba_rms_norm(const void *x, const void *residual, const float *weight, void *out,
+                            void *residual_out, int64_t M, int64_t D, float eps, mamba_dtype io,
+                            mamba_dtype residual_type, void *stream);
+
+/*
+ * The same norm with its output in 8-bit integers and one scale per row, the
+ * left operand of mamba_int8_matmul:
+ *   scale[m] = max_d|y| / 127,   out[m, d] = round(y * 127 / max_d|y|)
+ * (to nearest, ties to even; values in -127..127), y the unrounded norm.  A
+ * zero row has scale 0; a row with a NaN or an infinity has scale NaN and
+ * zeros, so that everything computed from it is NaN.
+ *   out : [M, D] int8;  scale : [M] float
+ */
+mamba_status mamba_rms_norm_int8(const void *x, const void *residual, const float *weight, int8_t *out,
+                                 float *scale, void *residual_out, int64_t M, int64_t D, float eps,
+                                 mamba_dtype io, mamba_dtype residual_type, void *stream);
+
+/*
+ * Gradient of mamba_rms_norm.  With h the stored sum (the forward call's
+ * residual_out, or x where it had no residual), r = 1/sqrt(mean(h^2) + eps)
+ * recomputed from it, and dresidual_out the gradient that reaches residual_out
+ * (NULL = zero):
+ *   dh = r weight dy - h r^3 mean(weight dy h) + dresidual_out
+ *   dweight = sum over rows of dy h r
+ * dh is the gradient of both x and the residual.
+ *   dy, dx                      : [M, D] of `io`
+ *   h, dresidual_out, dresidual : [M, D] of `h_type`, which is fp32 or `io`
+ *   dx                          : dh rounded to `io`, required
+ *   dresidual                   : dh rounded to `h_type`, or NULL (not
+ *                                 returned); must be NULL when h_type is io
+ *                                 (dx is then the residual's gradient too)
+ *   weight, dweight             : [D] float, required
+ *   workspace                   : mamba_rms_norm_bwd_workspace_size(M, D) bytes,
+ *                                 256-byte aligned; scratch as in the scan
+ * Sums are taken in a fixed order.  With M = 0, dweight is zero.
+ */
+size_t mamba_rms_norm_bwd_workspace_size(int64_t M, int64_t D);
+mamba_status mamba_rms_norm_bwd(const void *dy, const void *h, const float *weight, const void *dresidual_out,
+                                void *dx, void *dresidual, float *dweight, void *workspace,
+                                size_t workspace_bytes, int64_t M, int64_t D, float eps, mamba_dtype io,
+                                mamba_dtype h_type, void *stream);
+
+/*
+ * Quantisation of rows to 8-bit integers with a scale each (the rounding and
+ * the special rows of mamba_rms_norm_int8): activations with a scale per
+ * token, or a weight [N, K] with a scale per output channel (B = 1, L = N).
+ *   channel_major 0 : x [B, L, K] of `io`, K at most 32768
+ *   channel_major 1 : x [B, K, L] of `io`, as the scans write their output
+ *   q               : [B, L, K] int8;  scale : [B, L] float
+ * B * L < 2^22; K at least 1 unless B * L is 0.
+ */
+mamba_status mamba_quantize_int8(const void *x, int8_t *q, float *scale, int64_t B, int64_t L, int64_t K,
+                                 int channel_major, mamba_dtype io, void *stream);
+
+/* Flags of mamba_int8_matmul: the operand is one matrix, used by every batch. */
+#define MAMBA_INT8_SHARED_A 1u
+#define MAMBA_INT8_SHARED_B 2u
+
+/*
+ * Product of 8-bit integers with a scale for each row of both operands:
+ *   out[i, m, n] = a_scale[i, m] * b_scale[i, n] * sum_k a[i, m, k] * b[i, n, k]
+ * The sum is exact; it is converted to fp32, multiplied by a_scale and then by
+ * b_scale, and rounded once.  Both operands have the inner axis last, so a
+ * projection y = x W^T takes x's rows (tokens) and W's rows (output channels)
+ * as they are, either on the left: with W as `a` and the tokens as `b`, `out`
+ * is channel-major, as the scans take it.
+ *   a, a_scale : [batch, M, K] int8, [batch, M] float; with MAMBA_INT8_SHARED_A
+ *                [M, K] and [M]
+ *   b, b_scale : [batch, N, K], [batch, N]; with MAMBA_INT8_SHARED_B [N, K], [N]
+ *   out        : [batch, M, N] of `out_type`
+ *   workspace  : mamba_int8_matmul_workspace_size(batch, M, N, K) bytes (0 for
+ *                most shapes), 256-byte aligned; scratch as in the scan
+ * Any K from 0 (zeros) to 131071, at any alignment; K a multiple of 16 with
+ * 16-byte aligned operands is fastest.
+ */
+size_t mamba_int8_matmul_workspace_size(int64_t batch, int64_t M, int64_t N, int64_t K);
+mamba_status mamba_int8_matmul(const int8_t *a, const int8_t *b, const float *a_scale, const float *b_scale,
+                               void *out, void *workspace, size_t workspace_bytes, int64_t batch, int64_t M,
+                               int64_t N, int64_t K, mamba_dtype out_type, unsigned flags, void *stream);
+
+/*
  * Profiling hook.  When both are non-NULL hipEvent_t handles (passed as
  * void*), later calls made from this host thread record `start` right before
  * and `stop` right after the main scan kernel of mamba_selective_scan_fwd (and

@@ -21,6 +21,11 @@ Entry points (same names as the C ABI, without the ``mamba_`` prefix):
   ssd_scan_fwd(x, dt, A, Bm, Cm, dt_bias=None, Dskip=None, z=None, h0=None,
                return_last_state=False, out=None, h_last=None)
   selective_scan_fwd_noalloc(x, dt, A, Bm, Cm, ..., out=None, h_last=None)
+  rms_norm(x, weight, residual=None, eps=1e-5, out=None, residual_out=None)
+  rms_norm_int8(x, weight, residual=None, eps=1e-5, out=None, scale=None, residual_out=None)
+  rms_norm_bwd(dy, h, weight, dresidual_out=None, eps=1e-5, workspace=None)
+  quantize_int8(x, channel_major=False, out=None, scale=None)
+  int8_matmul(a, b, a_scale, b_scale, out_dtype=torch.bfloat16, out=None, workspace=None)
   selective_scan_check(workspace)        the carry's error word (after a sync)
   set_scan_spin_limit(polls)             diagnostic bound of the carry waits
 Test helper: set_carry_checks(True) checks the carry after every scan call.
@@ -53,7 +58,9 @@ EXPORTED = ["mamba_status_string", "mamba_abi_version", "mamba_conv1d_silu",
             "mamba_selective_scan_bwd_workspace_size", "mamba_selective_scan_bwd",
             "mamba_ssd_scan_fwd", "mamba_conv1d_selective_state_update",
             "mamba_selective_scan_check", "mamba_set_scan_spin_limit",
-            "mamba_selective_scan_fwd_noalloc"]
+            "mamba_selective_scan_fwd_noalloc", "mamba_rms_norm", "mamba_rms_norm_int8",
+            "mamba_rms_norm_bwd_workspace_size", "mamba_rms_norm_bwd", "mamba_quantize_int8",
+            "mamba_int8_matmul_workspace_size", "mamba_int8_matmul"]
 
 _lib = None
 
@@ -115,6 +122,21 @@ def load_library(path: str = LIBRARY):
     lib.mamba_selective_scan_check.argtypes = [P, SZ, P]
     lib.mamba_set_scan_spin_limit.restype = None
     lib.mamba_set_scan_spin_limit.argtypes = [I32]
+    U32, F = ctypes.c_uint, ctypes.c_float
+    lib.mamba_rms_norm.restype = I32
+    lib.mamba_rms_norm.argtypes = [P] * 5 + [I64, I64, F, I32, I32, P]
+    lib.mamba_rms_norm_int8.restype = I32
+    lib.mamba_rms_norm_int8.argtypes = [P] * 6 + [I64, I64, F, I32, I32, P]
+    lib.mamba_rms_norm_bwd_workspace_size.restype = SZ
+    lib.mamba_rms_norm_bwd_workspace_size.argtypes = [I64, I64]
+    lib.mamba_rms_norm_bwd.restype = I32
+    lib.mamba_rms_norm_bwd.argtypes = [P] * 8 + [SZ, I64, I64, F, I32, I32, P]
+    lib.mamba_quantize_int8.restype = I32
+    lib.mamba_quantize_int8.argtypes = [P] * 3 + [I64, I64, I64, I32, I32, P]
+    lib.mamba_int8_matmul_workspace_size.restype = SZ
+    lib.mamba_int8_matmul_workspace_size.argtypes = [I64] * 4
+    lib.mamba_int8_matmul.restype = I32
+    lib.mamba_int8_matmul.argtypes = [P] * 6 + [SZ, I64, I64, I64, I64, I32, U32, P]
     _lib = lib
     return lib
 
@@ -161,6 +183,14 @@ def _check(t, name, shape, dtype=None, device=None, optional=False):
 
 def _stream(device):
     return ctypes.c_void_p(_torch().cuda.current_stream(device).cuda_stream)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(t):
+    return _torch().cuda.current_stream(t.device).cuda_stream
 
 
 def _raise(st, where):
@@ -540,6 +570,190 @@ def ssd_scan_fwd(x, dt, A, Bm, Cm, dt_bias=None, Dskip=None, z=None, h0=None,
     _raise(st, "mamba_ssd_scan_fwd")
     if return_last_state:
         return out, h_last
+    return out
+
+
+def _norm_arguments(x, weight, residual, residual_out):
+    """Checks shared by the two forward norms; returns (rows, D, residual_out)."""
+    torch = _torch()
+    if x.dim() < 1:
+        raise ValueError("x has no axis to normalise")
+    shape, dev = x.shape, x.device
+    D = shape[-1]
+    _check(x, "x", shape)
+    _check(weight, "weight", (D,), torch.float32, dev)
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs residual")
+    else:
+        if residual.dtype != torch.float32 and residual.dtype != x.dtype:
+            raise TypeError(f"residual must be float32 or {x.dtype}, got {residual.dtype}")
+        _check(residual, "residual", shape, device=dev)
+        if residual_out is None:
+            residual_out = torch.empty_like(residual)
+        else:
+            _check(residual_out, "residual_out", shape, residual.dtype, dev)
+    return _rows(x), D, residual_out
+
+
+def _rows(x):
+    rows = 1
+    for n in x.shape[:-1]:
+        rows *= n
+    return rows
+
+
+def rms_norm(x, weight, residual=None, eps=1e-5, out=None, residual_out=None):
+    """Root-mean-square norm over the last axis with the residual's addition:
+    h = x + residual, out = h / sqrt(mean(h^2) + eps) * weight.  x [..., D]
+    f32/bf16; weight [D] f32; residual [..., D] f32 or x's dtype.  Returns out
+    of x's dtype, and with a residual (out, residual_out): h in the residual's
+    dtype (`residual_out` may be `residual` itself, updated in place)."""
+    torch = _torch()
+    lib = load_library()
+    M, D, residual_out = _norm_arguments(x, weight, residual, residual_out)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _check(out, "out", x.shape, x.dtype, x.device)
+    st = lib.mamba_rms_norm(_addr(x), _addr(residual), _addr(weight), _addr(out),
+                            _addr(residual_out), M, D, eps, _io_dtype(x),
+                            0 if residual is None else _io_dtype(residual), _raw_stream(x))
+    _raise(st, "mamba_rms_norm")
+    return out if residual is None else (out, residual_out)
+
+
+def rms_norm_int8(x, weight, residual=None, eps=1e-5, out=None, scale=None, residual_out=None):
+    """rms_norm with its output in 8-bit integers and a scale per row (the
+    left operand of int8_matmul): scale = max|y| / 127, q = round(y / scale).
+    Returns (q [..., D] int8, scale [...] f32), and residual_out with a
+    residual.  A row with a NaN or an infinity has scale NaN."""
+    torch = _torch()
+    lib = load_library()
+    M, D, residual_out = _norm_arguments(x, weight, residual, residual_out)
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+    else:
+        _check(out, "out", x.shape, torch.int8, x.device)
+    if scale is None:
+        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    else:
+        _check(scale, "scale", x.shape[:-1], torch.float32, x.device)
+    st = lib.mamba_rms_norm_int8(_addr(x), _addr(residual), _addr(weight), _addr(out),
+                                 _addr(scale), _addr(residual_out), M, D, eps, _io_dtype(x),
+                                 0 if residual is None else _io_dtype(residual), _raw_stream(x))
+    _raise(st, "mamba_rms_norm_int8")
+    return (out, scale) if residual is None else (out, scale, residual_out)
+
+
+def rms_norm_bwd(dy, h, weight, dresidual_out=None, eps=1e-5, workspace=None):
+    """Gradient of rms_norm.  dy [..., D] f32/bf16; h [..., D] the stored sum
+    (residual_out of the forward call, or its x where it had no residual) in
+    f32 or dy's dtype; dresidual_out the gradient that reaches residual_out, of
+    h's dtype, or None.  Returns a dict: dx of dy's dtype, dresidual of h's
+    dtype (the same tensor as dx where the dtypes are equal), dweight [D] f32."""
+    torch = _torch()
+    lib = load_library()
+    if dy.dim() < 1:
+        raise ValueError("dy has no axis to normalise")
+    shape, dev = dy.shape, dy.device
+    D = shape[-1]
+    _check(dy, "dy", shape)
+    if h.dtype != torch.float32 and h.dtype != dy.dtype:
+        raise TypeError(f"h must be float32 or {dy.dtype}, got {h.dtype}")
+    _check(h, "h", shape, device=dev)
+    _check(weight, "weight", (D,), torch.float32, dev)
+    _check(dresidual_out, "dresidual_out", shape, h.dtype, dev, optional=True)
+    M = _rows(dy)
+    dx = torch.empty_like(dy)
+    dresidual = None if h.dtype == dy.dtype else torch.empty_like(h)
+    dweight = torch.empty((D,), dtype=torch.float32, device=dev)
+    if workspace is None:
+        need = int(lib.mamba_rms_norm_bwd_workspace_size(M, D))
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    st = lib.mamba_rms_norm_bwd(
+        _addr(dy), _addr(h), _addr(weight), _addr(dresidual_out), _addr(dx), _addr(dresidual),
+        _addr(dweight), _addr(workspace), 0 if workspace is None else workspace.numel(), M, D, eps,
+        _io_dtype(dy), _io_dtype(h), _raw_stream(dy))
+    _raise(st, "mamba_rms_norm_bwd")
+    return {"dx": dx, "dresidual": dx if dresidual is None else dresidual, "dweight": dweight}
+
+
+def quantize_int8(x, channel_major=False, out=None, scale=None):
+    """8-bit integers with a scale per row: scale = max|x| / 127 over the row,
+    q = round(x / scale).  x [..., K] f32/bf16 -> q [..., K] int8, scale [...]
+    f32 (tokens, or a weight's output channels).  channel_major: x is [B, K, L],
+    as the scans write their output, and q [B, L, K], scale [B, L]."""
+    torch = _torch()
+    lib = load_library()
+    dev = x.device
+    _check(x, "x", x.shape)
+    if channel_major:
+        B, K, L = x.shape
+        lead = (B, L)
+    else:
+        if x.dim() < 1:
+            raise ValueError("x has no axis to quantise")
+        lead, K = tuple(x.shape[:-1]), x.shape[-1]
+        B, L = 1, _rows(x)
+    if out is None:
+        out = torch.empty(lead + (K,), dtype=torch.int8, device=dev)
+    else:
+        _check(out, "out", lead + (K,), torch.int8, dev)
+    if scale is None:
+        scale = torch.empty(lead, dtype=torch.float32, device=dev)
+    else:
+        _check(scale, "scale", lead, torch.float32, dev)
+    st = lib.mamba_quantize_int8(_addr(x), _addr(out), _addr(scale), B, L, K, int(channel_major),
+                                 _io_dtype(x), _raw_stream(x))
+    _raise(st, "mamba_quantize_int8")
+    return out, scale
+
+
+INT8_SHARED_A = 1  # MAMBA_INT8_SHARED_A
+INT8_SHARED_B = 2  # MAMBA_INT8_SHARED_B
+
+
+def int8_matmul_workspace_size(batch, M, N, K) -> int:
+    return int(load_library().mamba_int8_matmul_workspace_size(batch, M, N, K))
+
+
+def int8_matmul(a, b, a_scale, b_scale, out_dtype=None, out=None, workspace=None):
+    """out[..., m, n] = a_scale[m] b_scale[n] sum_k a[m, k] b[n, k], summed
+    exactly.  a [M, K] or [B, M, K], b [N, K] or [B, N, K] int8 (a 2-D operand
+    is used by every batch of a 3-D one); scales f32 of the operands' leading
+    shapes.  Returns out [M, N] or [B, M, N] of out_dtype (bfloat16, the
+    default, or float32).  With tokens as `a` and a weight [N, K] as `b` it is
+    a projection; with the weight as `a`, its channel-major form."""
+    torch = _torch()
+    lib = load_library()
+    if a.dim() not in (2, 3) or b.dim() not in (2, 3):
+        raise ValueError(f"a and b are 2-D or 3-D, got {a.dim()}-D and {b.dim()}-D")
+    dev = a.device
+    M, K = a.shape[-2:]
+    N = b.shape[-2]
+    if a.dim() == 2 and b.dim() == 2:
+        batch, lead, flags = 1, (), 0
+    else:
+        batch = a.shape[0] if a.dim() == 3 else b.shape[0]
+        lead = (batch,)
+        flags = ((INT8_SHARED_A if a.dim() == 2 else 0) | (INT8_SHARED_B if b.dim() == 2 else 0))
+    _check(a, "a", (lead if a.dim() == 3 else ()) + (M, K), torch.int8)
+    _check(b, "b", (lead if b.dim() == 3 else ()) + (N, K), torch.int8, dev)
+    _check(a_scale, "a_scale", a.shape[:-1], torch.float32, dev)
+    _check(b_scale, "b_scale", b.shape[:-1], torch.float32, dev)
+    if out is None:
+        out = torch.empty(lead + (M, N), dtype=torch.bfloat16 if out_dtype is None else out_dtype,
+                          device=dev)
+    else:
+        _check(out, "out", lead + (M, N), out_dtype, dev)
+    if workspace is None:
+        need = int(lib.mamba_int8_matmul_workspace_size(batch, M, N, K))
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    st = lib.mamba_int8_matmul(_addr(a), _addr(b), _addr(a_scale), _addr(b_scale), _addr(out),
+                               _addr(workspace), 0 if workspace is None else workspace.numel(),
+                               batch, M, N, K, _io_dtype(out), flags, _raw_stream(a))
+    _raise(st, "mamba_int8_matmul")
     return out
 
 

@@ -18,7 +18,8 @@ LIBRARY = os.path.join(HERE, "libmamba_amd.so")
 # VALU issue-rate probe (measurement aid for the roofline; not part of the C ABI)
 PROBE_SOURCE = "valu_probe.hip"
 PROBE_LIBRARY = os.path.join(HERE, "libmamba_probe.so")
-SOURCES = ["api.cpp", "scan_fwd.hip", "scan_bwd.hip", "ssd_fwd.hip", "conv1d_silu.hip", "state_update.hip"]
+SOURCES = ["api.cpp", "scan_fwd.hip", "scan_bwd.hip", "ssd_fwd.hip", "conv1d_silu.hip", "state_update.hip",
+           "quant_api.cpp", "rms_norm.hip", "rms_norm_bwd.hip", "quantize.hip", "int8_matmul.hip"]
 ARCH = "gfx950"
 
 # Packed-fp32 VALU forms are disabled on purpose: the kernels are written for
@@ -47,7 +48,7 @@ def _compile(src: str) -> str:
 def build(verbose: bool = False) -> str:
     """Compile every source for gfx950 and link the shared library."""
     os.makedirs(BUILD_DIR, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=8) as ex:
         objs = list(ex.map(_compile, SOURCES))
     tmp = LIBRARY + ".tmp%d" % os.getpid()
     cmd = [hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}", "-o", tmp] + objs

@@ -1,0 +1,213 @@
+// Root-mean-square norm with the residual's addition, its 8-bit output, and
+// the 8-bit quantisation of rows.
+//
+// Forward, per row of D elements (all in fp32):
+//   h = x + residual,  r = 1 / sqrt(mean(h^2) + eps),  y = h r w
+//   residual_out = h rounded to the residual's type
+//   out = y rounded to x's type, or   scale = max|y| / 127,  q = rne(y * 127 / max|y|).
+// y is formed from the unrounded h: the only roundings are the outputs'.
+//
+// Every element is read once and written once: a row stays in the registers of
+// the lanes that loaded it (8-element chunks, 16 or 32 bytes a lane), the row's
+// sum (and largest value) crosses lanes by DPP and waves through LDS.
+#include <hip/hip_runtime.h>
+
+#include "quant.h"
+#include "row_chunk.h"
+
+namespace mamba {
+namespace {
+
+enum Mode { kNorm, kNormInt8, kQuant };
+
+struct NormParams {
+    const void *x, *res;
+    const float *w;
+    void *out;
+    float *scale;
+    void *res_out;
+    int64_t M;
+    int D;
+    float eps, inv_d;
+};
+
+// RES: 0 no residual, 1 fp32, 2 bf16.  WAVE_ROW: each of a workgroup's four
+// waves has a row of its own; otherwise the workgroup (any number of waves)
+// has one row.  NC chunks a lane.
+template <bool XBF, int RES, int MODE, bool WAVE_ROW, int NC, bool TINY>
+__global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void rms_norm_kernel(const NormParams p)
+{
+    using XT = typename Elem<XBF>::T;
+    using RT = typename Elem<RES == 2>::T;
+    __shared__ float red[2][16];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n_waves = WAVE_ROW ? 1 : (int)(blockDim.x >> 6);
+    const int64_t row = WAVE_ROW ? (int64_t)blockIdx.x * 4 + wave : (int64_t)blockIdx.x;
+    if (WAVE_ROW && row >= p.M)
+        return;  // the whole wave; no barrier follows in this form
+    const int tid = WAVE_ROW ? lane : (int)threadIdx.x;
+    const int T = WAVE_ROW ? 64 : (int)blockDim.x;
+    const int D = p.D;
+    const bool ragged = D % kChunk != 0;
+
+    ChunkAt at[NC];
+    float h[NC][8];
+    const XT *xr = (const XT *)p.x + row * D;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+        at[j] = chunk_at<TINY>(tid + j * T, D);
+        load_chunk<XBF, TINY>(xr, at[j], D, h[j]);
+    }
+    if constexpr (RES != 0) {
+        const RT *rr = (const RT *)p.res + row * D;
+        float r[NC][8];
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+            load_chunk<RES == 2, TINY>(rr, at[j], D, r[j]);
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                h[j][i] += r[j][i];
+    }
+    if constexpr (MODE != kQuant) {
+        float w[NC][8];
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+            load_chunk<false, TINY>(p.w, at[j], D, w[j]);
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+            s += own_sum<TINY>(at[j], D, ragged, [&](int i) { return h[j][i] * h[j][i]; });
+        s = wave_sum(s);
+        if constexpr (!WAVE_ROW) {
+            if (lane == 0)
+                red[0][wave] = s;
+            __syncthreads();
+            s = red[0][0];
+            for (int k = 1; k < n_waves; ++k)
+                s += red[0][k];
+        }
+        // every element of the row has been read: the residual may be overwritten
+        if constexpr (RES != 0) {
+            if (p.res_out) {
+                RT *ro = (RT *)p.res_out + row * D;
+#pragma unroll
+                for (int j = 0; j < NC; ++j)
+                    store_chunk<RES == 2, TINY>(ro, at[j], D, h[j]);
+            }
+        }
+        const float r = 1.f / sqrtf(fmaf(s, p.inv_d, p.eps));
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                h[j][i] = h[j][i] * r * w[j][i];
+    }
+    if constexpr (MODE == kNorm) {
+        XT *yo = (XT *)p.out + row * D;
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+            store_chunk<XBF, TINY>(yo, at[j], D, h[j]);
+    } else {
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)  // lanes without a chunk hold the row's first: no mask
+                top = umax(top, abs_bits(h[j][i]));
+        top = wave_max(top);
+        if constexpr (!WAVE_ROW) {
+            if (lane == 0)
+                red[1][wave] = __uint_as_float(top);
+            __syncthreads();
+            for (int k = 0; k < n_waves; ++k)
+                top = umax(top, __float_as_uint(red[1][k]));
+        }
+        const RowScale rs = row_scale(top);
+        if (tid == 0)
+            p.scale[row] = rs.scale;
+        if (rs.raise != 1.f) {
+#pragma unroll
+            for (int j = 0; j < NC; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    h[j][i] *= rs.raise;
+        }
+        int8_t *qo = (int8_t *)p.out + row * D;
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+            const u32x2 q = pack_int8(h[j], rs.mul, rs.mask);
+            if (!at[j].live)
+                continue;
+            if constexpr (TINY) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < D)
+                        qo[i] = (int8_t)(q[i / 4] >> (8 * (i % 4)));
+            } else {
+                __builtin_memcpy(qo + at[j].off, &q, 8);
+            }
+        }
+    }
+}
+
+template <bool XBF, int RES, int MODE, bool WAVE_ROW, int NC, bool TINY>
+hipError_t start(const NormParams &p, int threads, hipStream_t s)
+{
+    const int64_t blocks = WAVE_ROW ? (p.M + 3) / 4 : p.M;
+    rms_norm_kernel<XBF, RES, MODE, WAVE_ROW, NC, TINY><<<dim3((unsigned)blocks), dim3(threads), 0, s>>>(p);
+    return hipGetLastError();
+}
+
+template <bool XBF, int RES, int MODE> hipError_t pick(const NormParams &p, hipStream_t s)
+{
+    if (p.D < kChunk)
+        return start<XBF, RES, MODE, true, 1, true>(p, 256, s);
+    const int chunks = (p.D + kChunk - 1) / kChunk;
+    // A wave holds up to 8 chunks a lane (4096 elements).
+    const int per_lane = (chunks + 63) / 64;
+    if (per_lane <= 1 || (per_lane <= 8 && p.M >= 1024)) {
+        switch (per_lane) {
+        case 1: return start<XBF, RES, MODE, true, 1, false>(p, 256, s);
+        case 2: return start<XBF, RES, MODE, true, 2, false>(p, 256, s);
+        case 3: return start<XBF, RES, MODE, true, 3, false>(p, 256, s);
+        case 4: return start<XBF, RES, MODE, true, 4, false>(p, 256, s);
+        case 5: return start<XBF, RES, MODE, true, 5, false>(p, 256, s);
+        default: return start<XBF, RES, MODE, true, 8, false>(p, 256, s);
+        }
+    }
+    const int nc = chunks <= 512 ? 1 : chunks <= 2048 ? 2 : 4;
+    const int lanes = (chunks + nc - 1) / nc;
+    const int threads = (lanes + 63) / 64 * 64;
+    if (nc == 1)
+        return start<XBF, RES, MODE, false, 1, false>(p, threads, s);
+    if (nc == 2)
+        return start<XBF, RES, MODE, false, 2, false>(p, threads, s);
+    return start<XBF, RES, MODE, false, 4, false>(p, threads, s);
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm(const NormArgs &a, hipStream_t s)
+{
+    NormParams p{a.x, a.residual, a.weight, a.out, a.scale, a.residual_out, a.M, a.D, a.eps, 1.f / (float)a.D};
+    if (!a.weight)
+        return a.bf16 ? pick<true, 0, kQuant>(p, s) : pick<false, 0, kQuant>(p, s);
+    const int res = !a.residual ? 0 : a.residual_bf16 ? 2 : 1;
+    if (a.scale) {
+        if (!a.bf16)
+            return res ? pick<false, 1, kNormInt8>(p, s) : pick<false, 0, kNormInt8>(p, s);
+        return res == 2 ? pick<true, 2, kNormInt8>(p, s)
+               : res    ? pick<true, 1, kNormInt8>(p, s)
+                        : pick<true, 0, kNormInt8>(p, s);
+    }
+    if (!a.bf16)
+        return res ? pick<false, 1, kNorm>(p, s) : pick<false, 0, kNorm>(p, s);
+    return res == 2 ? pick<true, 2, kNorm>(p, s)
+           : res    ? pick<true, 1, kNorm>(p, s)
+                    : pick<true, 0, kNorm>(p, s);
+}
+
+}  // namespace mamba

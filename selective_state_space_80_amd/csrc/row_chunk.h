@@ -1,0 +1,216 @@
+// Device helpers of the row operators (norms, quantiser): a row of D elements
+// in the registers of its lanes, 8-element chunks, sums and largest values
+// over a wave, and the 8-bit rounding.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "device_common.h"
+
+namespace mamba {
+namespace {
+
+constexpr int kChunk = 8;
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// 8 elements at any element's alignment (rows of odd width start at any
+// element; gfx950 loads and stores 16 bytes at any address).
+template <bool BF16> __device__ __forceinline__ void load8(const typename Elem<BF16>::T *p, float (&v)[8])
+{
+    if constexpr (BF16) {
+        u32x4 r;
+        __builtin_memcpy(&r, p, 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(r[i] << 16);
+            v[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
+        }
+    } else {
+        u32x4 r0, r1;
+        __builtin_memcpy(&r0, p, 16);
+        __builtin_memcpy(&r1, p + 4, 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = __uint_as_float(r0[i]);
+            v[4 + i] = __uint_as_float(r1[i]);
+        }
+    }
+}
+
+template <bool BF16> __device__ __forceinline__ void store8(typename Elem<BF16>::T *p, const float (&v)[8])
+{
+    if constexpr (BF16) {
+        u32x4 r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            r[i] = cvt2(v[2 * i], v[2 * i + 1]);
+        __builtin_memcpy(p, &r, 16);
+    } else {
+        u32x4 r0, r1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            r0[i] = __float_as_uint(v[i]);
+            r1[i] = __float_as_uint(v[4 + i]);
+        }
+        __builtin_memcpy(p, &r0, 16);
+        __builtin_memcpy(p + 4, &r1, 16);
+    }
+}
+
+template <int CTRL> __device__ __forceinline__ uint32_t dpp(uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+template <int CTRL> __device__ __forceinline__ float dppf(float v)
+{
+    return __uint_as_float(dpp<CTRL>(__float_as_uint(v)));
+}
+
+// Sum / unsigned maximum over the wave, in every lane: quads, half rows, rows
+// of 16 by DPP, then the four rows through scalar registers.  A fixed order.
+__device__ __forceinline__ float wave_sum(float v)
+{
+    v = quad_sum(v);
+    v += dppf<0x141>(v);  // row_half_mirror
+    v += dppf<0x140>(v);  // row_mirror
+    const int b = __float_as_int(v);
+    return (__int_as_float(__builtin_amdgcn_readlane(b, 0)) +
+            __int_as_float(__builtin_amdgcn_readlane(b, 16))) +
+           (__int_as_float(__builtin_amdgcn_readlane(b, 32)) +
+            __int_as_float(__builtin_amdgcn_readlane(b, 48)));
+}
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+{
+    v = umax(v, dpp<0xB1>(v));
+    v = umax(v, dpp<0x4E>(v));
+    v = umax(v, dpp<0x141>(v));
+    v = umax(v, dpp<0x140>(v));
+    const int b = (int)v;
+    return umax(umax((uint32_t)__builtin_amdgcn_readlane(b, 0), (uint32_t)__builtin_amdgcn_readlane(b, 16)),
+                umax((uint32_t)__builtin_amdgcn_readlane(b, 32), (uint32_t)__builtin_amdgcn_readlane(b, 48)));
+}
+
+// The bits of |v| order as |v| does, infinity above every finite value and NaN
+// above infinity, so one unsigned maximum also tells a row that is not finite.
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// Scale and multiplier of a row whose largest |value| has the bits `top`.
+// A zero row has scale 0; a row that is not finite has scale NaN and q = 0, so
+// that everything computed from it is NaN.  Below 2^-120 the multiplier
+// 127 / top would pass the fp32 range: such rows are raised by 2^64 first.
+struct RowScale {
+    float scale, mul, raise;
+    uint32_t mask;
+};
+__device__ __forceinline__ RowScale row_scale(uint32_t top)
+{
+    RowScale r;
+    const float t = __uint_as_float(top);
+    r.raise = t < 0x1p-120f ? 0x1p64f : 1.f;
+    r.scale = t / 127.f;
+    r.mul = top == 0 ? 0.f : 127.f / (t * r.raise);
+    r.mask = 0xffffffffu;
+    if (top >= 0x7f800000u) {
+        r.scale = __uint_as_float(0x7fc00000u);
+        r.mul = 0.f;
+        r.mask = 0u;
+    }
+    return r;
+}
+
+// Eight integers in [-127, 127] as bytes.  v * mul + 1.5 * 2^23 is rounded to
+// an integer by the addition itself (to nearest, ties to even), whose low byte
+// is then that integer in two's complement.
+__device__ __forceinline__ u32x2 pack_int8(const float (&v)[8], float mul, uint32_t mask)
+{
+    uint32_t b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        b[i] = __float_as_uint(fmaf(v[i], mul, 12582912.f));
+    u32x2 q;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t lo = __builtin_amdgcn_perm(b[4 * i + 1], b[4 * i], 0x0c0c0400u);
+        const uint32_t hi = __builtin_amdgcn_perm(b[4 * i + 3], b[4 * i + 2], 0x0c0c0400u);
+        q[i] = __builtin_amdgcn_perm(hi, lo, 0x05040100u) & mask;
+    }
+    return q;
+}
+
+// Where a lane's chunk of 8 elements lies in a row of D, and which of them are
+// its own.  A row that is no multiple of 8 ends in a chunk that is moved back
+// to end with the row: it overlaps the one before, computes the same values
+// there, and owns only the elements from `lo` on.  Rows shorter than a chunk
+// (TINY) are read element by element with the index held below D.
+struct ChunkAt {
+    int off, lo;
+    bool live;
+};
+template <bool TINY> __device__ __forceinline__ ChunkAt chunk_at(int c, int D)
+{
+    const int full = D / kChunk, tail = D % kChunk;
+    ChunkAt r;
+    if (TINY) {
+        r.off = 0;
+        r.lo = 0;
+        r.live = c == 0;
+    } else {
+        const bool last = tail != 0 && c == full;
+        r.off = c < full ? c * kChunk : (last ? D - kChunk : 0);
+        r.lo = last ? kChunk - tail : 0;
+        r.live = c < full || last;
+    }
+    return r;
+}
+
+template <bool BF16, bool TINY>
+__device__ __forceinline__ void load_chunk(const typename Elem<BF16>::T *row, const ChunkAt &at, int D,
+                                           float (&v)[8])
+{
+    if constexpr (TINY) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = Elem<BF16>::load(row + (i < D ? i : D - 1));
+    } else {
+        load8<BF16>(row + at.off, v);
+    }
+}
+template <bool BF16, bool TINY>
+__device__ __forceinline__ void store_chunk(typename Elem<BF16>::T *row, const ChunkAt &at, int D,
+                                            const float (&v)[8])
+{
+    if (!at.live)
+        return;
+    if constexpr (TINY) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < D)
+                Elem<BF16>::store(row + i, v[i]);
+    } else {
+        store8<BF16>(row + at.off, v);
+    }
+}
+
+// Sum of f(i) over the chunk's own elements.
+template <bool TINY, typename F>
+__device__ __forceinline__ float own_sum(const ChunkAt &at, int D, bool ragged, F f)
+{
+    float s = 0.f;
+    if (TINY || ragged) {
+        const int end = TINY ? D : kChunk;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            s += (i >= at.lo && i < end) ? f(i) : 0.f;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            s += f(i);
+    }
+    return at.live ? s : 0.f;
+}
+
+}  // namespace
+}  // namespace mamba
