@@ -134,7 +134,7 @@ def load_library(path: str = LIBRARY):
     lib.mamba_quantize_int8.restype = I32
     lib.mamba_quantize_int8.argtypes = [P] * 3 + [I64, I64, I64, I32, I32, P]
     lib.mamba_int8_matmul_workspace_size.restype = SZ
-    lib.mamba_int8_matmul_workspace_size.argtypes = [I64] * 4
+    lib.mamba_int8_matmul_workspace_size.argtypes = [I64] * 4 + [U32]
     lib.mamba_int8_matmul.restype = I32
     lib.mamba_int8_matmul.argtypes = [P] * 6 + [SZ, I64, I64, I64, I64, I32, U32, P]
     _lib = lib
@@ -712,10 +712,11 @@ def quantize_int8(x, channel_major=False, out=None, scale=None):
 
 INT8_SHARED_A = 1  # MAMBA_INT8_SHARED_A
 INT8_SHARED_B = 2  # MAMBA_INT8_SHARED_B
+INT8_UNALIGNED = 4  # MAMBA_INT8_UNALIGNED
 
 
-def int8_matmul_workspace_size(batch, M, N, K) -> int:
-    return int(load_library().mamba_int8_matmul_workspace_size(batch, M, N, K))
+def int8_matmul_workspace_size(batch, M, N, K, flags=0) -> int:
+    return int(load_library().mamba_int8_matmul_workspace_size(batch, M, N, K, flags))
 
 
 def int8_matmul(a, b, a_scale, b_scale, out_dtype=None, out=None, workspace=None):
@@ -747,8 +748,8 @@ def int8_matmul(a, b, a_scale, b_scale, out_dtype=None, out=None, workspace=None
                           device=dev)
     else:
         _check(out, "out", lead + (M, N), out_dtype, dev)
-    if workspace is None:
-        need = int(lib.mamba_int8_matmul_workspace_size(batch, M, N, K))
+    if workspace is None and (K % 16 or (a.data_ptr() | b.data_ptr()) % 16):
+        need = int(lib.mamba_int8_matmul_workspace_size(batch, M, N, K, flags | INT8_UNALIGNED))
         workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     st = lib.mamba_int8_matmul(_addr(a), _addr(b), _addr(a_scale), _addr(b_scale), _addr(out),
                                _addr(workspace), 0 if workspace is None else workspace.numel(),

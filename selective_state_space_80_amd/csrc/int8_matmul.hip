@@ -2,6 +2,19 @@
 //   out[m, n] = a_scale[m] b_scale[n] sum_k a[m, k] b[n, k]
 // The sum is exact (32-bit integers); it is converted to fp32, scaled, and
 // rounded once to the output type.
+//
+// Two kernels, both fed by loads that go from memory straight into LDS
+// (global_load_lds_dwordx4: no registers, so as many are in flight as LDS
+// holds), both with the operand rows in tiles of 128 bytes (one cache line) of
+// the inner axis:
+//   tile_kernel  a workgroup's waves share a tile of both operands (256 x 256
+//                or 128 x 128 outputs) and step through the inner axis together
+//   ring_kernel  few output tiles, or few rows on one side: the waves of a
+//                workgroup split the inner axis, each streaming its share
+//                through its own LDS ring, and add their integer sums
+// An inner size that is no multiple of 16, or operands off 16-byte alignment,
+// which the wide LDS loads do not take, are first laid out in the workspace
+// with their rows padded by zeros (pad_rows_kernel).
 #include <hip/hip_runtime.h>
 
 #include "device_common.h"
@@ -13,122 +26,596 @@ namespace {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kTile = 128;   // rows of each operand in a workgroup's tile
-constexpr int kStep = 128;   // bytes of the inner axis a step takes
+constexpr int kStep = 128;     // bytes of the inner axis a step takes: a cache line of every row
+constexpr int kCus = 256;
+constexpr int kXcds = 8;
 
 struct MatmulParams {
     const int8_t *a, *b;
     const float *a_scale, *b_scale;
     void *out;
-    int64_t M, N, K;
+    int64_t M, N;
+    int K, steps;              // steps of kStep bytes, at least 1 (K = 0: all zeros)
     int64_t a_batch, b_batch;  // rows between batches: 0 = shared
-    int64_t tiles_m, tiles_n;
+    int tiles_m, tiles_n;
+    int64_t tiles;             // of all batches
+    bool stream_out;           // output stores pass the caches by
 };
 
-// 16 bytes of a row at any address, zero past the end of the row.
-__device__ __forceinline__ i32x4 load16(const int8_t *row, int64_t k, int64_t K)
+// Past the inner axis' end a lane loads these instead.
+__device__ const u32x4 kZeros = {0, 0, 0, 0};
+
+// 16 bytes a lane from memory to LDS: lane l's go to lds + 16 l.  The first
+// form takes a scalar base and a 32-bit offset a lane, the second a pointer a
+// lane.  Completion is counted by vmcnt; the kernels wait for it themselves.
+__device__ __forceinline__ void load_lds(uint32_t lds, const int8_t *base, uint32_t offset)
 {
-    i32x4 v = {0, 0, 0, 0};
-    if (k + 16 <= K) {
-        __builtin_memcpy(&v, row + k, 16);
-    } else if (k < K) {
-        uint32_t w[4] = {0, 0, 0, 0};
-        for (int i = 0; i < (int)(K - k); ++i)
-            w[i / 4] |= (uint32_t)(uint8_t)row[k + i] << (8 * (i % 4));
-        v = i32x4{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
-    }
-    return v;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base)
+                 : "memory");
+}
+__device__ __forceinline__ void load_lds(uint32_t lds, const int8_t *ptr)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(ptr) : "memory");
 }
 
-// Place of a 16-byte chunk in a tile of 128-byte rows: the chunks of a row are
-// permuted by its number, so that 16 rows read at one chunk index touch all
-// 64 banks once.
-__device__ __forceinline__ int slot(int row, int chunk) { return row * 8 + (chunk ^ ((row >> 1) & 7)); }
-
-template <bool BF16> __global__ __launch_bounds__(256) void int8_matmul_kernel(const MatmulParams p)
+__device__ __forceinline__ uint32_t lds_address(const char *p)
 {
-    __shared__ i32x4 sa[kTile * 8], sb[kTile * 8];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wm = (wave & 1) * 64, wn = (wave >> 1) * 64;
-    int64_t t = blockIdx.x;
-    const int64_t tm = t % p.tiles_m;
-    t /= p.tiles_m;
-    const int64_t tn = t % p.tiles_n, batch = t / p.tiles_n;
-    const int64_t m0 = tm * kTile, n0 = tn * kTile;
-    const int8_t *a = p.a + batch * p.a_batch * p.K;
-    const int8_t *b = p.b + batch * p.b_batch * p.K;
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char *)p;
+}
 
-    i32x16 acc[2][2] = {};
-    for (int64_t k0 = 0; k0 < p.K; k0 += kStep) {
-        i32x4 ra[4], rb[4];
+// A tile's rows are 128 bytes, eight chunks of 16, permuted by the row's
+// number: chunk c of row r lies at place c ^ (r / 2 % 8).  16 rows read at one
+// chunk index then touch every one of the 64 banks once.
+__device__ __forceinline__ int place(int row, int chunk) { return chunk ^ ((row >> 1) & 7); }
+
+// A wave's loads of 8 * N rows of a tile.  A load takes 8 rows, 8 lanes each;
+// rows past the operand's end repeat its last (their products are not stored).
+template <int N> struct RowLoads {
+    uint32_t off[N];
+    __device__ __forceinline__ void set(int first_row, int step_rows, int rows, int K)
+    {
+        const int lane = threadIdx.x & 63;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = threadIdx.x + i * 256, row = c >> 3;
-            const int64_t k = k0 + (c & 7) * 16;
-            const int64_t m = m0 + row < p.M ? m0 + row : p.M - 1;
-            const int64_t n = n0 + row < p.N ? n0 + row : p.N - 1;
-            ra[i] = load16(a + m * p.K, k, p.K);
-            rb[i] = load16(b + n * p.K, k, p.K);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = threadIdx.x + i * 256;
-            sa[slot(c >> 3, c & 7)] = ra[i];
-            sb[slot(c >> 3, c & 7)] = rb[i];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            i32x4 fa[2], fb[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                fa[i] = sa[slot(wm + i * 32 + (lane & 31), kk * 2 + (lane >> 5))];
-                fb[i] = sb[slot(wn + i * 32 + (lane & 31), kk * 2 + (lane >> 5))];
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
+        for (int i = 0; i < N; ++i) {
+            const int row = first_row + i * step_rows + (lane >> 3);
+            off[i] = (uint32_t)((row < rows ? row : rows - 1) * K + place(row, lane & 7) * 16);
         }
     }
-    // a lane holds one m and four runs of four consecutive n per 32 x 32 block
+    __device__ __forceinline__ void whole(uint32_t lds, int step_bytes, const int8_t *base) const
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            load_lds(lds + i * step_bytes, base, off[i]);
+    }
+    // the last step of an inner axis that is no multiple of kStep: `left` bytes
+    __device__ __forceinline__ void partial(uint32_t lds, int step_bytes, const int8_t *base, int first_row,
+                                            int step_rows, int left) const
+    {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int row = first_row + i * step_rows + (lane >> 3);
+            const int8_t *p = place(row, lane & 7) * 16 < left ? base + off[i] : (const int8_t *)&kZeros;
+            load_lds(lds + i * step_bytes, p);
+        }
+    }
+};
+
+// Workgroups go to the 8 XCDs in turn.  Each XCD gets a contiguous share of
+// the tiles, so that neighbours, which read the same operand rows, share an L2.
+struct Share {
+    int64_t first, count;
+};
+__device__ __forceinline__ Share xcd_share(int64_t tiles, int xcd)
+{
+    const int64_t q = tiles / kXcds, r = tiles % kXcds;
+    return {xcd * q + (xcd < r ? xcd : r), q + (xcd < r ? 1 : 0)};
+}
+
+// ---- large products ------------------------------------------------------------
+//
+// WM x WN waves of FM x FN blocks of 32 x 32 outputs; STAGES tiles of both
+// operands in LDS, the products working on one while the others load.  The
+// workgroup stays for several output tiles, and its loads run ahead of the
+// products across the end of a tile: the next tile's first stages load while
+// this one's sums are scaled and stored.
+//
+// A step is 4 rounds of 32 bytes; a round's fragments are read from LDS during
+// the round before.  The one barrier of a step stands before its last round:
+// there every wave has read this stage (it may be overwritten) and the next
+// stage has arrived.
+//
+// 256 x 256 outputs by 8 waves reads 26 bytes a clock and CU from L2 and fills
+// the matrix units to 62 % at 1.9 GHz, which is where this card's power limit
+// holds random data (the same kernel without any loads: 2.7 POP/s; with zeros
+// as data: 3.2; as it is: 2.45 at 8192^3, the library's 8-bit product 2.14).
+template <int WM, int WN, int FM, int FN, int STAGES, bool BF16>
+__global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const MatmulParams p)
+{
+    constexpr int TM = WM * FM * 32, TN = WN * FN * 32, NW = WM * WN;
+    constexpr int kStage = (TM + TN) * kStep;
+    constexpr int LA = TM / 8 / NW, LB = TN / 8 / NW;  // loads of a wave and stage
+    constexpr int kStaging = 4096;                     // of a wave's outputs: 32 rows of 128 bytes
+    __shared__ __attribute__((aligned(16))) char smem[STAGES * kStage + NW * kStaging];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave % WM, wn = wave / WM;
+
+    const int xcd = blockIdx.x % kXcds, slot = blockIdx.x / kXcds;
+    const int stride = ((int)gridDim.x - xcd + kXcds - 1) / kXcds;  // workgroups of this XCD
+    const Share share = xcd_share(p.tiles, xcd);
+    if (slot >= share.count)
+        return;
+    // Bands of two tile rows, walked along n: 32 neighbouring tiles (an XCD's)
+    // then read 2 + 16 operand tiles.  Bands of 1..8 rows at four shapes: 2 is
+    // never more than 1 % behind the best; 1 loses 15 % at 8192^3.
+    constexpr int kBand = 2;
+    struct Tile {
+        int64_t batch, m0, n0;
+    };
+    auto tile_at = [&](int64_t i) {
+        const int64_t id = share.first + i, per = (int64_t)p.tiles_m * p.tiles_n;
+        Tile t;
+        t.batch = id / per;
+        const int rest = (int)(id % per), band = rest / (kBand * p.tiles_n), in = rest % (kBand * p.tiles_n);
+        const int left = p.tiles_m - band * kBand, rows = left < kBand ? left : kBand;
+        t.m0 = (int64_t)(band * kBand + in % rows) * TM;
+        t.n0 = (int64_t)(in / rows) * TN;
+        return t;
+    };
+
+    // the loads' cursor: STAGES steps ahead of the products
+    RowLoads<LA> loads_a;
+    RowLoads<LB> loads_b;
+    const int8_t *next_a = nullptr, *next_b = nullptr;
+    int64_t load_tile = slot;
+    int load_step = 0, ahead = 0;  // ahead: stages issued and not yet waited for
+    auto start_tile = [&]() {
+        const Tile t = tile_at(load_tile);
+        next_a = p.a + (t.batch * p.a_batch + t.m0) * p.K;
+        next_b = p.b + (t.batch * p.b_batch + t.n0) * p.K;
+        loads_a.set(wave * 8, NW * 8, (int)(p.M - t.m0 < TM ? p.M - t.m0 : TM), p.K);
+        loads_b.set(wave * 8, NW * 8, (int)(p.N - t.n0 < TN ? p.N - t.n0 : TN), p.K);
+    };
+    const uint32_t lds = lds_address(smem) + wave * 1024;
+    auto issue = [&](int stage) {
+        if (load_tile >= share.count)
+            return;
+        ++ahead;
+        const uint32_t to = lds + stage * kStage;
+        const int left = p.K - load_step * kStep;
+        if (left >= kStep) {
+            loads_a.whole(to, NW * 1024, next_a);
+            loads_b.whole(to + TM * kStep, NW * 1024, next_b);
+        } else {
+            loads_a.partial(to, NW * 1024, next_a, wave * 8, NW * 8, left);
+            loads_b.partial(to + TM * kStep, NW * 1024, next_b, wave * 8, NW * 8, left);
+        }
+        next_a += kStep;
+        next_b += kStep;
+        if (++load_step == p.steps) {
+            load_step = 0;
+            load_tile += stride;
+            if (load_tile < share.count)
+                start_tile();
+        }
+    };
+
+    // fragments: a lane holds 16 bytes of row lane % 32, half lane / 32
+    const int fr = lane & 31, half = lane >> 5;
+    auto fragments = [&](i32x4(&fa)[FM], i32x4(&fb)[FN], int stage, int round) {
+        const char *s = smem + stage * kStage + fr * kStep + place(fr, round * 2 + half) * 16;
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+            fa[i] = *(const i32x4 *)(s + (wm * FM + i) * 32 * kStep);
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            fb[j] = *(const i32x4 *)(s + (TM + (wn * FN + j) * 32) * kStep);
+    };
+
+    start_tile();
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i)
+        issue(i);
+    if (ahead == STAGES)
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((STAGES - 1) * (LA + LB)) : "memory");
+    else
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    --ahead;
+    asm volatile("s_barrier" ::: "memory");
+    i32x4 fa[2][FM], fb[2][FN];
+    fragments(fa[0], fb[0], 0, 0);
+    int stage = 0;
+    for (int64_t ti = slot; ti < share.count; ti += stride) {
+        i32x16 acc[FM][FN];
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                acc[i][j] = i32x16{0};
+        for (int s = 0; s < p.steps; ++s) {
+            const int next = stage + 1 == STAGES ? 0 : stage + 1;
+#pragma unroll
+            for (int round = 0; round < 4; ++round) {
+                if (round < 3) {
+                    fragments(fa[(round + 1) & 1], fb[(round + 1) & 1], stage, round + 1);
+                } else {
+                    // The oldest stage in flight has to have arrived.  With all
+                    // others issued behind it, all but theirs may be pending;
+                    // stores of the tile before may be among the pending ones
+                    // in a tile's first step, which waits for everything.
+                    if (STAGES > 2 && ahead == STAGES - 1 && (s > 0 || ti == slot))
+                        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((STAGES - 2) * (LA + LB)) : "memory");
+                    else
+                        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                    if (ahead > 0)
+                        --ahead;
+                    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                    fragments(fa[0], fb[0], next, 0);  // after the last step: read, not used
+                    issue(stage);
+                }
+                // b's rows on the first side: a lane then holds four
+                // consecutive n of one m
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+#pragma unroll
+                    for (int j = 0; j < FN; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[round & 1][j], fa[round & 1][i],
+                                                                          acc[i][j], 0, 0, 0);
+                // the reads spread evenly between the products
+#pragma unroll
+                for (int q = 0; q < FM + FN; ++q) {
+                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x8, FM * FN / (FM + FN), 0);
+                }
+            }
+            stage = next;
+        }
+        // Scale and store, 32 rows of 128 bytes at a time through the wave's
+        // own piece of LDS, so that a store instruction writes 8 whole lines
+        // (straight from the registers it would touch 32 rows, 16 bytes each:
+        // 40 us more at 8 x 5120 x 2048 x 2560).
+        const Tile t = tile_at(ti);
+        using T = typename Elem<BF16>::T;
+        char *st = smem + STAGES * kStage + wave * kStaging;
+        const float *a_scale = p.a_scale + t.batch * p.a_batch, *b_scale = p.b_scale + t.batch * p.b_batch;
+        constexpr int kWide = BF16 ? 2 : 1;        // blocks of 32 columns in 128 bytes
+        constexpr int kPerChunk = BF16 ? 8 : 4;    // elements in 16 bytes
+        static_assert(FN % kWide == 0, "a wave's columns fill whole lines");
+#pragma unroll
+        for (int j0 = 0; j0 < FN; j0 += kWide) {
+            float sb[kWide][4][4];
+#pragma unroll
+            for (int j = 0; j < kWide; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int64_t n = t.n0 + (wn * FN + j0 + j) * 32 + e * 8 + half * 4;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        sb[j][e][q] = b_scale[n + q < p.N ? n + q : p.N - 1];
+                }
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                const int64_t m = t.m0 + (wm * FM + i) * 32;
+                const float sa = a_scale[m + fr < p.M ? m + fr : p.M - 1];
+#pragma unroll
+                for (int j = 0; j < kWide; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float v[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            v[q] = (float)acc[i][j0 + j][e * 4 + q] * sa * sb[j][e][q];
+                        if constexpr (BF16) {
+                            const u32x2 w = {cvt2(v[0], v[1]), cvt2(v[2], v[3])};
+                            *(u32x2 *)(st + fr * 128 + place(fr, j * 4 + e) * 16 + half * 8) = w;
+                        } else {
+                            const u32x4 w = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                             __float_as_uint(v[3])};
+                            *(u32x4 *)(st + fr * 128 + place(fr, e * 2 + half) * 16) = w;
+                        }
+                    }
+                const int64_t n = t.n0 + (wn * FN + j0) * 32 + (lane & 7) * kPerChunk;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = r * 8 + (lane >> 3);
+                    const u32x4 v = *(const u32x4 *)(st + row * 128 + place(row, lane & 7) * 16);
+                    if (m + row >= p.M)
+                        continue;
+                    T *o = (T *)p.out + (t.batch * p.M + m + row) * p.N + n;
+                    if (n + kPerChunk <= p.N) {
+                        typedef u32x4 __attribute__((aligned(2))) loose;  // rows start at any element
+                        if (p.stream_out)
+                            __builtin_nontemporal_store(v, (loose *)o);
+                        else
+                            *(loose *)o = v;
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < kPerChunk; ++q)
+                            if (n + q < p.N) {
+                                if constexpr (BF16)
+                                    o[q] = (uint16_t)(v[q / 2] >> (16 * (q & 1)));
+                                else
+                                    o[q] = __uint_as_float(v[q]);
+                            }
+                    }
+                }
+            }
+        }
+    }
+}
+
+// ---- few tiles -------------------------------------------------------------------
+//
+// A workgroup has one tile of FM x FN blocks of 16 x 16 outputs; its NW waves
+// split the inner axis.  No wave waits for another before the sums are added
+// (integers: in any order), so the loads of 8 waves, 128 KB a workgroup, run
+// without a common pause.  What bounds it is the rate at which one CU takes
+// lines into LDS (a single workgroup on an idle card: 97 bytes a ns, all of
+// them together about 60) and, for one token, the launch.
+template <int FM, int FN, int STAGES, bool BF16> __global__ __launch_bounds__(512) void ring_kernel(const MatmulParams p)
+{
+    constexpr int NW = 8, TM = FM * 16, TN = FN * 16, kStage = (TM + TN) * kStep, kLoads = 2 * (FM + FN);
+    constexpr int kPitch = TN + 4;
+    __shared__ __attribute__((aligned(16))) char smem[NW * STAGES * kStage];
+    __shared__ int sum[TM * kPitch];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Share share = xcd_share(p.tiles, blockIdx.x % kXcds);
+    const int64_t id = share.first + blockIdx.x / kXcds, per = (int64_t)p.tiles_m * p.tiles_n;
+    const int64_t batch = id / per;
+    const int rest = (int)(id % per);
+    const int64_t m0 = (int64_t)(rest % p.tiles_m) * TM, n0 = (int64_t)(rest / p.tiles_m) * TN;
+    const int8_t *a = p.a + (batch * p.a_batch + m0) * p.K, *b = p.b + (batch * p.b_batch + n0) * p.K;
+    const int rows_a = (int)(p.M - m0 < TM ? p.M - m0 : TM), rows_b = (int)(p.N - n0 < TN ? p.N - n0 : TN);
+    RowLoads<2 * FM> loads_a;
+    RowLoads<2 * FN> loads_b;
+    loads_a.set(0, 8, rows_a, p.K);
+    loads_b.set(0, 8, rows_b, p.K);
+
+    const int each = (p.steps + NW - 1) / NW, from = wave * each;
+    const int to = from + each < p.steps ? from + each : p.steps;
+    const char *mine = smem + wave * STAGES * kStage;
+    const uint32_t lds = lds_address(mine);
+    auto issue = [&](int step, int stage) {
+        const uint32_t l = lds + stage * kStage;
+        const int8_t *sa = a + (int64_t)step * kStep, *sb = b + (int64_t)step * kStep;
+        const int left = p.K - step * kStep;
+        if (left >= kStep) {
+            loads_a.whole(l, 1024, sa);
+            loads_b.whole(l + TM * kStep, 1024, sb);
+        } else {
+            loads_a.partial(l, 1024, sa, 0, 8, left);
+            loads_b.partial(l + TM * kStep, 1024, sb, 0, 8, left);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i)
+        if (from + i < to)
+            issue(from + i, i);
+    for (int i = threadIdx.x; i < TM * kPitch; i += 64 * NW)
+        sum[i] = 0;
+    // fragments: a lane holds 16 bytes of row lane % 16, quarter lane / 16
+    const int fr = lane & 15, quarter = lane >> 4;
+    i32x4 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            acc[i][j] = i32x4{0, 0, 0, 0};
+    int stage = 0;
+    for (int s = from; s < to; ++s) {
+        // this stage has arrived when only the younger ones' loads are pending
+        if (s + STAGES <= to)
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads * (STAGES - 1)) : "memory");
+        else
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        i32x4 fa[2][FM], fb[2][FN];
+#pragma unroll
+        for (int round = 0; round < 2; ++round) {
+            const char *f = mine + stage * kStage + fr * kStep + place(fr, round * 4 + quarter) * 16;
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+                fa[round][i] = *(const i32x4 *)(f + i * 16 * kStep);
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                fb[round][j] = *(const i32x4 *)(f + (TM + j * 16) * kStep);
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read: the stage may be overwritten
+        if (s + STAGES < to)
+            issue(s + STAGES, stage);
+#pragma unroll
+        for (int round = 0; round < 2; ++round)
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[round][j], fa[round][i], acc[i][j], 0, 0, 0);
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                atomicAdd(sum + (i * 16 + fr) * kPitch + j * 16 + quarter * 4 + e, acc[i][j][e]);
+    __syncthreads();
     using T = typename Elem<BF16>::T;
-    const float *asc = p.a_scale + batch * p.a_batch, *bsc = p.b_scale + batch * p.b_batch;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int64_t m = m0 + wm + i * 32 + (lane & 31);
-        if (m >= p.M)
-            continue;
-        const float s = asc[m];
-        T *row = (T *)p.out + (batch * p.M + m) * p.N;
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int64_t n = n0 + wn + j * 32 + (e >> 2) * 8 + (lane >> 5) * 4 + (e & 3);
-                if (n < p.N)
-                    Elem<BF16>::store(row + n, (float)acc[i][j][e] * s * bsc[n]);
-            }
+    const float *a_scale = p.a_scale + batch * p.a_batch + m0, *b_scale = p.b_scale + batch * p.b_batch + n0;
+    T *out = (T *)p.out + (batch * p.M + m0) * p.N + n0;
+    for (int i = threadIdx.x; i < TM * TN; i += 64 * NW) {
+        const int m = i / TN, n = i % TN;
+        if (m < rows_a && n < rows_b)
+            Elem<BF16>::store(out + (int64_t)m * p.N + n, (float)sum[m * kPitch + n] * a_scale[m] * b_scale[n]);
     }
 }
+
+// ---- rows of any size and alignment -------------------------------------------------
+
+// [rows, K] at any byte to [rows, pitch], pitch = K rounded up to 16: one
+// 16-byte chunk of the result a thread.
+__global__ __launch_bounds__(256) void pad_rows_kernel(const int8_t *src, int8_t *dst, int64_t chunks, int K,
+                                                       int per_row)
+{
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < chunks; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / per_row;
+        const int k = (int)(i % per_row) * 16;
+        const int8_t *from = src + row * K + k;
+        u32x4 v = {0, 0, 0, 0};
+        if (k + 16 <= K) {
+            __builtin_memcpy(&v, from, 16);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (k + j < K)
+                    v[j / 4] |= (uint32_t)(uint8_t)from[j] << (8 * (j % 4));
+        }
+        *(u32x4 *)(dst + i * 16) = v;
+    }
+}
+
+int64_t padded(int64_t K) { return (K + 15) / 16 * 16; }
+size_t padded_bytes(int64_t rows, int64_t K) { return ((size_t)(rows * padded(K)) + 255) / 256 * 256; }
+
+hipError_t pad_rows(const int8_t *src, int8_t *dst, int64_t rows, int64_t K, hipStream_t s)
+{
+    const int64_t chunks = rows * (padded(K) / 16);
+    const int64_t blocks = (chunks + 255) / 256 < (1 << 16) ? (chunks + 255) / 256 : 1 << 16;
+    pad_rows_kernel<<<dim3((unsigned)blocks), dim3(256), 0, s>>>(src, dst, chunks, (int)K, (int)(padded(K) / 16));
+    return hipGetLastError();
+}
+
+// ---- choice --------------------------------------------------------------------------
+//
+// Which tile: the one whose busiest CU is done first, from a model of it in us,
+//   rounds * (bytes of both operand tiles / rate + each),
+// rounds the output tiles a workgroup slot takes after one another.  The rates
+// (bytes a ns and workgroup) and the time for a tile's end were measured at
+// 12 shapes from 1 x 5120 x 2560 to 8192 x 2560 x 5120, where the model is
+// within 20 % of the kernels: for instance 256 x 2560 x 5120 as 4 x 3 blocks
+// 11.2 us (128 x 128 tiles 23.8), 1024 x 2560 x 5120 in 128 x 128 tiles of four
+// stages 24.4 (256 x 256: 51.5), 2048 x 5120 x 2560 in 256 x 256 tiles 33.5
+// (128 x 128: 39.3), 8192 x 2560 x 5120 in 128 x 128 tiles, two workgroups a
+// CU, 114 (256 x 256, which leave the second round a quarter full: 124).
+enum Form { kTile256, kTile128, kTile128Deep, kRing44, kRing43, kRing34, kRing42, kRing24, kRing22, kRing12, kRing21, kRing11, kForms };
+struct FormCost {
+    int tm, tn, slots;
+    double rate, each;
+};
+constexpr FormCost kCosts[kForms] = {
+    {256, 256, kCus, 38., 2.5}, {128, 128, 2 * kCus, 36., 1.5}, {128, 128, kCus, 59., 2.0},
+    {64, 64, kCus, 60., 1.5},   {64, 48, kCus, 60., 1.5},       {48, 64, kCus, 60., 1.5},
+    {64, 32, kCus, 60., 1.5},   {32, 64, kCus, 60., 1.5},       {32, 32, kCus, 60., 1.5},
+    {16, 32, kCus, 60., 1.5},   {32, 16, kCus, 60., 1.5},       {16, 16, kCus, 60., 1.5}};
+constexpr int64_t kMostRingTiles = 1 << 16;  // of 512 threads
+
+int64_t tiles_of(const FormCost &f, int64_t batch, int64_t M, int64_t N)
+{
+    return batch * ((M + f.tm - 1) / f.tm) * ((N + f.tn - 1) / f.tn);
+}
+
+Form choose(int64_t batch, int64_t M, int64_t N, int64_t K)
+{
+    Form best = kTile256;
+    double least = 0.;
+    for (int f = 0; f < kForms; ++f) {
+        const FormCost &c = kCosts[f];
+        const int64_t tiles = tiles_of(c, batch, M, N);
+        if (f >= kRing44 && tiles > kMostRingTiles)
+            continue;
+        const int64_t rounds = (tiles + c.slots - 1) / c.slots;
+        const double steps = (double)((K + kStep - 1) / kStep);
+        const double cost = (double)rounds * ((c.tm + c.tn) * kStep * steps / (1000. * c.rate) + c.each);
+        if (f == 0 || cost < least) {
+            best = (Form)f;
+            least = cost;
+        }
+    }
+    return best;
+}
+
+template <int WM, int WN, int FM, int FN, int STAGES> hipError_t tile(const MatmulParams &p, int slots, bool bf16, hipStream_t s)
+{
+    const dim3 grid((unsigned)(p.tiles < slots ? p.tiles : slots)), block(64 * WM * WN);
+    if (bf16)
+        tile_kernel<WM, WN, FM, FN, STAGES, true><<<grid, block, 0, s>>>(p);
+    else
+        tile_kernel<WM, WN, FM, FN, STAGES, false><<<grid, block, 0, s>>>(p);
+    return hipGetLastError();
+}
+
+template <int FM, int FN, int STAGES> hipError_t ring(const MatmulParams &p, bool bf16, hipStream_t s)
+{
+    const dim3 grid((unsigned)p.tiles);
+    if (bf16)
+        ring_kernel<FM, FN, STAGES, true><<<grid, dim3(512), 0, s>>>(p);
+    else
+        ring_kernel<FM, FN, STAGES, false><<<grid, dim3(512), 0, s>>>(p);
+    return hipGetLastError();
+}
+
+bool off16(const void *p) { return (uintptr_t)p % 16 != 0; }
 
 }  // namespace
 
-size_t int8_matmul_workspace(int64_t, int64_t, int64_t, int64_t) { return 0; }
+size_t int8_matmul_workspace(int64_t rows_a, int64_t rows_b, int64_t K, bool unaligned)
+{
+    return K % 16 != 0 || unaligned ? padded_bytes(rows_a, K) + padded_bytes(rows_b, K) : 0;
+}
 
 hipError_t launch_int8_matmul(const Int8MatmulArgs &a, hipStream_t s)
 {
-    MatmulParams p{a.a, a.b, a.a_scale, a.b_scale, a.out, a.M, a.N, a.K, a.a_shared ? 0 : a.M, a.b_shared ? 0 : a.N,
-                   (a.M + kTile - 1) / kTile, (a.N + kTile - 1) / kTile};
-    const dim3 grid((unsigned)(p.tiles_m * p.tiles_n * a.batch));
-    if (a.bf16)
-        int8_matmul_kernel<true><<<grid, dim3(256), 0, s>>>(p);
-    else
-        int8_matmul_kernel<false><<<grid, dim3(256), 0, s>>>(p);
-    return hipGetLastError();
+    const int64_t rows_a = a.M * (a.a_shared ? 1 : a.batch), rows_b = a.N * (a.b_shared ? 1 : a.batch);
+    MatmulParams p{};
+    p.a = a.a;
+    p.b = a.b;
+    int64_t K = a.K;
+    if (K > 0 && (K % 16 != 0 || off16(a.a) || off16(a.b))) {
+        int8_t *pa = (int8_t *)a.workspace, *pb = pa + padded_bytes(rows_a, K);
+        hipError_t e = pad_rows(a.a, pa, rows_a, K, s);
+        if (e == hipSuccess)
+            e = pad_rows(a.b, pb, rows_b, K, s);
+        if (e != hipSuccess)
+            return e;
+        p.a = pa;
+        p.b = pb;
+        K = padded(K);
+    }
+    const Form f = choose(a.batch, a.M, a.N, K);
+    p.a_scale = a.a_scale;
+    p.b_scale = a.b_scale;
+    p.out = a.out;
+    p.M = a.M;
+    p.N = a.N;
+    p.K = (int)K;
+    p.steps = K > 0 ? (int)((K + kStep - 1) / kStep) : 1;
+    p.a_batch = a.a_shared ? 0 : a.M;
+    p.b_batch = a.b_shared ? 0 : a.N;
+    p.tiles_m = (int)((a.M + kCosts[f].tm - 1) / kCosts[f].tm);
+    p.tiles_n = (int)((a.N + kCosts[f].tn - 1) / kCosts[f].tn);
+    p.tiles = tiles_of(kCosts[f], a.batch, a.M, a.N);
+    // An output that the 256 MB last-level cache cannot keep is stored past
+    // the caches: 1536 x 131072 x 768 takes 188 us so, 202 us without; at
+    // 168 MB of output the two are within 1 %, and a reader may find it cached.
+    p.stream_out = (double)a.batch * a.M * a.N * (a.bf16 ? 2 : 4) > 256e6;
+    switch (f) {
+    case kTile256: return tile<2, 4, 4, 2, 2>(p, kCus, a.bf16, s);
+    case kTile128: return tile<2, 2, 2, 2, 2>(p, 2 * kCus, a.bf16, s);
+    case kTile128Deep: return tile<4, 2, 1, 2, 4>(p, kCus, a.bf16, s);
+    case kRing44: return ring<4, 4, 1>(p, a.bf16, s);
+    case kRing43: return ring<4, 3, 1>(p, a.bf16, s);
+    case kRing34: return ring<3, 4, 1>(p, a.bf16, s);
+    case kRing42: return ring<4, 2, 1>(p, a.bf16, s);
+    case kRing24: return ring<2, 4, 1>(p, a.bf16, s);
+    case kRing22: return ring<2, 2, 2>(p, a.bf16, s);
+    case kRing12: return ring<1, 2, 2>(p, a.bf16, s);
+    case kRing21: return ring<2, 1, 2>(p, a.bf16, s);
+    default: return ring<1, 1, 2>(p, a.bf16, s);
+    }
 }
 
 }  // namespace mamba

@@ -62,6 +62,10 @@ mamba_status norm_entry(const void *x, const void *residual, const float *weight
     return launched(mamba::launch_rms_norm(a, (hipStream_t)stream));
 }
 
+constexpr unsigned kMatmulFlags = MAMBA_INT8_SHARED_A | MAMBA_INT8_SHARED_B | MAMBA_INT8_UNALIGNED;
+
+int64_t operand_rows(int64_t batch, int64_t rows, unsigned shared) { return shared ? rows : batch * rows; }
+
 }  // namespace
 
 extern "C" {
@@ -165,11 +169,14 @@ mamba_status mamba_quantize_int8(const void *x, int8_t *q, float *scale, int64_t
     return launched(mamba::launch_rms_norm(a, (hipStream_t)stream));
 }
 
-size_t mamba_int8_matmul_workspace_size(int64_t batch, int64_t M, int64_t N, int64_t K)
+size_t mamba_int8_matmul_workspace_size(int64_t batch, int64_t M, int64_t N, int64_t K, unsigned flags)
 {
-    if (!sizes_ok(batch, M, N) || K < 0 || K > mamba::kMaxInner || batch * M * N == 0)
+    if (!sizes_ok(batch, M, N) || K < 0 || K > mamba::kMaxInner || (flags & ~kMatmulFlags) != 0 ||
+        !sizes_ok(batch, M, K) || !sizes_ok(batch, N, K) || batch * M * N == 0 || K == 0)
         return 0;
-    return mamba::int8_matmul_workspace(batch, M, N, K);
+    return mamba::int8_matmul_workspace(operand_rows(batch, M, flags & MAMBA_INT8_SHARED_A),
+                                        operand_rows(batch, N, flags & MAMBA_INT8_SHARED_B), K,
+                                        (flags & MAMBA_INT8_UNALIGNED) != 0);
 }
 
 mamba_status mamba_int8_matmul(const int8_t *a, const int8_t *b, const float *a_scale, const float *b_scale,
@@ -180,7 +187,7 @@ mamba_status mamba_int8_matmul(const int8_t *a, const int8_t *b, const float *a_
         return MAMBA_ERR_DTYPE;
     if (!sizes_ok(batch, M, N) || !sizes_ok(batch, M, K) || !sizes_ok(batch, N, K))
         return MAMBA_ERR_SHAPE;
-    if (K > mamba::kMaxInner || (flags & ~(unsigned)(MAMBA_INT8_SHARED_A | MAMBA_INT8_SHARED_B)) != 0)
+    if (K > mamba::kMaxInner || (flags & ~kMatmulFlags) != 0)
         return MAMBA_ERR_UNSUPPORTED;
     // launch grid: one workgroup of at most 512 threads per 128 x 128 outputs
     if (batch > 0 && ((M + 127) / 128) * ((N + 127) / 128) >= (int64_t(1) << 23) / batch)
@@ -191,9 +198,10 @@ mamba_status mamba_int8_matmul(const int8_t *a, const int8_t *b, const float *a_
         return MAMBA_ERR_NULL;
     if (!aligned(a_scale, 4) || !aligned(b_scale, 4) || !aligned(out, esize(out_type)))
         return MAMBA_ERR_ALIGN;
-    const int64_t rows_a = M * ((flags & MAMBA_INT8_SHARED_A) ? 1 : batch),
-                  rows_b = N * ((flags & MAMBA_INT8_SHARED_B) ? 1 : batch);
-    const size_t need = mamba::int8_matmul_workspace(batch, M, N, K);
+    const int64_t rows_a = operand_rows(batch, M, flags & MAMBA_INT8_SHARED_A),
+                  rows_b = operand_rows(batch, N, flags & MAMBA_INT8_SHARED_B);
+    // whether an operand needs the workspace shows in its address, with or without the flag
+    const size_t need = K == 0 ? 0 : mamba::int8_matmul_workspace(rows_a, rows_b, K, !aligned(a, 16) || !aligned(b, 16));
     if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
         return MAMBA_ERR_WORKSPACE;
     const Range ro = rng(out, (size_t)(batch * M * N) * esize(out_type)), rw = rng(workspace, need);
@@ -207,7 +215,7 @@ mamba_status mamba_int8_matmul(const int8_t *a, const int8_t *b, const float *a_
     mamba_status st = device_ok();
     if (st != MAMBA_OK)
         return st;
-    mamba::Int8MatmulArgs args{a, b, a_scale, b_scale, out, (int32_t *)workspace, batch, M, N, K,
+    mamba::Int8MatmulArgs args{a, b, a_scale, b_scale, out, workspace, batch, M, N, K,
                                (flags & MAMBA_INT8_SHARED_A) != 0, (flags & MAMBA_INT8_SHARED_B) != 0,
                                out_type == MAMBA_BF16};
     return launched(mamba::launch_int8_matmul(args, (hipStream_t)stream));
