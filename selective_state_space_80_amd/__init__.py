@@ -189,8 +189,22 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+_current_raw_stream = None
+
+
 def _raw_stream(t):
-    return _torch().cuda.current_stream(t.device).cuda_stream
+    """The current stream of t's GPU as an integer (raises for a CPU tensor)."""
+    global _current_raw_stream
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"expected a tensor on a GPU, got one on {t.device}")
+    if _current_raw_stream is None:
+        torch = _torch()
+        # the handle itself costs 0.1 us; by way of a torch.cuda.Stream object, 1.9
+        _current_raw_stream = getattr(
+            torch._C, "_cuda_getCurrentRawStream",
+            lambda i: torch.cuda.current_stream(torch.device("cuda", i)).cuda_stream)
+    return _current_raw_stream(index)
 
 
 def _raise(st, where):
@@ -573,27 +587,11 @@ def ssd_scan_fwd(x, dt, A, Bm, Cm, dt_bias=None, Dskip=None, z=None, h0=None,
     return out
 
 
-def _norm_arguments(x, weight, residual, residual_out):
-    """Checks shared by the two forward norms; returns (rows, D, residual_out)."""
-    torch = _torch()
-    if x.dim() < 1:
-        raise ValueError("x has no axis to normalise")
-    shape, dev = x.shape, x.device
-    D = shape[-1]
-    _check(x, "x", shape)
-    _check(weight, "weight", (D,), torch.float32, dev)
-    if residual is None:
-        if residual_out is not None:
-            raise ValueError("residual_out needs residual")
-    else:
-        if residual.dtype != torch.float32 and residual.dtype != x.dtype:
-            raise TypeError(f"residual must be float32 or {x.dtype}, got {residual.dtype}")
-        _check(residual, "residual", shape, device=dev)
-        if residual_out is None:
-            residual_out = torch.empty_like(residual)
-        else:
-            _check(residual_out, "residual_out", shape, residual.dtype, dev)
-    return _rows(x), D, residual_out
+def _is(t, shape, dtype, index):
+    """A contiguous tensor of this shape and dtype on GPU `index` (the quick
+    form of _check, which says what is wrong with one that is not)."""
+    return (t.shape == shape and t.dtype == dtype and t.get_device() == index
+            and t.is_contiguous())
 
 
 def _rows(x):
@@ -603,23 +601,49 @@ def _rows(x):
     return rows
 
 
+def _norm_arguments(x, weight, residual, residual_out):
+    """Checks shared by the two forward norms; returns (rows, D, residual's
+    element type, residual_out)."""
+    torch = _torch()
+    if x.dim() < 1:
+        raise ValueError("x has no axis to normalise")
+    shape, index = x.shape, x.get_device()
+    D = shape[-1]
+    if not (x.is_contiguous() and _is(weight, (D,), torch.float32, index)):
+        _check(x, "x", shape)
+        _check(weight, "weight", (D,), torch.float32, x.device)
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs residual")
+        return _rows(x), D, 0, None
+    res_t = residual.dtype
+    if res_t != torch.float32 and res_t != x.dtype:
+        raise TypeError(f"residual must be float32 or {x.dtype}, got {res_t}")
+    if not _is(residual, shape, res_t, index):
+        _check(residual, "residual", shape, device=x.device)
+    if residual_out is None:
+        residual_out = torch.empty_like(residual)
+    elif not _is(residual_out, shape, res_t, index):
+        _check(residual_out, "residual_out", shape, res_t, x.device)
+    return _rows(x), D, _io_dtype(residual), residual_out
+
+
 def rms_norm(x, weight, residual=None, eps=1e-5, out=None, residual_out=None):
     """Root-mean-square norm over the last axis with the residual's addition:
     h = x + residual, out = h / sqrt(mean(h^2) + eps) * weight.  x [..., D]
     f32/bf16; weight [D] f32; residual [..., D] f32 or x's dtype.  Returns out
     of x's dtype, and with a residual (out, residual_out): h in the residual's
     dtype (`residual_out` may be `residual` itself, updated in place)."""
-    torch = _torch()
     lib = load_library()
-    M, D, residual_out = _norm_arguments(x, weight, residual, residual_out)
+    M, D, res_t, residual_out = _norm_arguments(x, weight, residual, residual_out)
     if out is None:
-        out = torch.empty_like(x)
+        out = _torch().empty_like(x)
     else:
         _check(out, "out", x.shape, x.dtype, x.device)
-    st = lib.mamba_rms_norm(_addr(x), _addr(residual), _addr(weight), _addr(out),
-                            _addr(residual_out), M, D, eps, _io_dtype(x),
-                            0 if residual is None else _io_dtype(residual), _raw_stream(x))
-    _raise(st, "mamba_rms_norm")
+    st = lib.mamba_rms_norm(x.data_ptr(), _addr(residual), weight.data_ptr(), out.data_ptr(),
+                            _addr(residual_out), M, D, eps, _io_dtype(x), res_t, _raw_stream(x))
+    if st:
+        _raise(st, "mamba_rms_norm")
     return out if residual is None else (out, residual_out)
 
 
@@ -630,20 +654,25 @@ def rms_norm_int8(x, weight, residual=None, eps=1e-5, out=None, scale=None, resi
     residual.  A row with a NaN or an infinity has scale NaN."""
     torch = _torch()
     lib = load_library()
-    M, D, residual_out = _norm_arguments(x, weight, residual, residual_out)
+    M, D, res_t, residual_out = _norm_arguments(x, weight, residual, residual_out)
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+        out = torch.empty_like(x, dtype=torch.int8)
     else:
         _check(out, "out", x.shape, torch.int8, x.device)
     if scale is None:
         scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
     else:
         _check(scale, "scale", x.shape[:-1], torch.float32, x.device)
-    st = lib.mamba_rms_norm_int8(_addr(x), _addr(residual), _addr(weight), _addr(out),
-                                 _addr(scale), _addr(residual_out), M, D, eps, _io_dtype(x),
-                                 0 if residual is None else _io_dtype(residual), _raw_stream(x))
-    _raise(st, "mamba_rms_norm_int8")
+    st = lib.mamba_rms_norm_int8(x.data_ptr(), _addr(residual), weight.data_ptr(), out.data_ptr(),
+                                 scale.data_ptr(), _addr(residual_out), M, D, eps, _io_dtype(x),
+                                 res_t, _raw_stream(x))
+    if st:
+        _raise(st, "mamba_rms_norm_int8")
     return (out, scale) if residual is None else (out, scale, residual_out)
+
+
+def rms_norm_bwd_workspace_size(M, D) -> int:
+    return int(load_library().mamba_rms_norm_bwd_workspace_size(M, D))
 
 
 def rms_norm_bwd(dy, h, weight, dresidual_out=None, eps=1e-5, workspace=None):
@@ -656,26 +685,31 @@ def rms_norm_bwd(dy, h, weight, dresidual_out=None, eps=1e-5, workspace=None):
     lib = load_library()
     if dy.dim() < 1:
         raise ValueError("dy has no axis to normalise")
-    shape, dev = dy.shape, dy.device
+    shape, dev, index, h_t = dy.shape, dy.device, dy.get_device(), h.dtype
     D = shape[-1]
-    _check(dy, "dy", shape)
-    if h.dtype != torch.float32 and h.dtype != dy.dtype:
-        raise TypeError(f"h must be float32 or {dy.dtype}, got {h.dtype}")
-    _check(h, "h", shape, device=dev)
-    _check(weight, "weight", (D,), torch.float32, dev)
-    _check(dresidual_out, "dresidual_out", shape, h.dtype, dev, optional=True)
+    if h_t != torch.float32 and h_t != dy.dtype:
+        raise TypeError(f"h must be float32 or {dy.dtype}, got {h_t}")
+    if not (dy.is_contiguous() and _is(h, shape, h_t, index)
+            and _is(weight, (D,), torch.float32, index)):
+        _check(dy, "dy", shape)
+        _check(h, "h", shape, device=dev)
+        _check(weight, "weight", (D,), torch.float32, dev)
+    if dresidual_out is not None and not _is(dresidual_out, shape, h_t, index):
+        _check(dresidual_out, "dresidual_out", shape, h_t, dev)
     M = _rows(dy)
     dx = torch.empty_like(dy)
-    dresidual = None if h.dtype == dy.dtype else torch.empty_like(h)
-    dweight = torch.empty((D,), dtype=torch.float32, device=dev)
+    dresidual = None if h_t == dy.dtype else torch.empty_like(h)
+    dweight = torch.empty_like(weight)
     if workspace is None:
-        need = int(lib.mamba_rms_norm_bwd_workspace_size(M, D))
+        need = lib.mamba_rms_norm_bwd_workspace_size(M, D)
         workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     st = lib.mamba_rms_norm_bwd(
-        _addr(dy), _addr(h), _addr(weight), _addr(dresidual_out), _addr(dx), _addr(dresidual),
-        _addr(dweight), _addr(workspace), 0 if workspace is None else workspace.numel(), M, D, eps,
-        _io_dtype(dy), _io_dtype(h), _raw_stream(dy))
-    _raise(st, "mamba_rms_norm_bwd")
+        dy.data_ptr(), h.data_ptr(), weight.data_ptr(), _addr(dresidual_out), dx.data_ptr(),
+        _addr(dresidual), dweight.data_ptr(), _addr(workspace),
+        0 if workspace is None else workspace.numel(), M, D, eps, _io_dtype(dy), _io_dtype(h),
+        _raw_stream(dy))
+    if st:
+        _raise(st, "mamba_rms_norm_bwd")
     return {"dx": dx, "dresidual": dx if dresidual is None else dresidual, "dweight": dweight}
 
 
@@ -686,27 +720,31 @@ def quantize_int8(x, channel_major=False, out=None, scale=None):
     as the scans write their output, and q [B, L, K], scale [B, L]."""
     torch = _torch()
     lib = load_library()
-    dev = x.device
-    _check(x, "x", x.shape)
+    dev, shape = x.device, x.shape
+    if not x.is_contiguous():
+        _check(x, "x", shape)
     if channel_major:
-        B, K, L = x.shape
+        if len(shape) != 3:
+            raise ValueError(f"channel-major x is [B, K, L], got {tuple(shape)}")
+        B, K, L = shape
         lead = (B, L)
     else:
-        if x.dim() < 1:
+        if len(shape) < 1:
             raise ValueError("x has no axis to quantise")
-        lead, K = tuple(x.shape[:-1]), x.shape[-1]
+        lead, K = shape[:-1], shape[-1]
         B, L = 1, _rows(x)
     if out is None:
-        out = torch.empty(lead + (K,), dtype=torch.int8, device=dev)
+        out = torch.empty((*lead, K), dtype=torch.int8, device=dev)
     else:
-        _check(out, "out", lead + (K,), torch.int8, dev)
+        _check(out, "out", (*lead, K), torch.int8, dev)
     if scale is None:
         scale = torch.empty(lead, dtype=torch.float32, device=dev)
     else:
         _check(scale, "scale", lead, torch.float32, dev)
-    st = lib.mamba_quantize_int8(_addr(x), _addr(out), _addr(scale), B, L, K, int(channel_major),
-                                 _io_dtype(x), _raw_stream(x))
-    _raise(st, "mamba_quantize_int8")
+    st = lib.mamba_quantize_int8(x.data_ptr(), out.data_ptr(), scale.data_ptr(), B, L, K,
+                                 1 if channel_major else 0, _io_dtype(x), _raw_stream(x))
+    if st:
+        _raise(st, "mamba_quantize_int8")
     return out, scale
 
 
@@ -739,22 +777,31 @@ def int8_matmul(a, b, a_scale, b_scale, out_dtype=None, out=None, workspace=None
         batch = a.shape[0] if a.dim() == 3 else b.shape[0]
         lead = (batch,)
         flags = ((INT8_SHARED_A if a.dim() == 2 else 0) | (INT8_SHARED_B if b.dim() == 2 else 0))
-    _check(a, "a", (lead if a.dim() == 3 else ()) + (M, K), torch.int8)
-    _check(b, "b", (lead if b.dim() == 3 else ()) + (N, K), torch.int8, dev)
-    _check(a_scale, "a_scale", a.shape[:-1], torch.float32, dev)
-    _check(b_scale, "b_scale", b.shape[:-1], torch.float32, dev)
+    index, i8, f32 = a.get_device(), torch.int8, torch.float32
+    a_lead = lead if a.dim() == 3 else ()
+    b_lead = lead if b.dim() == 3 else ()
+    if not (a.dtype == i8 and a.is_contiguous() and _is(b, (*b_lead, N, K), i8, index)
+            and _is(a_scale, (*a_lead, M), f32, index) and _is(b_scale, (*b_lead, N), f32, index)):
+        _check(a, "a", (*a_lead, M, K), i8)
+        _check(b, "b", (*b_lead, N, K), i8, dev)
+        _check(a_scale, "a_scale", (*a_lead, M), f32, dev)
+        _check(b_scale, "b_scale", (*b_lead, N), f32, dev)
     if out is None:
-        out = torch.empty(lead + (M, N), dtype=torch.bfloat16 if out_dtype is None else out_dtype,
+        out = torch.empty((*lead, M, N), dtype=torch.bfloat16 if out_dtype is None else out_dtype,
                           device=dev)
     else:
-        _check(out, "out", lead + (M, N), out_dtype, dev)
-    if workspace is None and (K % 16 or (a.data_ptr() | b.data_ptr()) % 16):
-        need = int(lib.mamba_int8_matmul_workspace_size(batch, M, N, K, flags | INT8_UNALIGNED))
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    st = lib.mamba_int8_matmul(_addr(a), _addr(b), _addr(a_scale), _addr(b_scale), _addr(out),
-                               _addr(workspace), 0 if workspace is None else workspace.numel(),
-                               batch, M, N, K, _io_dtype(out), flags, _raw_stream(a))
-    _raise(st, "mamba_int8_matmul")
+        _check(out, "out", (*lead, M, N), out_dtype, dev)
+    pa, pb, nbytes = a.data_ptr(), b.data_ptr(), 0
+    if workspace is not None:
+        nbytes = workspace.numel()
+    elif K % 16 or (pa | pb) % 16:
+        nbytes = lib.mamba_int8_matmul_workspace_size(batch, M, N, K, flags | INT8_UNALIGNED)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    st = lib.mamba_int8_matmul(pa, pb, a_scale.data_ptr(), b_scale.data_ptr(), out.data_ptr(),
+                               _addr(workspace), nbytes, batch, M, N, K, _io_dtype(out), flags,
+                               _raw_stream(a))
+    if st:
+        _raise(st, "mamba_int8_matmul")
     return out
 
 
