@@ -17,6 +17,8 @@
 // with their rows padded by zeros (pad_rows_kernel).
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "device_common.h"
 #include "quant.h"
 
@@ -27,6 +29,7 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kStep = 128;     // bytes of the inner axis a step takes: a cache line of every row
 constexpr int kCus = 256;
@@ -41,7 +44,6 @@ struct MatmulParams {
     int64_t a_batch, b_batch;  // rows between batches: 0 = shared
     int tiles_m, tiles_n;
     int64_t tiles;             // of all batches
-    bool stream_out;           // output stores pass the caches by
 };
 
 // Past the inner axis' end a lane loads these instead.
@@ -127,10 +129,16 @@ __device__ __forceinline__ Share xcd_share(int64_t tiles, int xcd)
 // there every wave has read this stage (it may be overwritten) and the next
 // stage has arrived.
 //
-// 256 x 256 outputs by 8 waves reads 26 bytes a clock and CU from L2 and fills
-// the matrix units to 62 % at 1.9 GHz, which is where this card's power limit
-// holds random data (the same kernel without any loads: 2.7 POP/s; with zeros
-// as data: 3.2; as it is: 2.45 at 8192^3, the library's 8-bit product 2.14).
+// What bounds it is the card's power: 256 x 256 outputs by 8 waves fill the
+// matrix units to 62 % at 1.85 GHz on random data (2.45 POP/s at 8192^3, where
+// the library's 8-bit product reaches 2.14).  With zeros as data the clock
+// stays at 2.4 GHz; without any loads, on random data, the products alone
+// reach 2.75.  LDS has no bank conflicts and is read a quarter of the time.
+// Of a tile's end, 5 us of the model below, most is arithmetic (3.5
+// instructions an output) and the stores' way to memory: whole lines past the
+// caches, issued without branches, and not waited for by the next tile's first
+// step (8 x 5120 x 2048 x 2560: 212 us with cached, guarded, waited-for stores
+// and scales loaded there, 178 so).
 template <int WM, int WN, int FM, int FN, int STAGES, bool BF16>
 __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const MatmulParams p)
 {
@@ -138,6 +146,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const MatmulParam
     constexpr int kStage = (TM + TN) * kStep;
     constexpr int LA = TM / 8 / NW, LB = TN / 8 / NW;  // loads of a wave and stage
     constexpr int kStaging = 4096;                     // of a wave's outputs: 32 rows of 128 bytes
+    constexpr int SA = (FM + 1) / 2, SB = (FN + 1) / 2;  // registers of a wave's scales
+    constexpr int kWide = BF16 ? 2 : 1;                // blocks of 32 columns in 128 bytes
+    constexpr int kPerChunk = BF16 ? 8 : 4;            // elements in 16 bytes
+    constexpr int kStores = FM * 4 * (FN / kWide);     // of a wave and a whole tile
+    static_assert(FN % kWide == 0, "a wave's columns fill whole lines");
     __shared__ __attribute__((aligned(16))) char smem[STAGES * kStage + NW * kStaging];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -228,26 +241,48 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const MatmulParam
     i32x4 fa[2][FM], fb[2][FN];
     fragments(fa[0], fb[0], 0, 0);
     int stage = 0;
+    bool stores_known = false;  // kStores stores were issued behind the last loads
     for (int64_t ti = slot; ti < share.count; ti += stride) {
+        const Tile t = tile_at(ti);
+        // this wave's scales, a row or column a lane; they wait here for the end of the tile
+        const float *a_scale = p.a_scale + t.batch * p.a_batch, *b_scale = p.b_scale + t.batch * p.b_batch;
+        float sa[SA], sb[SB];
+#pragma unroll
+        for (int i = 0; i < SA; ++i) {
+            const int64_t m = t.m0 + wm * FM * 32 + i * 64 + lane;
+            sa[i] = a_scale[m < p.M ? m : p.M - 1];
+        }
+#pragma unroll
+        for (int i = 0; i < SB; ++i) {
+            const int64_t n = t.n0 + wn * FN * 32 + i * 64 + lane;
+            sb[i] = b_scale[n < p.N ? n : p.N - 1];
+        }
         i32x16 acc[FM][FN];
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-            for (int j = 0; j < FN; ++j)
-                acc[i][j] = i32x16{0};
-        for (int s = 0; s < p.steps; ++s) {
+        auto step = [&](int s, auto first) {
             const int next = stage + 1 == STAGES ? 0 : stage + 1;
 #pragma unroll
             for (int round = 0; round < 4; ++round) {
                 if (round < 3) {
                     fragments(fa[(round + 1) & 1], fb[(round + 1) & 1], stage, round + 1);
                 } else {
-                    // The oldest stage in flight has to have arrived.  With all
-                    // others issued behind it, all but theirs may be pending;
-                    // stores of the tile before may be among the pending ones
-                    // in a tile's first step, which waits for everything.
-                    if (STAGES > 2 && ahead == STAGES - 1 && (s > 0 || ti == slot))
+                    if (s == p.steps - 1) {  // the scales have arrived long since: the compiler's wait for them
+#pragma unroll
+                        for (int i = 0; i < SA; ++i)
+                            asm volatile("" : "+v"(sa[i]));
+#pragma unroll
+                        for (int i = 0; i < SB; ++i)
+                            asm volatile("" : "+v"(sb[i]));
+                    }
+                    // The oldest stage in flight has to have arrived: what was
+                    // issued behind it may be pending (memory operations count
+                    // down in order).  Behind it are the younger stages, or in
+                    // a tile's first step of a two-stage kernel the stores of
+                    // the tile before.  Where their number is not known,
+                    // everything is waited for.
+                    if (STAGES > 2 && !first && ahead == STAGES - 1)
                         asm volatile("s_waitcnt vmcnt(%0)" ::"n"((STAGES - 2) * (LA + LB)) : "memory");
+                    else if (STAGES == 2 && first && stores_known)
+                        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kStores) : "memory");
                     else
                         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
                     if (ahead > 0)
@@ -261,9 +296,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const MatmulParam
 #pragma unroll
                 for (int i = 0; i < FM; ++i)
 #pragma unroll
-                    for (int j = 0; j < FN; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[round & 1][j], fa[round & 1][i],
-                                                                          acc[i][j], 0, 0, 0);
+                    for (int j = 0; j < FN; ++j) {
+                        const i32x16 to = first && round == 0 ? i32x16{0} : acc[i][j];
+                        acc[i][j] =
+                            __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[round & 1][j], fa[round & 1][i], to, 0, 0, 0);
+                    }
                 // the reads spread evenly between the products
 #pragma unroll
                 for (int q = 0; q < FM + FN; ++q) {
@@ -272,78 +309,88 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const MatmulParam
                 }
             }
             stage = next;
-        }
+        };
+        step(0, std::true_type{});
+        for (int s = 1; s < p.steps; ++s)
+            step(s, std::false_type{});
         // Scale and store, 32 rows of 128 bytes at a time through the wave's
         // own piece of LDS, so that a store instruction writes 8 whole lines
         // (straight from the registers it would touch 32 rows, 16 bytes each:
         // 40 us more at 8 x 5120 x 2048 x 2560).
-        const Tile t = tile_at(ti);
         using T = typename Elem<BF16>::T;
         char *st = smem + STAGES * kStage + wave * kStaging;
-        const float *a_scale = p.a_scale + t.batch * p.a_batch, *b_scale = p.b_scale + t.batch * p.b_batch;
-        constexpr int kWide = BF16 ? 2 : 1;        // blocks of 32 columns in 128 bytes
-        constexpr int kPerChunk = BF16 ? 8 : 4;    // elements in 16 bytes
-        static_assert(FN % kWide == 0, "a wave's columns fill whole lines");
 #pragma unroll
-        for (int j0 = 0; j0 < FN; j0 += kWide) {
-            float sb[kWide][4][4];
+        for (int i = 0; i < SA; ++i)
+            ((float *)st)[i * 64 + lane] = sa[i];
 #pragma unroll
-            for (int j = 0; j < kWide; ++j)
+        for (int i = 0; i < SB; ++i)
+            ((float *)st)[(SA + i) * 64 + lane] = sb[i];
+        float row_scale[FM];
+        f32x4 col_scale[FN][4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int64_t n = t.n0 + (wn * FN + j0 + j) * 32 + e * 8 + half * 4;
+        for (int i = 0; i < FM; ++i)
+            row_scale[i] = ((const float *)st)[i * 32 + fr];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        sb[j][e][q] = b_scale[n + q < p.N ? n + q : p.N - 1];
-                }
+        for (int j = 0; j < FN; ++j)
 #pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                const int64_t m = t.m0 + (wm * FM + i) * 32;
-                const float sa = a_scale[m + fr < p.M ? m + fr : p.M - 1];
+            for (int e = 0; e < 4; ++e)
+                col_scale[j][e] = *(const f32x4 *)(st + (SA * 64 + j * 32 + e * 8 + half * 4) * 4);
+        auto finish = [&](auto full) {
 #pragma unroll
-                for (int j = 0; j < kWide; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float v[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            v[q] = (float)acc[i][j0 + j][e * 4 + q] * sa * sb[j][e][q];
-                        if constexpr (BF16) {
-                            const u32x2 w = {cvt2(v[0], v[1]), cvt2(v[2], v[3])};
-                            *(u32x2 *)(st + fr * 128 + place(fr, j * 4 + e) * 16 + half * 8) = w;
-                        } else {
-                            const u32x4 w = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                                             __float_as_uint(v[3])};
-                            *(u32x4 *)(st + fr * 128 + place(fr, e * 2 + half) * 16) = w;
-                        }
-                    }
+            for (int j0 = 0; j0 < FN; j0 += kWide) {
                 const int64_t n = t.n0 + (wn * FN + j0) * 32 + (lane & 7) * kPerChunk;
+                const int64_t m = t.m0 + wm * FM * 32 + (lane >> 3);
+                T *o = (T *)p.out + (t.batch * p.M + m) * p.N + n;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = r * 8 + (lane >> 3);
-                    const u32x4 v = *(const u32x4 *)(st + row * 128 + place(row, lane & 7) * 16);
-                    if (m + row >= p.M)
-                        continue;
-                    T *o = (T *)p.out + (t.batch * p.M + m + row) * p.N + n;
-                    if (n + kPerChunk <= p.N) {
-                        typedef u32x4 __attribute__((aligned(2))) loose;  // rows start at any element
-                        if (p.stream_out)
-                            __builtin_nontemporal_store(v, (loose *)o);
-                        else
-                            *(loose *)o = v;
-                    } else {
+                for (int i = 0; i < FM; ++i) {
 #pragma unroll
-                        for (int q = 0; q < kPerChunk; ++q)
-                            if (n + q < p.N) {
-                                if constexpr (BF16)
-                                    o[q] = (uint16_t)(v[q / 2] >> (16 * (q & 1)));
-                                else
-                                    o[q] = __uint_as_float(v[q]);
+                    for (int j = 0; j < kWide; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float v[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                v[q] = (float)acc[i][j0 + j][e * 4 + q] * row_scale[i] * col_scale[j0 + j][e][q];
+                            if constexpr (BF16) {
+                                const u32x2 w = {cvt2(v[0], v[1]), cvt2(v[2], v[3])};
+                                *(u32x2 *)(st + fr * 128 + place(fr, j * 4 + e) * 16 + half * 8) = w;
+                            } else {
+                                const u32x4 w = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                                 __float_as_uint(v[3])};
+                                *(u32x4 *)(st + fr * 128 + place(fr, e * 2 + half) * 16) = w;
                             }
+                        }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = r * 8 + (lane >> 3);
+                        const u32x4 v = *(const u32x4 *)(st + row * 128 + place(row, lane & 7) * 16);
+                        typedef u32x4 __attribute__((aligned(2))) loose;  // rows start at any element
+                        T *to = o + (int64_t)(i * 32 + r * 8) * p.N;
+                        if constexpr (full) {
+                            __builtin_nontemporal_store(v, (loose *)to);
+                        } else if (m + i * 32 + r * 8 < p.M) {
+                            if (n + kPerChunk <= p.N) {
+                                __builtin_nontemporal_store(v, (loose *)to);
+                            } else {
+#pragma unroll
+                                for (int q = 0; q < kPerChunk; ++q)
+                                    if (n + q < p.N) {
+                                        if constexpr (BF16)
+                                            to[q] = (uint16_t)(v[q / 2] >> (16 * (q & 1)));
+                                        else
+                                            to[q] = __uint_as_float(v[q]);
+                                    }
+                            }
+                        }
                     }
                 }
             }
-        }
+        };
+        stores_known = t.m0 + TM <= p.M && t.n0 + TN <= p.N;
+        if (stores_known)
+            finish(std::true_type{});
+        else
+            finish(std::false_type{});
     }
 }
 
@@ -456,61 +503,72 @@ template <int FM, int FN, int STAGES, bool BF16> __global__ __launch_bounds__(51
 
 // ---- rows of any size and alignment -------------------------------------------------
 
-// [rows, K] at any byte to [rows, pitch], pitch = K rounded up to 16: one
-// 16-byte chunk of the result a thread.
-__global__ __launch_bounds__(256) void pad_rows_kernel(const int8_t *src, int8_t *dst, int64_t chunks, int K,
-                                                       int per_row)
+// [rows, K] at any byte to [rows, pitch], pitch = K rounded up to 16, both
+// operands in one launch: one 16-byte chunk of the result a thread.
+struct PadParams {
+    const int8_t *src[2];
+    int8_t *dst[2];
+    int64_t chunks[2];
+    int K, per_row;
+};
+__global__ __launch_bounds__(256) void pad_rows_kernel(const PadParams p)
 {
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < chunks; i += (int64_t)gridDim.x * 256) {
-        const int64_t row = i / per_row;
-        const int k = (int)(i % per_row) * 16;
-        const int8_t *from = src + row * K + k;
+    const int64_t stride = (int64_t)gridDim.x * 256;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.chunks[0] + p.chunks[1]; i += stride) {
+        const bool second = i >= p.chunks[0];
+        const int64_t chunk = second ? i - p.chunks[0] : i, row = chunk / p.per_row;
+        const int k = (int)(chunk % p.per_row) * 16;
+        const int8_t *from = (second ? p.src[1] : p.src[0]) + row * p.K + k;
         u32x4 v = {0, 0, 0, 0};
-        if (k + 16 <= K) {
+        if (k + 16 <= p.K) {
             __builtin_memcpy(&v, from, 16);
         } else {
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-                if (k + j < K)
+                if (k + j < p.K)
                     v[j / 4] |= (uint32_t)(uint8_t)from[j] << (8 * (j % 4));
         }
-        *(u32x4 *)(dst + i * 16) = v;
+        *(u32x4 *)((second ? p.dst[1] : p.dst[0]) + chunk * 16) = v;
     }
 }
 
 int64_t padded(int64_t K) { return (K + 15) / 16 * 16; }
 size_t padded_bytes(int64_t rows, int64_t K) { return ((size_t)(rows * padded(K)) + 255) / 256 * 256; }
 
-hipError_t pad_rows(const int8_t *src, int8_t *dst, int64_t rows, int64_t K, hipStream_t s)
-{
-    const int64_t chunks = rows * (padded(K) / 16);
-    const int64_t blocks = (chunks + 255) / 256 < (1 << 16) ? (chunks + 255) / 256 : 1 << 16;
-    pad_rows_kernel<<<dim3((unsigned)blocks), dim3(256), 0, s>>>(src, dst, chunks, (int)K, (int)(padded(K) / 16));
-    return hipGetLastError();
-}
-
 // ---- choice --------------------------------------------------------------------------
 //
-// Which tile: the one whose busiest CU is done first, from a model of it in us,
-//   rounds * (bytes of both operand tiles / rate + each),
-// rounds the output tiles a workgroup slot takes after one another.  The rates
-// (bytes a ns and workgroup) and the time for a tile's end were measured at
-// 12 shapes from 1 x 5120 x 2560 to 8192 x 2560 x 5120, where the model is
-// within 20 % of the kernels: for instance 256 x 2560 x 5120 as 4 x 3 blocks
-// 11.2 us (128 x 128 tiles 23.8), 1024 x 2560 x 5120 in 128 x 128 tiles of four
-// stages 24.4 (256 x 256: 51.5), 2048 x 5120 x 2560 in 256 x 256 tiles 33.5
-// (128 x 128: 39.3), 8192 x 2560 x 5120 in 128 x 128 tiles, two workgroups a
-// CU, 114 (256 x 256, which leave the second round a quarter full: 124).
+// Which tile: the one whose time, by this model, is least, in us:
+//   max(rounds * steps * alone, tiles / slots * steps * busy) + rounds * each + once
+// rounds: output tiles a workgroup slot takes after one another; alone: a step
+// of 128 bytes of the inner axis on an otherwise free card; busy: with every
+// slot taken, where power and the shared caches hold the rate; each: a tile's
+// end.  The constants are fitted to 49 shapes from 1 x 5120 x 2560 to
+// 16384 x 16384 x 2560, each timed in every form that suits it; the form chosen
+// is the fastest or within 7 % of it at all of them.  Both sides of some of the
+// choices, in us:
+//   8 x 5120 x 2048 x 2560   256 x 256 tiles 178, 128 x 128 217
+//   4096 x 1536 x 768        256 x 256 tiles 12.5, 128 x 128 9.5
+//   1024 x 2560 x 5120       128 x 128 tiles of two stages 30.8, of four 23.7
+//   300 x 8192 x 256         the same 5.4 and 5.6; rings of 64 x 64 16.3
+//   256 x 2560 x 5120        128 x 128 tiles 23.4, rings of 64 x 64 13.1, of 64 x 48 11.7
+//   64 x 2560 x 5120         rings of 64 x 64 13.5, of 32 x 32 7.0
+//   2048 x 64 x 5120         rings of 32 x 32 7.3, of 16 x 32 6.0
+//   16 x 2560 x 5120         rings of 32 x 32 6.2, of 16 x 32 5.7, of 16 x 16 4.6
 enum Form { kTile256, kTile128, kTile128Deep, kRing44, kRing43, kRing34, kRing42, kRing24, kRing22, kRing12, kRing21, kRing11, kForms };
 struct FormCost {
     int tm, tn, slots;
-    double rate, each;
+    double alone, busy, each, once;
 };
-constexpr FormCost kCosts[kForms] = {
-    {256, 256, kCus, 38., 2.5}, {128, 128, 2 * kCus, 36., 1.5}, {128, 128, kCus, 59., 2.0},
-    {64, 64, kCus, 60., 1.5},   {64, 48, kCus, 60., 1.5},       {48, 64, kCus, 60., 1.5},
-    {64, 32, kCus, 60., 1.5},   {32, 64, kCus, 60., 1.5},       {32, 32, kCus, 60., 1.5},
-    {16, 32, kCus, 60., 1.5},   {32, 16, kCus, 60., 1.5},       {16, 16, kCus, 60., 1.5}};
+constexpr FormCost ring_cost(int tm, int tn)
+{
+    return {tm, tn, kCus, .00124 * (tm + tn), .00166 * (tm + tn), 1.1 + .0008 * tm * tn, 1.6};
+}
+constexpr FormCost kCosts[kForms] = {{256, 256, kCus, 1.14, 1.64, 5.35, 1.25},
+                                     {128, 128, 2 * kCus, 0.69, 1.03, 2.31, 1.54},
+                                     {128, 128, kCus, 0.53, 0.61, 1.41, 2.26},
+                                     ring_cost(64, 64), ring_cost(64, 48), ring_cost(48, 64),
+                                     ring_cost(64, 32), ring_cost(32, 64), ring_cost(32, 32),
+                                     ring_cost(16, 32), ring_cost(32, 16), ring_cost(16, 16)};
 constexpr int64_t kMostRingTiles = 1 << 16;  // of 512 threads
 
 int64_t tiles_of(const FormCost &f, int64_t batch, int64_t M, int64_t N)
@@ -527,9 +585,9 @@ Form choose(int64_t batch, int64_t M, int64_t N, int64_t K)
         const int64_t tiles = tiles_of(c, batch, M, N);
         if (f >= kRing44 && tiles > kMostRingTiles)
             continue;
-        const int64_t rounds = (tiles + c.slots - 1) / c.slots;
-        const double steps = (double)((K + kStep - 1) / kStep);
-        const double cost = (double)rounds * ((c.tm + c.tn) * kStep * steps / (1000. * c.rate) + c.each);
+        const double rounds = (double)((tiles + c.slots - 1) / c.slots), steps = (double)((K + kStep - 1) / kStep);
+        const double alone = rounds * c.alone, busy = (double)tiles / c.slots * c.busy;
+        const double cost = steps * (alone > busy ? alone : busy) + rounds * c.each + c.once;
         if (f == 0 || cost < least) {
             best = (Form)f;
             least = cost;
@@ -576,9 +634,11 @@ hipError_t launch_int8_matmul(const Int8MatmulArgs &a, hipStream_t s)
     int64_t K = a.K;
     if (K > 0 && (K % 16 != 0 || off16(a.a) || off16(a.b))) {
         int8_t *pa = (int8_t *)a.workspace, *pb = pa + padded_bytes(rows_a, K);
-        hipError_t e = pad_rows(a.a, pa, rows_a, K, s);
-        if (e == hipSuccess)
-            e = pad_rows(a.b, pb, rows_b, K, s);
+        const int64_t per_row = padded(K) / 16, chunks = (rows_a + rows_b) * per_row;
+        const PadParams pad{{a.a, a.b}, {pa, pb}, {rows_a * per_row, rows_b * per_row}, (int)K, (int)per_row};
+        const int64_t blocks = (chunks + 255) / 256 < (1 << 16) ? (chunks + 255) / 256 : 1 << 16;
+        pad_rows_kernel<<<dim3((unsigned)blocks), dim3(256), 0, s>>>(pad);
+        const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
         p.a = pa;
@@ -598,10 +658,6 @@ hipError_t launch_int8_matmul(const Int8MatmulArgs &a, hipStream_t s)
     p.tiles_m = (int)((a.M + kCosts[f].tm - 1) / kCosts[f].tm);
     p.tiles_n = (int)((a.N + kCosts[f].tn - 1) / kCosts[f].tn);
     p.tiles = tiles_of(kCosts[f], a.batch, a.M, a.N);
-    // An output that the 256 MB last-level cache cannot keep is stored past
-    // the caches: 1536 x 131072 x 768 takes 188 us so, 202 us without; at
-    // 168 MB of output the two are within 1 %, and a reader may find it cached.
-    p.stream_out = (double)a.batch * a.M * a.N * (a.bf16 ? 2 : 4) > 256e6;
     switch (f) {
     case kTile256: return tile<2, 4, 4, 2, 2>(p, kCus, a.bf16, s);
     case kTile128: return tile<2, 2, 2, 2, 2>(p, 2 * kCus, a.bf16, s);
