@@ -44,6 +44,7 @@ struct MatmulParams {
     int64_t a_batch, b_batch;  // rows between batches: 0 = shared
     int tiles_m, tiles_n;
     int64_t tiles;             // of all batches
+    bool stream_out;           // whole-line stores go past the caches
 };
 
 // Past the inner axis' end a lane loads these instead.
@@ -137,8 +138,8 @@ __device__ __forceinline__ Share xcd_share(int64_t tiles, int xcd)
 // Of a tile's end, 5 us of the model below, most is arithmetic (3.5
 // instructions an output) and the stores' way to memory: whole lines past the
 // caches, issued without branches, and not waited for by the next tile's first
-// step (8 x 5120 x 2048 x 2560: 212 us with cached, guarded, waited-for stores
-// and scales loaded there, 178 so).
+// step (8 x 5120 x 2048 x 2560: 178 us, by way of the caches 204; before also
+// guarded, waited for, and with the scales loaded there 212).
 template <int WM, int WN, int FM, int FN, int STAGES, bool BF16>
 __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const MatmulParams p)
 {
@@ -335,7 +336,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const MatmulParam
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 col_scale[j][e] = *(const f32x4 *)(st + (SA * 64 + j * 32 + e * 8 + half * 4) * 4);
-        auto finish = [&](auto full) {
+        auto finish = [&](auto full, auto stream) {
 #pragma unroll
             for (int j0 = 0; j0 < FN; j0 += kWide) {
                 const int64_t n = t.n0 + (wn * FN + j0) * 32 + (lane & 7) * kPerChunk;
@@ -366,11 +367,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const MatmulParam
                         const u32x4 v = *(const u32x4 *)(st + row * 128 + place(row, lane & 7) * 16);
                         typedef u32x4 __attribute__((aligned(2))) loose;  // rows start at any element
                         T *to = o + (int64_t)(i * 32 + r * 8) * p.N;
-                        if constexpr (full) {
+                        if constexpr (full && stream) {
                             __builtin_nontemporal_store(v, (loose *)to);
+                        } else if constexpr (full) {
+                            *(loose *)to = v;
                         } else if (m + i * 32 + r * 8 < p.M) {
                             if (n + kPerChunk <= p.N) {
-                                __builtin_nontemporal_store(v, (loose *)to);
+                                *(loose *)to = v;
                             } else {
 #pragma unroll
                                 for (int q = 0; q < kPerChunk; ++q)
@@ -387,10 +390,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const MatmulParam
             }
         };
         stores_known = t.m0 + TM <= p.M && t.n0 + TN <= p.N;
-        if (stores_known)
-            finish(std::true_type{});
+        if (stores_known && p.stream_out)
+            finish(std::true_type{}, std::true_type{});
+        else if (stores_known)
+            finish(std::true_type{}, std::false_type{});
         else
-            finish(std::false_type{});
+            finish(std::false_type{}, std::false_type{});
     }
 }
 
@@ -516,8 +521,10 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const PadParams p)
     const int64_t stride = (int64_t)gridDim.x * 256;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.chunks[0] + p.chunks[1]; i += stride) {
         const bool second = i >= p.chunks[0];
-        const int64_t chunk = second ? i - p.chunks[0] : i, row = chunk / p.per_row;
-        const int k = (int)(chunk % p.per_row) * 16;
+        const int64_t chunk = second ? i - p.chunks[0] : i;
+        // a 64-bit division costs several times a 32-bit one
+        const int64_t row = chunk >> 32 ? chunk / p.per_row : (uint32_t)chunk / (uint32_t)p.per_row;
+        const int k = (int)(chunk - row * p.per_row) * 16;
         const int8_t *from = (second ? p.src[1] : p.src[0]) + row * p.K + k;
         u32x4 v = {0, 0, 0, 0};
         if (k + 16 <= p.K) {
@@ -658,6 +665,11 @@ hipError_t launch_int8_matmul(const Int8MatmulArgs &a, hipStream_t s)
     p.tiles_m = (int)((a.M + kCosts[f].tm - 1) / kCosts[f].tm);
     p.tiles_n = (int)((a.N + kCosts[f].tn - 1) / kCosts[f].tn);
     p.tiles = tiles_of(kCosts[f], a.batch, a.M, a.N);
+    // Rows that start at 64-byte boundaries are stored past the caches in whole
+    // pieces of memory traffic (16384 x 5120 x 160: 40 us, 46 by the caches;
+    // 16384 x 5152: 47 and 53); others leave pieces that a cache has to join
+    // (16384 x 5128: 88 us past the caches, 56 by them; 5121: 99 and 58).
+    p.stream_out = (a.N * (a.bf16 ? 2 : 4)) % 64 == 0 && (uintptr_t)a.out % 64 == 0;
     switch (f) {
     case kTile256: return tile<2, 4, 4, 2, 2>(p, kCus, a.bf16, s);
     case kTile128: return tile<2, 2, 2, 2, 2>(p, 2 * kCus, a.bf16, s);

@@ -161,7 +161,7 @@ mamba_status mamba_quantize_int8(const void *x, int8_t *q, float *scale, int64_t
     mamba_status st = device_ok();
     if (st != MAMBA_OK)
         return st;
-    if (channel_major) {
+    if (channel_major && !(L == 1 && K <= mamba::kMaxNormWidth)) {  // of one token, both orders are the same
         mamba::QuantChannelArgs a{x, q, scale, B, L, K, io == MAMBA_BF16};
         return launched(mamba::launch_quantize_channel_major(a, (hipStream_t)stream));
     }

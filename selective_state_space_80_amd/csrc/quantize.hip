@@ -3,12 +3,14 @@
 // the token-major form:  scale = max_k|x| / 127,  q = rne(x * 127 / max_k|x|).
 //
 // A scale needs all K channels of its token before the first of them can be
-// written.  A workgroup of 1024 threads takes 64 bytes of tokens (32 bf16 or
-// 16 fp32) of one sequence and holds all their channels in registers, packed
-// as loaded, so the input is read once: 320 KB of the CU's 512 KB at K = 5120.
-// A thread has 16 bytes of tokens of four neighbouring channels per 1024
-// channels; the four bytes it makes of a token are one 4-byte store, and 16
-// lanes' stores are 64 neighbouring bytes: the transposition needs no LDS.
+// written.  A workgroup takes 64 bytes of tokens (32 bf16 or 16 fp32) of one
+// sequence and holds all their channels in registers, packed as loaded, so the
+// input is read once: 320 KB of the CU's 512 KB at K = 5120.  A thread has 16
+// bytes of tokens of four neighbouring channels per group of as many channels
+// as the workgroup has threads (up to 1024: one wave for 64 channels, five
+// groups of 1024 for 5120); the four bytes it makes of a token are one 4-byte
+// store, and 16 lanes' stores are 64 neighbouring bytes: the transposition
+// needs no LDS.
 //
 // Bound by memory: 8 x 5120 x 2048 bf16 (252 MB) takes 45 us (5.5 TB/s;
 // 70 before neighbouring tiles shared an XCD).
@@ -20,9 +22,8 @@
 namespace mamba {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kGroup = kThreads;  // channels a group of four loads a thread covers
-constexpr int kMaxHeld = 6;       // groups held in registers (96 of the 128 there are)
+constexpr int kMostThreads = 1024;
+constexpr int kMaxHeld = 6;  // groups held in registers (96 of the 128 there are)
 
 struct ChannelParams {
     const void *x;
@@ -78,18 +79,19 @@ template <bool BF16> __device__ __forceinline__ uint32_t max_abs(uint32_t top, u
     }
 }
 
-// HELD groups of 1024 channels stay in registers; 0: the channels are more
-// than that, and the second pass reads them again.
+// HELD groups of channels stay in registers; 0: they are more than that, and
+// the second pass reads them again.
 template <bool BF16, int HELD, bool SHORT>
-__global__ __launch_bounds__(kThreads) void quantize_channel_kernel(const ChannelParams p)
+__global__ __launch_bounds__(kMostThreads) void quantize_channel_kernel(const ChannelParams p)
 {
     using T = typename Elem<BF16>::T;
     using Tok = Tokens<BF16>;
     constexpr int kTok = Tok::kCount, kTile = 4 * kTok;
-    __shared__ uint32_t tops[kThreads / 64][4][4];
+    __shared__ uint32_t tops[kMostThreads / 64][4][4];
     __shared__ RowScale rows[kTile];
     __shared__ int special;  // a row is raised, or not finite
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n_waves = blockDim.x >> 6;
+    const int64_t group = blockDim.x;  // channels: a thread has four, four threads share them
     const int part = lane & 3;                    // which 16 bytes of the tokens
     const int64_t c0 = (int64_t)(threadIdx.x >> 2) * 4;  // first of the four channels
     // Neighbouring tiles read the two halves of the same cache lines: each of
@@ -103,7 +105,7 @@ __global__ __launch_bounds__(kThreads) void quantize_channel_kernel(const Channe
     const int short_l = (int)p.L;
     const T *x = (const T *)p.x + b * p.K * p.L + l;
     auto load = [&](int64_t c) { return load_tokens<BF16, SHORT>(x + (c < p.K ? c : p.K - 1) * p.L, short_l); };
-    const int64_t groups = (p.K + kGroup - 1) / kGroup;
+    const int64_t groups = (p.K + group - 1) / group;
 
     if (threadIdx.x == 0)
         special = 0;
@@ -114,7 +116,7 @@ __global__ __launch_bounds__(kThreads) void quantize_channel_kernel(const Channe
         for (int g = 0; g < HELD; ++g)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                held[g][r] = load(g * kGroup + c0 + r);
+                held[g][r] = load(g * group + c0 + r);
 #pragma unroll
         for (int g = 0; g < HELD; ++g)
 #pragma unroll
@@ -128,7 +130,7 @@ __global__ __launch_bounds__(kThreads) void quantize_channel_kernel(const Channe
             Tok t[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                t[r] = load(g * kGroup + c0 + r);
+                t[r] = load(g * group + c0 + r);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -150,8 +152,7 @@ __global__ __launch_bounds__(kThreads) void quantize_channel_kernel(const Channe
     if (threadIdx.x < kTile) {
         const int pt = threadIdx.x / kTok, i = threadIdx.x % kTok;
         uint32_t t = 0;
-#pragma unroll
-        for (int w = 0; w < kThreads / 64; ++w)
+        for (int w = 0; w < n_waves; ++w)
             t = max_abs<BF16>(t, tops[w][pt][BF16 ? i / 2 : i]);
         if constexpr (BF16)
             t = (i % 2 ? t >> 16 : t & 0xffffu) << 16;
@@ -207,14 +208,14 @@ __global__ __launch_bounds__(kThreads) void quantize_channel_kernel(const Channe
     if constexpr (HELD > 0) {
 #pragma unroll
         for (int g = 0; g < HELD; ++g)
-            put(held[g], g * kGroup + c0);
+            put(held[g], g * group + c0);
     } else {
         for (int64_t g = 0; g < groups; ++g) {
             Tok t[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                t[r] = load(g * kGroup + c0 + r);
-            put(t, g * kGroup + c0);
+                t[r] = load(g * group + c0 + r);
+            put(t, g * group + c0);
         }
     }
 }
@@ -224,12 +225,15 @@ template <bool BF16> hipError_t start(const QuantChannelArgs &a, hipStream_t s)
     constexpr int kTok = Tokens<BF16>::kCount;
     const int64_t tiles = (a.L + 4 * kTok - 1) / (4 * kTok);
     const ChannelParams p{a.x, a.q, a.scale, a.L, a.K, tiles};
-    const dim3 grid((unsigned)(a.B * tiles)), block(kThreads);
+    // as few groups as 1024 threads allow, then as few waves as those need
+    const int64_t groups = (a.K + kMostThreads - 1) / kMostThreads;
+    const int64_t per_group = (a.K + groups - 1) / groups;
+    const dim3 grid((unsigned)(a.B * tiles)), block((unsigned)((per_group + 63) / 64 * 64));
     if (a.L < kTok) {
         quantize_channel_kernel<BF16, 0, true><<<grid, block, 0, s>>>(p);
         return hipGetLastError();
     }
-    switch ((a.K + kGroup - 1) / kGroup) {
+    switch (groups) {
     case 1: quantize_channel_kernel<BF16, 1, false><<<grid, block, 0, s>>>(p); break;
     case 2: quantize_channel_kernel<BF16, 2, false><<<grid, block, 0, s>>>(p); break;
     case 3: quantize_channel_kernel<BF16, 3, false><<<grid, block, 0, s>>>(p); break;

@@ -28,7 +28,7 @@ struct BwdParams {
 // HF32: h (and the residual gradients) are fp32 while dy and dx are bf16.
 // DRES: dres_out is given.  WAVE_ROW as in the forward kernel.
 template <bool XBF, bool HF32, bool DRES, bool WAVE_ROW, int NC, bool TINY>
-__global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void rms_norm_bwd_kernel(const BwdParams p)
+__global__ __launch_bounds__(WAVE_ROW ? 256 : NC == 1 ? 512 : 1024) void rms_norm_bwd_kernel(const BwdParams p)
 {
     constexpr bool HBF = XBF && !HF32;
     using XT = typename Elem<XBF>::T;
@@ -55,16 +55,36 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void rms_norm_bwd_kernel(con
         for (int i = 0; i < 8; ++i)
             acc[j][i] = 0.f;
     }
+    // Where registers allow, the next row is loaded while this one is worked on
+    // (PERF).
+    constexpr bool kAhead = WAVE_ROW || NC == 1;
+    RawChunk<HBF> rh[NC], rd[NC];
+    RawChunk<XBF> rg[NC];
+    auto load_row = [&](int64_t row) {
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+            rh[j].template load<TINY>((const HT *)p.h + row * D, at[j], D);
+            rg[j].template load<TINY>((const XT *)p.dy + row * D, at[j], D);
+            if constexpr (DRES)
+                rd[j].template load<TINY>((const HT *)p.dres_out + row * D, at[j], D);
+        }
+    };
+    if (kAhead && first < p.M)
+        load_row(first);
     int parity = 0;
     for (int64_t row = first; row < p.M; row += step) {
+        if (!kAhead)
+            load_row(row);
         float h[NC][8], g[NC][8], d[NC][8];
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
-            load_chunk<HBF, TINY>((const HT *)p.h + row * D, at[j], D, h[j]);
-            load_chunk<XBF, TINY>((const XT *)p.dy + row * D, at[j], D, g[j]);
+            rh[j].get(h[j]);
+            rg[j].get(g[j]);
             if constexpr (DRES)
-                load_chunk<HBF, TINY>((const HT *)p.dres_out + row * D, at[j], D, d[j]);
+                rd[j].get(d[j]);
         }
+        if (kAhead && row + step < p.M)
+            load_row(row + step);
         float s = 0.f, t = 0.f;
 #pragma unroll
         for (int j = 0; j < NC; ++j) {

@@ -178,6 +178,38 @@ __device__ __forceinline__ void load_chunk(const typename Elem<BF16>::T *row, co
         load8<BF16>(row + at.off, v);
     }
 }
+// A chunk as it lies in memory, to be unpacked later.
+template <bool BF16> struct RawChunk {
+    u32x4 v[BF16 ? 1 : 2];
+    template <bool TINY>
+    __device__ __forceinline__ void load(const typename Elem<BF16>::T *row, const ChunkAt &at, int D)
+    {
+        if constexpr (TINY) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const typename Elem<BF16>::T e = row[i < D ? i : D - 1];
+                if constexpr (BF16)
+                    v[0][i / 2] = i % 2 ? v[0][i / 2] | (uint32_t)e << 16 : (uint32_t)e;
+                else
+                    v[i / 4][i % 4] = __float_as_uint(e);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < (BF16 ? 1 : 2); ++i)
+                __builtin_memcpy(&v[i], row + at.off + 4 * i, 16);
+        }
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (BF16)
+                f[i] = __uint_as_float(i % 2 ? v[0][i / 2] & 0xffff0000u : v[0][i / 2] << 16);
+            else
+                f[i] = __uint_as_float(v[i / 4][i % 4]);
+        }
+    }
+};
 template <bool BF16, bool TINY>
 __device__ __forceinline__ void store_chunk(typename Elem<BF16>::T *row, const ChunkAt &at, int D,
                                             const float (&v)[8])
