@@ -12,8 +12,11 @@
 // store, and 16 lanes' stores are 64 neighbouring bytes: the transposition
 // needs no LDS.
 //
-// Bound by memory: 8 x 5120 x 2048 bf16 (252 MB) takes 45 us (5.5 TB/s;
-// 70 before neighbouring tiles shared an XCD).
+// Bound by memory.  8 x 5120 x 2048 bf16 (252 MB) takes 45 us (5.5 TB/s) with
+// the input in the last-level cache, where a scan has just left it, and 73 us
+// from memory: there is room for one workgroup a CU, so its loads do not
+// overlap its stores (64 without the stores, 70 and 99 us before neighbouring
+// tiles shared an XCD's L2).  1 x 1536 x 131072 bf16 (604 MB) takes 143 us.
 #include <hip/hip_runtime.h>
 
 #include "quant.h"
@@ -23,6 +26,7 @@ namespace mamba {
 namespace {
 
 constexpr int kMostThreads = 1024;
+constexpr int kChan = 4;     // neighbouring channels of a thread
 constexpr int kMaxHeld = 6;  // groups held in registers (96 of the 128 there are)
 
 struct ChannelParams {
@@ -45,18 +49,19 @@ template <bool BF16> struct Tokens {
     }
 };
 
-// Sequences shorter than 16 bytes (SHORT) are read token by token, the index
-// held below L; otherwise the last 16 bytes are moved back to end with L.
+// Sequences shorter than 16 bytes, and fewer than four channels (SHORT), are
+// read token by token, the index held below the `left` there are; otherwise the
+// last 16 bytes are moved back to end with the sequence.
 template <bool BF16, bool SHORT>
-__device__ __forceinline__ Tokens<BF16> load_tokens(const typename Elem<BF16>::T *channel, int L)
+__device__ __forceinline__ Tokens<BF16> load_tokens(const typename Elem<BF16>::T *channel, int left)
 {
     Tokens<BF16> t;
     if constexpr (SHORT) {
         t.v = u32x4{0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < Tokens<BF16>::kCount; ++i) {
-            const uint32_t e = BF16 ? (uint32_t)((const uint16_t *)channel)[i < L ? i : L - 1]
-                                    : ((const uint32_t *)channel)[i < L ? i : L - 1];
+            const uint32_t e = BF16 ? (uint32_t)((const uint16_t *)channel)[i < left ? i : left - 1]
+                                    : ((const uint32_t *)channel)[i < left ? i : left - 1];
             t.v[BF16 ? i / 2 : i] |= BF16 && i % 2 ? e << 16 : e;
         }
     } else {
@@ -81,42 +86,59 @@ template <bool BF16> __device__ __forceinline__ uint32_t max_abs(uint32_t top, u
 
 // HELD groups of channels stay in registers; 0: they are more than that, and
 // the second pass reads them again.
-template <bool BF16, int HELD, bool SHORT>
-__global__ __launch_bounds__(kMostThreads) void quantize_channel_kernel(const ChannelParams p)
+template <bool BF16, int PARTS, int HELD, bool SHORT>
+__global__ __launch_bounds__(kMostThreads / 4 * PARTS) void quantize_channel_kernel(const ChannelParams p)
 {
     using T = typename Elem<BF16>::T;
     using Tok = Tokens<BF16>;
-    constexpr int kTok = Tok::kCount, kTile = 4 * kTok;
-    __shared__ uint32_t tops[kMostThreads / 64][4][4];
+    constexpr int kTok = Tok::kCount, kTile = PARTS * kTok;
+    __shared__ uint32_t tops[kMostThreads / 256 * PARTS][PARTS][4];
     __shared__ RowScale rows[kTile];
     __shared__ int special;  // a row is raised, or not finite
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n_waves = blockDim.x >> 6;
-    const int64_t group = blockDim.x;  // channels: a thread has four, four threads share them
-    const int part = lane & 3;                    // which 16 bytes of the tokens
-    const int64_t c0 = (int64_t)(threadIdx.x >> 2) * 4;  // first of the four channels
+    const int64_t group = blockDim.x / PARTS * kChan;  // channels
+    const int part = lane & (PARTS - 1);          // which 16 bytes of the tokens
+    const int64_t c0 = (int64_t)(threadIdx.x / PARTS) * kChan;  // first of its channels
     // Neighbouring tiles read the two halves of the same cache lines: each of
     // the 8 XCDs (workgroups go to them in turn) takes a contiguous share.
     const int64_t all = gridDim.x, xcd = blockIdx.x % 8, more = all % 8;
     const int64_t tile = xcd * (all / 8) + (xcd < more ? xcd : more) + blockIdx.x / 8;
     const int64_t b = tile / p.tiles, l0 = (tile % p.tiles) * kTile;
     const int64_t to = l0 + part * kTok;
-    const int64_t l = SHORT ? 0 : (to + kTok <= p.L ? to : p.L - kTok);
+    const int64_t l = SHORT ? (to < p.L ? to : p.L - 1) : (to + kTok <= p.L ? to : p.L - kTok);
     const bool live = to < p.L;
-    const int short_l = (int)p.L;
+    const int left = SHORT ? (int)(p.L - l < kTok ? p.L - l : kTok) : kTok;  // tokens there are
     const T *x = (const T *)p.x + b * p.K * p.L + l;
-    auto load = [&](int64_t c) { return load_tokens<BF16, SHORT>(x + (c < p.K ? c : p.K - 1) * p.L, short_l); };
+    // The four channels of a thread and group; the last ones are moved back to
+    // end with K (threads then make the same bytes twice).  Below four channels
+    // (SHORT) they repeat the last.
+    auto channel = [&](int64_t g) {
+        const int64_t c = g * group + c0;
+        return SHORT || c + kChan <= p.K ? c : p.K - kChan;
+    };
+    auto load4 = [&](Tok(&t)[kChan], int64_t g) {
+        const int64_t c = channel(g);
+        if constexpr (SHORT) {
+#pragma unroll
+            for (int r = 0; r < kChan; ++r)
+                t[r] = load_tokens<BF16, true>(x + (c + r < p.K ? c + r : p.K - 1) * p.L, left);
+        } else {
+            const T *from = x + c * p.L;
+#pragma unroll
+            for (int r = 0; r < kChan; ++r, from += p.L)
+                t[r] = load_tokens<BF16, false>(from, left);
+        }
+    };
     const int64_t groups = (p.K + group - 1) / group;
 
     if (threadIdx.x == 0)
         special = 0;
-    Tok held[HELD ? HELD : 1][4];
+    Tok held[HELD ? HELD : 1][kChan];
     u32x4 top = {0, 0, 0, 0};
     if constexpr (HELD > 0) {
 #pragma unroll
         for (int g = 0; g < HELD; ++g)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                held[g][r] = load(g * group + c0 + r);
+            load4(held[g], g);
 #pragma unroll
         for (int g = 0; g < HELD; ++g)
 #pragma unroll
@@ -127,10 +149,8 @@ __global__ __launch_bounds__(kMostThreads) void quantize_channel_kernel(const Ch
     } else {
 #pragma unroll 2
         for (int64_t g = 0; g < groups; ++g) {
-            Tok t[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                t[r] = load(g * group + c0 + r);
+            Tok t[kChan];
+            load4(t, g);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -141,11 +161,13 @@ __global__ __launch_bounds__(kMostThreads) void quantize_channel_kernel(const Ch
     // over the lanes of the same tokens (lane % 4), then over the waves
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        top[i] = max_abs<BF16>(top[i], dpp<0x124>(top[i]));  // row rotated by 4
+        if constexpr (PARTS == 2)
+            top[i] = max_abs<BF16>(top[i], dpp<0x122>(top[i]));  // row rotated by 2
+        top[i] = max_abs<BF16>(top[i], dpp<0x124>(top[i]));  // by 4
         top[i] = max_abs<BF16>(top[i], dpp<0x128>(top[i]));  // by 8
         top[i] = max_abs<BF16>(top[i], (uint32_t)__shfl_xor((int)top[i], 16));
         top[i] = max_abs<BF16>(top[i], (uint32_t)__shfl_xor((int)top[i], 32));
-        if (lane < 4)
+        if (lane < PARTS)
             tops[wave][part][i] = top[i];
     }
     __syncthreads();
@@ -161,7 +183,7 @@ __global__ __launch_bounds__(kMostThreads) void quantize_channel_kernel(const Ch
         if (rs.raise != 1.f || rs.mask == 0)
             atomicOr(&special, 1);
         const int64_t from = l0 + pt * kTok;
-        const int64_t tok = SHORT ? i : (from + kTok <= p.L ? from : p.L - kTok) + i;
+        const int64_t tok = (SHORT || from + kTok <= p.L ? from : p.L - kTok) + i;
         if (from < p.L && tok < p.L)
             p.scale[b * p.L + tok] = rs.scale;
     }
@@ -174,12 +196,13 @@ __global__ __launch_bounds__(kMostThreads) void quantize_channel_kernel(const Ch
         mul[i] = rows[part * kTok + i].mul;
     const bool any_special = special != 0;
     int8_t *q = p.q + (b * p.L + l) * p.K;
-    auto put = [&](const Tok(&t)[4], int64_t c) {
-        if (c >= p.K)
+    auto put = [&](const Tok(&t)[kChan], int64_t g) {
+        const int64_t c = channel(g);
+        if (SHORT && c >= p.K)
             return;
 #pragma unroll
         for (int i = 0; i < kTok; ++i) {
-            if (SHORT && i >= short_l)
+            if (SHORT && i >= left)
                 continue;
             uint32_t byte[4];
 #pragma unroll
@@ -195,7 +218,7 @@ __global__ __launch_bounds__(kMostThreads) void quantize_channel_kernel(const Ch
             if (any_special)
                 w &= rows[part * kTok + i].mask;
             int8_t *o = q + i * p.K + c;
-            if (c + 4 <= p.K) {
+            if (!SHORT || c + kChan <= p.K) {
                 __builtin_memcpy(o, &w, 4);
             } else {
 #pragma unroll
@@ -208,39 +231,37 @@ __global__ __launch_bounds__(kMostThreads) void quantize_channel_kernel(const Ch
     if constexpr (HELD > 0) {
 #pragma unroll
         for (int g = 0; g < HELD; ++g)
-            put(held[g], g * group + c0);
+            put(held[g], g);
     } else {
         for (int64_t g = 0; g < groups; ++g) {
-            Tok t[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                t[r] = load(g * group + c0 + r);
-            put(t, g * group + c0);
+            Tok t[kChan];
+            load4(t, g);
+            put(t, g);
         }
     }
 }
 
-template <bool BF16> hipError_t start(const QuantChannelArgs &a, hipStream_t s)
+template <bool BF16, int PARTS> hipError_t start(const QuantChannelArgs &a, hipStream_t s)
 {
-    constexpr int kTok = Tokens<BF16>::kCount;
-    const int64_t tiles = (a.L + 4 * kTok - 1) / (4 * kTok);
+    constexpr int kTok = Tokens<BF16>::kCount, kMostGroup = kMostThreads;
+    const int64_t tiles = (a.L + PARTS * kTok - 1) / (PARTS * kTok);
     const ChannelParams p{a.x, a.q, a.scale, a.L, a.K, tiles};
-    // as few groups as 1024 threads allow, then as few waves as those need
-    const int64_t groups = (a.K + kMostThreads - 1) / kMostThreads;
-    const int64_t per_group = (a.K + groups - 1) / groups;
-    const dim3 grid((unsigned)(a.B * tiles)), block((unsigned)((per_group + 63) / 64 * 64));
-    if (a.L < kTok) {
-        quantize_channel_kernel<BF16, 0, true><<<grid, block, 0, s>>>(p);
+    // as few groups as there can be, then as few waves as those need
+    const int64_t groups = (a.K + kMostGroup - 1) / kMostGroup;
+    const int64_t threads = (a.K + groups * kChan - 1) / (groups * kChan) * PARTS;
+    const dim3 grid((unsigned)(a.B * tiles)), block((unsigned)((threads + 63) / 64 * 64));
+    if (a.L < kTok || a.K < kChan) {
+        quantize_channel_kernel<BF16, PARTS, 0, true><<<grid, block, 0, s>>>(p);
         return hipGetLastError();
     }
     switch (groups) {
-    case 1: quantize_channel_kernel<BF16, 1, false><<<grid, block, 0, s>>>(p); break;
-    case 2: quantize_channel_kernel<BF16, 2, false><<<grid, block, 0, s>>>(p); break;
-    case 3: quantize_channel_kernel<BF16, 3, false><<<grid, block, 0, s>>>(p); break;
-    case 4: quantize_channel_kernel<BF16, 4, false><<<grid, block, 0, s>>>(p); break;
-    case 5: quantize_channel_kernel<BF16, 5, false><<<grid, block, 0, s>>>(p); break;
-    case kMaxHeld: quantize_channel_kernel<BF16, kMaxHeld, false><<<grid, block, 0, s>>>(p); break;
-    default: quantize_channel_kernel<BF16, 0, false><<<grid, block, 0, s>>>(p); break;
+    case 1: quantize_channel_kernel<BF16, PARTS, 1, false><<<grid, block, 0, s>>>(p); break;
+    case 2: quantize_channel_kernel<BF16, PARTS, 2, false><<<grid, block, 0, s>>>(p); break;
+    case 3: quantize_channel_kernel<BF16, PARTS, 3, false><<<grid, block, 0, s>>>(p); break;
+    case 4: quantize_channel_kernel<BF16, PARTS, 4, false><<<grid, block, 0, s>>>(p); break;
+    case 5: quantize_channel_kernel<BF16, PARTS, 5, false><<<grid, block, 0, s>>>(p); break;
+    case kMaxHeld: quantize_channel_kernel<BF16, PARTS, kMaxHeld, false><<<grid, block, 0, s>>>(p); break;
+    default: quantize_channel_kernel<BF16, PARTS, 0, false><<<grid, block, 0, s>>>(p); break;
     }
     return hipGetLastError();
 }
@@ -249,7 +270,13 @@ template <bool BF16> hipError_t start(const QuantChannelArgs &a, hipStream_t s)
 
 hipError_t launch_quantize_channel_major(const QuantChannelArgs &a, hipStream_t s)
 {
-    return a.bf16 ? start<true>(a, s) : start<false>(a, s);
+    // With fewer tiles than half the CUs, tiles of half the tokens by half the
+    // threads: 1 x 5120 x 1000 bf16 13.9 us instead of 16.6, 64 x 5120 x 8 8.1
+    // instead of 10.0; the other way 8 x 5120 x 2048 73 instead of 80.
+    const int64_t per_tile = 4 * (a.bf16 ? Tokens<true>::kCount : Tokens<false>::kCount);
+    if (a.B * ((a.L + per_tile - 1) / per_tile) < 128)
+        return a.bf16 ? start<true, 2>(a, s) : start<false, 2>(a, s);
+    return a.bf16 ? start<true, 4>(a, s) : start<false, 4>(a, s);
 }
 
 }  // namespace mamba

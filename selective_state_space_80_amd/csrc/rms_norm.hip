@@ -10,6 +10,12 @@
 // Every element is read once and written once: a row stays in the registers of
 // the lanes that loaded it (8-element chunks, 16 or 32 bytes a lane), the row's
 // sum (and largest value) crosses lanes by DPP and waves through LDS.
+//
+// Bound by memory: 16384 x 768 in fp32 with an fp32 residual (201 MB) takes
+// 39 us (5.1 TB/s, the rate of a large copy); 16384 x 2560 bf16 with a bf16
+// residual 59 us, with 8-bit output 46 us (5.7 and 6.4 TB/s, the inputs partly
+// in the last-level cache); 131072 rows of 64 bf16 11 us (26 with a wave to
+// each).  One row of 2560 is bound by its launch.
 #include <hip/hip_runtime.h>
 
 #include "quant.h"
@@ -31,23 +37,30 @@ struct NormParams {
     float eps, inv_d;
 };
 
-// RES: 0 no residual, 1 fp32, 2 bf16.  WAVE_ROW: each of a workgroup's four
-// waves has a row of its own; otherwise the workgroup (any number of waves)
-// has one row.  NC chunks a lane.
-template <bool XBF, int RES, int MODE, bool WAVE_ROW, int NC, bool TINY>
-__global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void rms_norm_kernel(const NormParams p)
+// RES: 0 no residual, 1 fp32, 2 bf16.  LANES > 0: every LANES lanes of a
+// workgroup's four waves have a row of their own; 0: the workgroup (any number
+// of waves) has one row.  NC chunks a lane.
+template <bool XBF, int RES, int MODE, int LANES, int NC, bool TINY>
+__global__ __launch_bounds__(LANES ? 256 : 1024) void rms_norm_kernel(const NormParams p)
 {
     using XT = typename Elem<XBF>::T;
     using RT = typename Elem<RES == 2>::T;
     __shared__ float red[2][16];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n_waves = WAVE_ROW ? 1 : (int)(blockDim.x >> 6);
-    const int64_t row = WAVE_ROW ? (int64_t)blockIdx.x * 4 + wave : (int64_t)blockIdx.x;
-    if (WAVE_ROW && row >= p.M)
+    constexpr int kRows = LANES ? 64 / LANES : 1;  // of a wave
+    const int n_waves = LANES ? 1 : (int)(blockDim.x >> 6);
+    int64_t row = LANES ? ((int64_t)blockIdx.x * 4 + wave) * kRows : (int64_t)blockIdx.x;
+    if (LANES && row >= p.M)
         return;  // the whole wave; no barrier follows in this form
-    const int tid = WAVE_ROW ? lane : (int)threadIdx.x;
-    const int T = WAVE_ROW ? 64 : (int)blockDim.x;
+    bool past = false;  // lanes of rows past the last repeat it and store nothing
+    if constexpr (kRows > 1) {
+        row += lane / LANES;
+        past = row >= p.M;
+        row = past ? p.M - 1 : row;
+    }
+    const int tid = LANES ? lane % LANES : (int)threadIdx.x;
+    const int T = LANES ? LANES : (int)blockDim.x;
     const int D = p.D;
     const bool ragged = D % kChunk != 0;
 
@@ -57,6 +70,8 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void rms_norm_kernel(const N
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
         at[j] = chunk_at<TINY>(tid + j * T, D);
+        if (past)
+            at[j].live = false;
         load_chunk<XBF, TINY>(xr, at[j], D, h[j]);
     }
     if constexpr (RES != 0) {
@@ -80,8 +95,8 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void rms_norm_kernel(const N
 #pragma unroll
         for (int j = 0; j < NC; ++j)
             s += own_sum<TINY>(at[j], D, ragged, [&](int i) { return h[j][i] * h[j][i]; });
-        s = wave_sum(s);
-        if constexpr (!WAVE_ROW) {
+        s = lane_sum<LANES ? LANES : 64>(s);
+        if constexpr (!LANES) {
             if (lane == 0)
                 red[0][wave] = s;
             __syncthreads();
@@ -117,8 +132,8 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void rms_norm_kernel(const N
 #pragma unroll
             for (int i = 0; i < 8; ++i)  // lanes without a chunk hold the row's first: no mask
                 top = umax(top, abs_bits(h[j][i]));
-        top = wave_max(top);
-        if constexpr (!WAVE_ROW) {
+        top = lane_max<LANES ? LANES : 64>(top);
+        if constexpr (!LANES) {
             if (lane == 0)
                 red[1][wave] = __uint_as_float(top);
             __syncthreads();
@@ -126,7 +141,7 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void rms_norm_kernel(const N
                 top = umax(top, __float_as_uint(red[1][k]));
         }
         const RowScale rs = row_scale(top);
-        if (tid == 0)
+        if (tid == 0 && !past)
             p.scale[row] = rs.scale;
         if (rs.raise != 1.f) {
 #pragma unroll
@@ -153,39 +168,47 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : 1024) void rms_norm_kernel(const N
     }
 }
 
-template <bool XBF, int RES, int MODE, bool WAVE_ROW, int NC, bool TINY>
+template <bool XBF, int RES, int MODE, int LANES, int NC, bool TINY>
 hipError_t start(const NormParams &p, int threads, hipStream_t s)
 {
-    const int64_t blocks = WAVE_ROW ? (p.M + 3) / 4 : p.M;
-    rms_norm_kernel<XBF, RES, MODE, WAVE_ROW, NC, TINY><<<dim3((unsigned)blocks), dim3(threads), 0, s>>>(p);
+    constexpr int kRows = LANES ? 4 * (64 / LANES) : 1;
+    const int64_t blocks = (p.M + kRows - 1) / kRows;
+    rms_norm_kernel<XBF, RES, MODE, LANES, NC, TINY><<<dim3((unsigned)blocks), dim3(threads), 0, s>>>(p);
     return hipGetLastError();
 }
 
 template <bool XBF, int RES, int MODE> hipError_t pick(const NormParams &p, hipStream_t s)
 {
     if (p.D < kChunk)
-        return start<XBF, RES, MODE, true, 1, true>(p, 256, s);
+        return start<XBF, RES, MODE, 8, 1, true>(p, 256, s);
+    switch (row_lanes(p.D)) {
+    case 8: return start<XBF, RES, MODE, 8, 1, false>(p, 256, s);
+    case 16: return start<XBF, RES, MODE, 16, 1, false>(p, 256, s);
+    case 32: return start<XBF, RES, MODE, 32, 1, false>(p, 256, s);
+    }
+    // A wave holds up to 8 chunks a lane (4096 elements); with fewer rows than
+    // fill the card with waves, a workgroup shares a row instead (8-bit
+    // output, in us: 64 x 2560 3.1 so, 3.7 a wave to each; 16384 x 2560 54 and 46).
     const int chunks = (p.D + kChunk - 1) / kChunk;
-    // A wave holds up to 8 chunks a lane (4096 elements).
     const int per_lane = (chunks + 63) / 64;
     if (per_lane <= 1 || (per_lane <= 8 && p.M >= 1024)) {
         switch (per_lane) {
-        case 1: return start<XBF, RES, MODE, true, 1, false>(p, 256, s);
-        case 2: return start<XBF, RES, MODE, true, 2, false>(p, 256, s);
-        case 3: return start<XBF, RES, MODE, true, 3, false>(p, 256, s);
-        case 4: return start<XBF, RES, MODE, true, 4, false>(p, 256, s);
-        case 5: return start<XBF, RES, MODE, true, 5, false>(p, 256, s);
-        default: return start<XBF, RES, MODE, true, 8, false>(p, 256, s);
+        case 1: return start<XBF, RES, MODE, 64, 1, false>(p, 256, s);
+        case 2: return start<XBF, RES, MODE, 64, 2, false>(p, 256, s);
+        case 3: return start<XBF, RES, MODE, 64, 3, false>(p, 256, s);
+        case 4: return start<XBF, RES, MODE, 64, 4, false>(p, 256, s);
+        case 5: return start<XBF, RES, MODE, 64, 5, false>(p, 256, s);
+        default: return start<XBF, RES, MODE, 64, 8, false>(p, 256, s);
         }
     }
     const int nc = chunks <= 512 ? 1 : chunks <= 2048 ? 2 : 4;
     const int lanes = (chunks + nc - 1) / nc;
     const int threads = (lanes + 63) / 64 * 64;
     if (nc == 1)
-        return start<XBF, RES, MODE, false, 1, false>(p, threads, s);
+        return start<XBF, RES, MODE, 0, 1, false>(p, threads, s);
     if (nc == 2)
-        return start<XBF, RES, MODE, false, 2, false>(p, threads, s);
-    return start<XBF, RES, MODE, false, 4, false>(p, threads, s);
+        return start<XBF, RES, MODE, 0, 2, false>(p, threads, s);
+    return start<XBF, RES, MODE, 0, 4, false>(p, threads, s);
 }
 
 }  // namespace

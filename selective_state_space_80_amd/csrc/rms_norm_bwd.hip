@@ -7,6 +7,10 @@
 // them together; dh follows from the registers.  dw is summed over the rows a
 // workgroup takes in its registers, written once per workgroup, and summed
 // over the workgroups in a fixed order by a second kernel.
+//
+// Bound by memory: 16384 x 2560, dy and dx bf16, h and both residual gradients
+// fp32 (671 MB), takes 129 us (5.2 TB/s, the rate of a large copy);
+// 16384 x 768 in fp32 (201 MB) 38 us; 1044 x 2339 is bound by its two launches.
 #include <hip/hip_runtime.h>
 
 #include "quant.h"
@@ -26,46 +30,54 @@ struct BwdParams {
 };
 
 // HF32: h (and the residual gradients) are fp32 while dy and dx are bf16.
-// DRES: dres_out is given.  WAVE_ROW as in the forward kernel.
-template <bool XBF, bool HF32, bool DRES, bool WAVE_ROW, int NC, bool TINY>
-__global__ __launch_bounds__(WAVE_ROW ? 256 : NC == 1 ? 512 : 1024) void rms_norm_bwd_kernel(const BwdParams p)
+// DRES: dres_out is given.  LANES as in the forward kernel.
+template <bool XBF, bool HF32, bool DRES, int LANES, int NC, bool TINY>
+__global__ __launch_bounds__(LANES ? 256 : NC == 1 ? 512 : 1024) void rms_norm_bwd_kernel(const BwdParams p)
 {
     constexpr bool HBF = XBF && !HF32;
     using XT = typename Elem<XBF>::T;
     using HT = typename Elem<HBF>::T;
     __shared__ float red[2][2][16];
-    __shared__ float dw_red[WAVE_ROW ? 4 : 1][WAVE_ROW ? NC * 512 : 1];
+    __shared__ float dw_red[LANES ? 4 : 1][LANES ? NC * 512 : 1];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n_waves = WAVE_ROW ? 1 : (int)(blockDim.x >> 6);
-    const int tid = WAVE_ROW ? lane : (int)threadIdx.x;
-    const int T = WAVE_ROW ? 64 : (int)blockDim.x;
+    constexpr int kRows = LANES ? 64 / LANES : 1;  // of a wave
+    const int n_waves = LANES ? 1 : (int)(blockDim.x >> 6);
+    const int tid = LANES ? lane % LANES : (int)threadIdx.x;
+    const int T = LANES ? LANES : (int)blockDim.x;
     const int D = p.D;
     const bool ragged = D % kChunk != 0;
-    const int64_t step = WAVE_ROW ? (int64_t)gridDim.x * 4 : (int64_t)gridDim.x;
-    const int64_t first = WAVE_ROW ? (int64_t)blockIdx.x * 4 + wave : (int64_t)blockIdx.x;
+    const int64_t step = LANES ? (int64_t)gridDim.x * 4 * kRows : (int64_t)gridDim.x;
+    const int64_t first = LANES ? ((int64_t)blockIdx.x * 4 + wave) * kRows : (int64_t)blockIdx.x;
+    const int sub = kRows > 1 ? lane / LANES : 0;  // its row of the wave's
 
     ChunkAt at[NC];
-    float w[NC][8], acc[NC][8];
+    // Four chunks a lane leave no registers for the weight, which is then read
+    // again for each row, nor for dres_out before it is needed (2048 x 20000,
+    // bf16 with fp32 h: 157 us; with all of it in registers, spilling, 259).
+    constexpr bool kLean = NC == 4;
+    float w[kLean ? 1 : NC][8], acc[NC][8];
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
         at[j] = chunk_at<TINY>(tid + j * T, D);
-        load_chunk<false, TINY>(p.w, at[j], D, w[j]);
+        if constexpr (!kLean)
+            load_chunk<false, TINY>(p.w, at[j], D, w[j]);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             acc[j][i] = 0.f;
     }
-    // Where registers allow, the next row is loaded while this one is worked on
-    // (PERF).
-    constexpr bool kAhead = WAVE_ROW || NC == 1;
-    RawChunk<HBF> rh[NC], rd[NC];
+    // Where registers allow, the next row is loaded while this one is worked on.
+    constexpr bool kAhead = LANES != 0 || NC == 1;
+    RawChunk<HBF> rh[NC], rd[kLean ? 1 : NC];
     RawChunk<XBF> rg[NC];
     auto load_row = [&](int64_t row) {
+        if constexpr (kRows > 1)  // lanes of rows past the last repeat it
+            row = row + sub < p.M ? row + sub : p.M - 1;
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
             rh[j].template load<TINY>((const HT *)p.h + row * D, at[j], D);
             rg[j].template load<TINY>((const XT *)p.dy + row * D, at[j], D);
-            if constexpr (DRES)
+            if constexpr (DRES && !kLean)
                 rd[j].template load<TINY>((const HT *)p.dres_out + row * D, at[j], D);
         }
     };
@@ -75,25 +87,42 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : NC == 1 ? 512 : 1024) void rms_nor
     for (int64_t row = first; row < p.M; row += step) {
         if (!kAhead)
             load_row(row);
-        float h[NC][8], g[NC][8], d[NC][8];
+        float h[kLean ? 1 : NC][8], g[kLean ? 1 : NC][8], d[kLean ? 1 : NC][8];
+        if constexpr (!kLean) {
 #pragma unroll
-        for (int j = 0; j < NC; ++j) {
-            rh[j].get(h[j]);
-            rg[j].get(g[j]);
-            if constexpr (DRES)
-                rd[j].get(d[j]);
+            for (int j = 0; j < NC; ++j) {
+                rh[j].get(h[j]);
+                rg[j].get(g[j]);
+                if constexpr (DRES)
+                    rd[j].get(d[j]);
+            }
         }
+        // What a lean lane needs of chunk j.  The empty statement keeps the
+        // compiler from carrying the results of one use to the next in registers.
+        const float *weight = p.w;
+        auto unpack = [&](int j) {
+            if constexpr (kLean) {
+                asm volatile("" : "+s"(weight));
+                rh[j].keep();
+                rg[j].keep();
+                rh[j].get(h[0]);
+                rg[j].get(g[0]);
+                load_chunk<false, TINY>(weight, at[j], D, w[0]);
+            }
+        };
         if (kAhead && row + step < p.M)
             load_row(row + step);
         float s = 0.f, t = 0.f;
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
-            s += own_sum<TINY>(at[j], D, ragged, [&](int i) { return h[j][i] * h[j][i]; });
-            t += own_sum<TINY>(at[j], D, ragged, [&](int i) { return g[j][i] * w[j][i] * h[j][i]; });
+            const int k = kLean ? 0 : j;
+            unpack(j);
+            s += own_sum<TINY>(at[j], D, ragged, [&](int i) { return h[k][i] * h[k][i]; });
+            t += own_sum<TINY>(at[j], D, ragged, [&](int i) { return g[k][i] * w[k][i] * h[k][i]; });
         }
-        s = wave_sum(s);
-        t = wave_sum(t);
-        if constexpr (!WAVE_ROW) {
+        s = lane_sum<LANES ? LANES : 64>(s);
+        t = lane_sum<LANES ? LANES : 64>(t);
+        if constexpr (!LANES) {
             // two sets of slots in turn: a wave writes the next row's while
             // others still read this row's
             if (lane == 0) {
@@ -111,40 +140,51 @@ __global__ __launch_bounds__(WAVE_ROW ? 256 : NC == 1 ? 512 : 1024) void rms_nor
         }
         const float r = 1.f / sqrtf(fmaf(s, p.inv_d, p.eps));
         const float k3 = r * r * r * (t * p.inv_d);
+        const bool past = kRows > 1 && row + sub >= p.M;
+        const int64_t mine = kRows > 1 ? row + sub : row;
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
+            if (past)
+                continue;
+            const int k = kLean ? 0 : j;
+            unpack(j);
+            if constexpr (kLean && DRES)
+                load_chunk<HBF, TINY>((const HT *)p.dres_out + mine * D, at[j], D, d[0]);
             float dh[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                acc[j][i] = fmaf(g[j][i] * r, h[j][i], acc[j][i]);
-                dh[i] = fmaf(r * w[j][i], g[j][i], -k3 * h[j][i]);
+                acc[j][i] = fmaf(g[k][i] * r, h[k][i], acc[j][i]);
+                dh[i] = fmaf(r * w[k][i], g[k][i], -k3 * h[k][i]);
                 if constexpr (DRES)
-                    dh[i] += d[j][i];
+                    dh[i] += d[k][i];
             }
-            store_chunk<XBF, TINY>((XT *)p.dx + row * D, at[j], D, dh);
+            store_chunk<XBF, TINY>((XT *)p.dx + mine * D, at[j], D, dh);
             if constexpr (HF32) {
                 if (p.dres)
-                    store_chunk<false, TINY>((float *)p.dres + row * D, at[j], D, dh);
+                    store_chunk<false, TINY>((float *)p.dres + mine * D, at[j], D, dh);
             }
         }
     }
     float *part = p.partials + (int64_t)blockIdx.x * D;
     const int end = TINY ? D : kChunk;
-    if constexpr (WAVE_ROW) {
+    if constexpr (LANES != 0) {
 #pragma unroll
         for (int j = 0; j < NC; ++j)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 dw_red[wave][(j * 64 + lane) * 8 + i] = acc[j][i];
         __syncthreads();
-        if (wave != 0)
+        if (wave != 0 || sub != 0)
             return;
 #pragma unroll
         for (int j = 0; j < NC; ++j)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int k = (j * 64 + lane) * 8 + i;
-                acc[j][i] = ((dw_red[0][k] + dw_red[1][k]) + dw_red[2][k]) + dw_red[3][k];
+                float sum = 0.f;
+#pragma unroll
+                for (int r = 0; r < 4 * kRows; ++r)
+                    sum += dw_red[r / kRows][(j * 64 + r % kRows * LANES + lane) * 8 + i];
+                acc[j][i] = sum;
             }
     }
 #pragma unroll
@@ -184,16 +224,20 @@ __global__ __launch_bounds__(1024) void dweight_sum_kernel(const float *partials
     }
 }
 
-// Workgroups: enough of them to fill 256 CUs, at least 8 rows each where there
-// are so many, so that the partial rows stay a small part of the traffic.
-constexpr int64_t kMaxGroups = 1024;
+// Workgroups: at least 8 rows each where there are so many, and not more than
+// the card runs at once, so that the partial rows stay a small part of the
+// traffic.  Two a CU, four of the light ones of short rows: 8192 x 5120 bf16
+// 48 us with 512 of them, 59 with 1024; 17929 x 567 fp32 26 and 31; but
+// 131072 x 320 bf16 62 and 52.
+int64_t most_groups(int64_t D) { return D <= 512 ? 1024 : 512; }
 
-bool wave_row(int64_t D) { return D <= 1024; }
+// Up to 1024 elements a wave holds whole rows.
+int64_t rows_at_once(int64_t D) { return D <= 1024 ? 4 * (64 / row_lanes(D)) : 1; }
 
-template <bool XBF, bool HF32, bool DRES, bool WAVE_ROW, int NC, bool TINY>
+template <bool XBF, bool HF32, bool DRES, int LANES, int NC, bool TINY>
 hipError_t start(const BwdParams &p, int64_t groups, int threads, hipStream_t s)
 {
-    rms_norm_bwd_kernel<XBF, HF32, DRES, WAVE_ROW, NC, TINY>
+    rms_norm_bwd_kernel<XBF, HF32, DRES, LANES, NC, TINY>
         <<<dim3((unsigned)groups), dim3(threads), 0, s>>>(p);
     return hipGetLastError();
 }
@@ -201,29 +245,34 @@ hipError_t start(const BwdParams &p, int64_t groups, int threads, hipStream_t s)
 template <bool XBF, bool HF32, bool DRES> hipError_t pick(const BwdParams &p, int64_t groups, hipStream_t s)
 {
     if (p.D < kChunk)
-        return start<XBF, HF32, DRES, true, 1, true>(p, groups, 256, s);
+        return start<XBF, HF32, DRES, 8, 1, true>(p, groups, 256, s);
+    switch (row_lanes(p.D)) {
+    case 8: return start<XBF, HF32, DRES, 8, 1, false>(p, groups, 256, s);
+    case 16: return start<XBF, HF32, DRES, 16, 1, false>(p, groups, 256, s);
+    case 32: return start<XBF, HF32, DRES, 32, 1, false>(p, groups, 256, s);
+    }
     const int chunks = (p.D + kChunk - 1) / kChunk;
-    if (wave_row(p.D))
-        return chunks <= 64 ? start<XBF, HF32, DRES, true, 1, false>(p, groups, 256, s)
-                            : start<XBF, HF32, DRES, true, 2, false>(p, groups, 256, s);
+    if (chunks <= 64)
+        return start<XBF, HF32, DRES, 64, 1, false>(p, groups, 256, s);
+    if (chunks <= 128)
+        return start<XBF, HF32, DRES, 64, 2, false>(p, groups, 256, s);
     const int nc = chunks <= 512 ? 1 : chunks <= 2048 ? 2 : 4;
     const int lanes = (chunks + nc - 1) / nc;
     const int threads = (lanes + 63) / 64 * 64;
     if (nc == 1)
-        return start<XBF, HF32, DRES, false, 1, false>(p, groups, threads, s);
+        return start<XBF, HF32, DRES, 0, 1, false>(p, groups, threads, s);
     if (nc == 2)
-        return start<XBF, HF32, DRES, false, 2, false>(p, groups, threads, s);
-    return start<XBF, HF32, DRES, false, 4, false>(p, groups, threads, s);
+        return start<XBF, HF32, DRES, 0, 2, false>(p, groups, threads, s);
+    return start<XBF, HF32, DRES, 0, 4, false>(p, groups, threads, s);
 }
 
 }  // namespace
 
 int64_t rms_norm_bwd_groups(int64_t M, int64_t D)
 {
-    const int64_t rows_at_once = wave_row(D) ? 4 : 1;
-    const int64_t most = (M + rows_at_once - 1) / rows_at_once;
+    const int64_t at_once = rows_at_once(D), most = (M + at_once - 1) / at_once;
     const int64_t wanted = most < 256 ? most : (most / 8 > 256 ? most / 8 : 256);
-    return wanted < kMaxGroups ? wanted : kMaxGroups;
+    return wanted < most_groups(D) ? wanted : most_groups(D);
 }
 
 hipError_t launch_rms_norm_bwd(const NormBwdArgs &a, hipStream_t s)

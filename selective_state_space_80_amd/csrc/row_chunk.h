@@ -68,13 +68,19 @@ template <int CTRL> __device__ __forceinline__ float dppf(float v)
     return __uint_as_float(dpp<CTRL>(__float_as_uint(v)));
 }
 
-// Sum / unsigned maximum over the wave, in every lane: quads, half rows, rows
-// of 16 by DPP, then the four rows through scalar registers.  A fixed order.
-__device__ __forceinline__ float wave_sum(float v)
+// Sum / unsigned maximum over each LANES (8, 16, 32 or 64) neighbouring lanes,
+// in every one of them: quads, half rows, rows of 16 by DPP, then rows by a
+// lane exchange, or of the whole wave through scalar registers.  A fixed order.
+template <int LANES> __device__ __forceinline__ float lane_sum(float v)
 {
     v = quad_sum(v);
     v += dppf<0x141>(v);  // row_half_mirror
-    v += dppf<0x140>(v);  // row_mirror
+    if constexpr (LANES >= 16)
+        v += dppf<0x140>(v);  // row_mirror
+    if constexpr (LANES == 32)
+        v += __shfl_xor(v, 16);
+    if constexpr (LANES < 64)
+        return v;
     const int b = __float_as_int(v);
     return (__int_as_float(__builtin_amdgcn_readlane(b, 0)) +
             __int_as_float(__builtin_amdgcn_readlane(b, 16))) +
@@ -82,16 +88,25 @@ __device__ __forceinline__ float wave_sum(float v)
             __int_as_float(__builtin_amdgcn_readlane(b, 48)));
 }
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
-__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+template <int LANES> __device__ __forceinline__ uint32_t lane_max(uint32_t v)
 {
     v = umax(v, dpp<0xB1>(v));
     v = umax(v, dpp<0x4E>(v));
     v = umax(v, dpp<0x141>(v));
-    v = umax(v, dpp<0x140>(v));
+    if constexpr (LANES >= 16)
+        v = umax(v, dpp<0x140>(v));
+    if constexpr (LANES == 32)
+        v = umax(v, (uint32_t)__shfl_xor((int)v, 16));
+    if constexpr (LANES < 64)
+        return v;
     const int b = (int)v;
     return umax(umax((uint32_t)__builtin_amdgcn_readlane(b, 0), (uint32_t)__builtin_amdgcn_readlane(b, 16)),
                 umax((uint32_t)__builtin_amdgcn_readlane(b, 32), (uint32_t)__builtin_amdgcn_readlane(b, 48)));
 }
+
+// Lanes that share a row of D elements where a wave holds whole rows: as few
+// as hold it in one chunk each (8 rows of 64 elements a wave), 64 for longer.
+inline int row_lanes(int64_t D) { return D <= 64 ? 8 : D <= 128 ? 16 : D <= 256 ? 32 : 64; }
 
 // The bits of |v| order as |v| does, infinity above every finite value and NaN
 // above infinity, so one unsigned maximum also tells a row that is not finite.
@@ -198,6 +213,12 @@ template <bool BF16> struct RawChunk {
             for (int i = 0; i < (BF16 ? 1 : 2); ++i)
                 __builtin_memcpy(&v[i], row + at.off + 4 * i, 16);
         }
+    }
+    __device__ __forceinline__ void keep()
+    {
+#pragma unroll
+        for (int i = 0; i < (BF16 ? 1 : 2); ++i)
+            asm volatile("" : "+v"(v[i]));
     }
     __device__ __forceinline__ void get(float (&f)[8]) const
     {
