@@ -44,7 +44,6 @@ struct MatmulParams {
     int64_t a_batch, b_batch;  // rows between batches: 0 = shared
     int tiles_m, tiles_n;
     int64_t tiles;             // of all batches
-    bool stream_out;           // whole-line stores go past the caches
 };
 
 // Past the inner axis' end a lane loads these instead.
@@ -140,7 +139,7 @@ __device__ __forceinline__ Share xcd_share(int64_t tiles, int xcd)
 // caches, issued without branches, and not waited for by the next tile's first
 // step (8 x 5120 x 2048 x 2560: 178 us, by way of the caches 204; before also
 // guarded, waited for, and with the scales loaded there 212).
-template <int WM, int WN, int FM, int FN, int STAGES, bool BF16>
+template <int WM, int WN, int FM, int FN, int STAGES, bool BF16, bool STREAM>
 __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const MatmulParams p)
 {
     constexpr int TM = WM * FM * 32, TN = WN * FN * 32, NW = WM * WN;
@@ -336,7 +335,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const MatmulParam
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 col_scale[j][e] = *(const f32x4 *)(st + (SA * 64 + j * 32 + e * 8 + half * 4) * 4);
-        auto finish = [&](auto full, auto stream) {
+        auto finish = [&](auto full) {
 #pragma unroll
             for (int j0 = 0; j0 < FN; j0 += kWide) {
                 const int64_t n = t.n0 + (wn * FN + j0) * 32 + (lane & 7) * kPerChunk;
@@ -367,7 +366,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const MatmulParam
                         const u32x4 v = *(const u32x4 *)(st + row * 128 + place(row, lane & 7) * 16);
                         typedef u32x4 __attribute__((aligned(2))) loose;  // rows start at any element
                         T *to = o + (int64_t)(i * 32 + r * 8) * p.N;
-                        if constexpr (full && stream) {
+                        if constexpr (full && STREAM) {
                             __builtin_nontemporal_store(v, (loose *)to);
                         } else if constexpr (full) {
                             *(loose *)to = v;
@@ -390,12 +389,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const MatmulParam
             }
         };
         stores_known = t.m0 + TM <= p.M && t.n0 + TN <= p.N;
-        if (stores_known && p.stream_out)
-            finish(std::true_type{}, std::true_type{});
-        else if (stores_known)
-            finish(std::true_type{}, std::false_type{});
+        if (stores_known)
+            finish(std::true_type{});
         else
-            finish(std::false_type{}, std::false_type{});
+            finish(std::false_type{});
     }
 }
 
@@ -603,13 +600,23 @@ Form choose(int64_t batch, int64_t M, int64_t N, int64_t K)
     return best;
 }
 
-template <int WM, int WN, int FM, int FN, int STAGES> hipError_t tile(const MatmulParams &p, int slots, bool bf16, hipStream_t s)
+template <int WM, int WN, int FM, int FN, int STAGES>
+hipError_t tile(const MatmulParams &p, int slots, bool bf16, hipStream_t s)
 {
     const dim3 grid((unsigned)(p.tiles < slots ? p.tiles : slots)), block(64 * WM * WN);
-    if (bf16)
-        tile_kernel<WM, WN, FM, FN, STAGES, true><<<grid, block, 0, s>>>(p);
+    // Rows that start at 64-byte boundaries are stored past the caches in whole
+    // pieces of memory traffic (16384 x 5120 x 160: 40 us, 46 by the caches;
+    // 16384 x 5152: 47 and 53); others leave pieces that a cache has to join
+    // (16384 x 5128: 88 us past the caches, 56 by them; 5121: 99 and 58).
+    const bool stream = (p.N * (bf16 ? 2 : 4)) % 64 == 0 && (uintptr_t)p.out % 64 == 0;
+    if (bf16 && stream)
+        tile_kernel<WM, WN, FM, FN, STAGES, true, true><<<grid, block, 0, s>>>(p);
+    else if (bf16)
+        tile_kernel<WM, WN, FM, FN, STAGES, true, false><<<grid, block, 0, s>>>(p);
+    else if (stream)
+        tile_kernel<WM, WN, FM, FN, STAGES, false, true><<<grid, block, 0, s>>>(p);
     else
-        tile_kernel<WM, WN, FM, FN, STAGES, false><<<grid, block, 0, s>>>(p);
+        tile_kernel<WM, WN, FM, FN, STAGES, false, false><<<grid, block, 0, s>>>(p);
     return hipGetLastError();
 }
 
@@ -665,11 +672,6 @@ hipError_t launch_int8_matmul(const Int8MatmulArgs &a, hipStream_t s)
     p.tiles_m = (int)((a.M + kCosts[f].tm - 1) / kCosts[f].tm);
     p.tiles_n = (int)((a.N + kCosts[f].tn - 1) / kCosts[f].tn);
     p.tiles = tiles_of(kCosts[f], a.batch, a.M, a.N);
-    // Rows that start at 64-byte boundaries are stored past the caches in whole
-    // pieces of memory traffic (16384 x 5120 x 160: 40 us, 46 by the caches;
-    // 16384 x 5152: 47 and 53); others leave pieces that a cache has to join
-    // (16384 x 5128: 88 us past the caches, 56 by them; 5121: 99 and 58).
-    p.stream_out = (a.N * (a.bf16 ? 2 : 4)) % 64 == 0 && (uintptr_t)a.out % 64 == 0;
     switch (f) {
     case kTile256: return tile<2, 4, 4, 2, 2>(p, kCus, a.bf16, s);
     case kTile128: return tile<2, 2, 2, 2, 2>(p, 2 * kCus, a.bf16, s);

@@ -81,6 +81,23 @@ def test_batches(batch, M, N, K, shared):
     _check(a, b, sa, sb, f"matmul batch={batch} shared={shared} {M}x{N}x{K}")
 
 
+# Sizes that take every tile form, with ragged edges, several tiles a workgroup,
+# inner sizes that end inside a step, and rows on and off 64-byte boundaries.
+@pytest.mark.parametrize("batch,M,N,K", [
+    (1, 5000, 5200, 1040), (1, 8200, 4100, 800), (1, 7000, 6101, 720), (1, 3000, 2900, 2096), (2, 2500, 2600, 1000),  # 256 x 256
+    (1, 9000, 8100, 304), (1, 6000, 6016, 400), (1, 5000, 4200, 200), (1, 4300, 4201, 64), (1, 9000, 1024, 100), (3, 1500, 1300, 16), (1, 6000, 6080, 128),  # 128 x 128
+    (1, 1100, 1100, 640), (1, 600, 5000, 1300), (1, 2000, 700, 2100), (1, 600, 4992, 144),      # the same, deep
+    (1, 1000, 400, 4000), (1, 400, 1000, 4000), (1, 300, 700, 4000), (1, 700, 300, 4000),       # rings
+    (1, 500, 500, 3000), (1, 700, 700, 900), (1, 900, 1000, 900), (1, 200, 2900, 3000), (1, 2500, 250, 6000),
+    (1, 250, 2500, 6000), (1, 50, 7000, 1500), (1, 7000, 50, 1500), (1, 2500, 100, 6000), (1, 100, 2500, 6000),
+    (1, 40, 3000, 2000), (1, 3000, 40, 2000), (1, 17, 5000, 3000), (1, 5000, 17, 3000), (1, 64, 8000, 1000)])
+def test_forms(batch, M, N, K):
+    lead = (batch,) if batch > 1 else ()
+    a, sa = _operand(lead + (M, K), M + K)
+    b, sb = _operand((N, K), N + K)
+    _check(a, b, sa, sb, f"matmul batch={batch} {M}x{N}x{K}")
+
+
 def test_extremes():
     """The largest sums an inner size of 131071 allows stay exact."""
     import torch
