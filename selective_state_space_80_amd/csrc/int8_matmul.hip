@@ -407,9 +407,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const MatmulParam
 template <int FM, int FN, int STAGES, bool BF16> __global__ __launch_bounds__(512) void ring_kernel(const MatmulParams p)
 {
     constexpr int NW = 8, TM = FM * 16, TN = FN * 16, kStage = (TM + TN) * kStep, kLoads = 2 * (FM + FN);
-    constexpr int kPitch = TN + 4;
     __shared__ __attribute__((aligned(16))) char smem[NW * STAGES * kStage];
-    __shared__ int sum[TM * kPitch];
+    __shared__ int sum[FM * FN * 4][64];  // as the products' lanes hold them: added without bank conflicts
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Share share = xcd_share(p.tiles, blockIdx.x % kXcds);
@@ -444,8 +443,8 @@ template <int FM, int FN, int STAGES, bool BF16> __global__ __launch_bounds__(51
     for (int i = 0; i < STAGES; ++i)
         if (from + i < to)
             issue(from + i, i);
-    for (int i = threadIdx.x; i < TM * kPitch; i += 64 * NW)
-        sum[i] = 0;
+    for (int i = threadIdx.x; i < TM * TN; i += 64 * NW)
+        sum[i / 64][i % 64] = 0;
     // fragments: a lane holds 16 bytes of row lane % 16, quarter lane / 16
     const int fr = lane & 15, quarter = lane >> 4;
     i32x4 acc[FM][FN];
@@ -491,15 +490,37 @@ template <int FM, int FN, int STAGES, bool BF16> __global__ __launch_bounds__(51
         for (int j = 0; j < FN; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                atomicAdd(sum + (i * 16 + fr) * kPitch + j * 16 + quarter * 4 + e, acc[i][j][e]);
+                atomicAdd(&sum[(i * FN + j) * 4 + e][lane], acc[i][j][e]);
     __syncthreads();
+    // four consecutive n of one m a thread
     using T = typename Elem<BF16>::T;
     const float *a_scale = p.a_scale + batch * p.a_batch + m0, *b_scale = p.b_scale + batch * p.b_batch + n0;
     T *out = (T *)p.out + (batch * p.M + m0) * p.N + n0;
-    for (int i = threadIdx.x; i < TM * TN; i += 64 * NW) {
-        const int m = i / TN, n = i % TN;
-        if (m < rows_a && n < rows_b)
-            Elem<BF16>::store(out + (int64_t)m * p.N + n, (float)sum[m * kPitch + n] * a_scale[m] * b_scale[n]);
+    for (int i = threadIdx.x; i < TM * TN / 4; i += 64 * NW) {
+        const int m = i / (TN / 4), n = i % (TN / 4) * 4;
+        if (m >= rows_a || n >= rows_b)
+            continue;
+        const float sa = a_scale[m];
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int from = (m / 16 * FN + n / 16) * 4 + e;
+            v[e] = (float)sum[from][n % 16 / 4 * 16 + m % 16] * sa * b_scale[n + e < rows_b ? n + e : rows_b - 1];
+        }
+        T *o = out + (int64_t)m * p.N + n;
+        if (n + 4 <= rows_b) {
+            if constexpr (BF16) {
+                const u32x2 w = {cvt2(v[0], v[1]), cvt2(v[2], v[3])};
+                __builtin_memcpy(o, &w, 8);
+            } else {
+                __builtin_memcpy(o, v, 16);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (n + e < rows_b)
+                    Elem<BF16>::store(o + e, v[e]);
+        }
     }
 }
 
@@ -554,10 +575,10 @@ size_t padded_bytes(int64_t rows, int64_t K) { return ((size_t)(rows * padded(K)
 //   4096 x 1536 x 768        256 x 256 tiles 12.5, 128 x 128 9.5
 //   1024 x 2560 x 5120       128 x 128 tiles of two stages 30.8, of four 23.7
 //   300 x 8192 x 256         the same 5.4 and 5.6; rings of 64 x 64 16.3
-//   256 x 2560 x 5120        128 x 128 tiles 23.4, rings of 64 x 64 13.1, of 64 x 48 11.7
-//   64 x 2560 x 5120         rings of 64 x 64 13.5, of 32 x 32 7.0
+//   256 x 2560 x 5120        128 x 128 tiles 23.4, rings of 64 x 64 13.1, of 64 x 48 11.2
+//   64 x 2560 x 5120         rings of 64 x 64 13.5, of 32 x 32 6.7
 //   2048 x 64 x 5120         rings of 32 x 32 7.3, of 16 x 32 6.0
-//   16 x 2560 x 5120         rings of 32 x 32 6.2, of 16 x 32 5.7, of 16 x 16 4.6
+//   16 x 2560 x 5120         rings of 32 x 32 6.1, of 16 x 32 5.7, of 16 x 16 4.7
 enum Form { kTile256, kTile128, kTile128Deep, kRing44, kRing43, kRing34, kRing42, kRing24, kRing22, kRing12, kRing21, kRing11, kForms };
 struct FormCost {
     int tm, tn, slots;
