@@ -368,7 +368,8 @@ mamba_status mamba_ssd_scan_fwd(const void *x, const void *dt, const float *dt_b
  *                            residual (updated in place)
  *   weight                 : [D] float, required
  *   eps                    : finite, >= 0 (else MAMBA_ERR_SHAPE)
- * D in 1..32768 (MAMBA_MAX_NORM_WIDTH), M < 2^22.  The square sum is an fp32
+ * D in 1..32768 (MAMBA_MAX_NORM_WIDTH), M < 2^26 for D up to 4096 and below
+ * 2^22 beyond.  The square sum is an fp32
  * sum: rows whose sum of squares passes the fp32 range give zeros or NaN.
  * Except for that in-place update, outputs must not overlap inputs or each
  * other.
@@ -423,7 +424,8 @@ mamba_status mamba_rms_norm_bwd(const void *dy, const void *h, const float *weig
  *   channel_major 0 : x [B, L, K] of `io`, K at most 32768
  *   channel_major 1 : x [B, K, L] of `io`, as the scans write their output
  *   q               : [B, L, K] int8;  scale : [B, L] float
- * B * L < 2^22; K at least 1 unless B * L is 0.
+ * K at least 1 unless B * L is 0.  Token-major B * L as M above; channel-major
+ * B * ceil(L / 16) < 2^22.
  */
 mamba_status mamba_quantize_int8(const void *x, int8_t *q, float *scale, int64_t B, int64_t L, int64_t K,
                                  int channel_major, mamba_dtype io, void *stream);

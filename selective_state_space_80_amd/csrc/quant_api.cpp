@@ -14,6 +14,10 @@ namespace {
 
 constexpr int64_t kMaxBlocks = int64_t(1) << 22;  // blocks x 1024 threads below 2^32 work-items
 
+// Rows the token-major kernels can be launched on: of up to 4096 elements four
+// or more share a 256-thread block, wider ones have up to 1024 threads each.
+int64_t max_rows(int64_t D) { return D <= 4096 ? kMaxBlocks * 16 : kMaxBlocks; }
+
 // Checks of both forward norms.  `out_bytes`: of one element of `out`.
 mamba_status norm_entry(const void *x, const void *residual, const float *weight, void *out, float *scale,
                         bool int8, void *residual_out, int64_t M, int64_t D, float eps, mamba_dtype io,
@@ -26,7 +30,7 @@ mamba_status norm_entry(const void *x, const void *residual, const float *weight
     if (D > mamba::kMaxNormWidth || (residual && io == MAMBA_F32 && residual_type == MAMBA_BF16) ||
         (residual_out && !residual))
         return MAMBA_ERR_UNSUPPORTED;
-    if (M >= kMaxBlocks)
+    if (M >= max_rows(D))
         return MAMBA_ERR_SHAPE;
     if (M * D == 0 && !(int8 && M > 0))
         return MAMBA_OK;
@@ -144,7 +148,8 @@ mamba_status mamba_quantize_int8(const void *x, int8_t *q, float *scale, int64_t
         return MAMBA_ERR_SHAPE;
     if ((channel_major != 0 && channel_major != 1) || (!channel_major && K > mamba::kMaxNormWidth))
         return MAMBA_ERR_UNSUPPORTED;
-    if (B * L >= kMaxBlocks)
+    // channel-major: a block has 16 tokens or more (fewer only in launches of few blocks)
+    if (channel_major ? L >= kMaxBlocks * 16 || B * ((L + 15) / 16) >= kMaxBlocks : B * L >= max_rows(K))
         return MAMBA_ERR_SHAPE;
     if (B * L == 0)
         return MAMBA_OK;

@@ -279,7 +279,9 @@ hipError_t launch_rms_norm_bwd(const NormBwdArgs &a, hipStream_t s)
 {
     const int64_t groups = rms_norm_bwd_groups(a.M, a.D);
     if (groups > 0) {
-        BwdParams p{a.dy, a.h, a.dres_out, a.weight, a.dx, a.dres, a.partials, a.M, a.D, a.eps, 1.f / (float)a.D};
+        // a single group's partial row is the gradient itself
+        float *partials = groups == 1 ? a.dweight : a.partials;
+        BwdParams p{a.dy, a.h, a.dres_out, a.weight, a.dx, a.dres, partials, a.M, a.D, a.eps, 1.f / (float)a.D};
         hipError_t e;
         if (!a.bf16)
             e = a.dres_out ? pick<false, false, true>(p, groups, s) : pick<false, false, false>(p, groups, s);
@@ -287,7 +289,7 @@ hipError_t launch_rms_norm_bwd(const NormBwdArgs &a, hipStream_t s)
             e = a.dres_out ? pick<true, false, true>(p, groups, s) : pick<true, false, false>(p, groups, s);
         else
             e = a.dres_out ? pick<true, true, true>(p, groups, s) : pick<true, true, false>(p, groups, s);
-        if (e != hipSuccess)
+        if (e != hipSuccess || groups == 1)
             return e;
     }
     dweight_sum_kernel<<<dim3((unsigned)((a.D + 31) / 32)), dim3(1024), 0, s>>>(a.partials, a.dweight, groups, a.D);

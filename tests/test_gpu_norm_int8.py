@@ -251,6 +251,52 @@ def test_special_rows(K, io, form):
         assert torch.equal(s[6], (rows[6].double().abs().max() / 127.0).float())
 
 
+@pytest.mark.parametrize("M,D", [((1 << 22) + 5, 40), (70000, 32768)])
+def test_many_rows_and_offsets_past_32_bits(M, D):
+    """More rows than 2^22, and tensors of more than 2^31 elements."""
+    import torch
+    import selective_state_space_80_amd as mamba
+    x = _draw((1, D), "bf16", 81).expand(M, D).contiguous()
+    x[-1] = _draw((D,), "bf16", 82)
+    x[M // 2] = 0.0
+    w = 1.0 + 0.1 * _draw((D,), "f32", 83)
+    rows = torch.tensor([0, 1, M // 2 - 1, M // 2, M // 2 + 1, M - 2, M - 1], device="cuda")
+    y = _norm64(x[rows], None, w, 1e-5)[2]
+    q, s = mamba.rms_norm_int8(x, w)
+    _check_int8(q[rows], s[rows], y, SUM, "norm int8")
+    del q
+    q, s = mamba.quantize_int8(x)
+    _check_int8(q[rows], s[rows], x[rows].double(), 0.0, "quantize")
+    del q
+    out = mamba.rms_norm(x, w)
+    _close(out[rows], y, _out_tol("bf16", SUM), "norm")
+    del out
+    if D <= 4096:
+        g = mamba.rms_norm_bwd(x, x, w)
+        h = x[rows].double()
+        r = 1.0 / (h.square().mean(-1, keepdim=True) + 1e-5).sqrt()
+        along = (w.double() * h * h).mean(-1, keepdim=True)
+        dh = r * w.double() * h - r ** 3 * h * along
+        size = (r * w.double() * h).abs() + r ** 3 * h.abs() * along.abs()
+        err = (g["dx"][rows].double() - dh).abs()
+        assert (err <= GRAD * size + HALF_BF16 * dh.abs() + 1e-37).all()
+    torch.cuda.empty_cache()
+
+
+def test_channel_major_offsets_past_32_bits():
+    import torch
+    import selective_state_space_80_amd as mamba
+    K, L = 5120, 440000
+    x = torch.empty((1, K, L), dtype=torch.bfloat16, device="cuda")
+    x[:] = _draw((1, K, 1), "bf16", 84)
+    x[0, K - 1, L - 1] = 1000.0
+    q, s = mamba.quantize_int8(x, channel_major=True)
+    for l in (0, 1, L // 2, L - 2, L - 1):
+        _check_int8(q[0, l], s[0, l:l + 1].squeeze(), x[0, :, l].double(), 0.0, f"token {l}")
+    del x, q
+    torch.cuda.empty_cache()
+
+
 def test_unaligned_storage():
     """Rows that start at any element of their storage."""
     import torch

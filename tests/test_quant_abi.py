@@ -41,7 +41,7 @@ def norm8(lib, **kw):
 @pytest.mark.parametrize("kw,want", [
     (dict(io=2), EDTYPE), (dict(rt=5), EDTYPE), (dict(M=-1), ESHAPE), (dict(D=-1), ESHAPE), (dict(eps=-1.0), ESHAPE),
     (dict(eps=math.nan), ESHAPE), (dict(eps=math.inf), ESHAPE), (dict(D=32769), EUNSUP), (dict(io=F32, rt=BF16), EUNSUP),
-    (dict(residual=None), EUNSUP), (dict(M=1 << 22), ESHAPE), (dict(M=1 << 39, D=4), ESHAPE), (dict(x=None), ENULL),
+    (dict(residual=None), EUNSUP), (dict(M=1 << 26), ESHAPE), (dict(M=1 << 22, D=4097), ESHAPE), (dict(M=1 << 39, D=4), ESHAPE), (dict(x=None), ENULL),
     (dict(weight=None), ENULL), (dict(out=None), ENULL), (dict(x=ctypes.c_void_p((1 << 40) + 1)), EALIGN),
     (dict(residual=ctypes.c_void_p((2 << 40) + 2)), EALIGN), (dict(weight=ctypes.c_void_p((3 << 40) + 2)), EALIGN),
     (dict(out=X), EALIAS), (dict(residual_out=X), EALIAS), (dict(residual_out=W), EALIAS), (dict(out=R), EALIAS),
@@ -80,7 +80,8 @@ def test_norm_bwd_workspace(lib):
 
 
 @pytest.mark.parametrize("kw,want", [
-    (dict(io=2), EDTYPE), (dict(B=-1), ESHAPE), (dict(cm=2), EUNSUP), (dict(K=32769), EUNSUP), (dict(L=1 << 22), ESHAPE),
+    (dict(io=2), EDTYPE), (dict(B=-1), ESHAPE), (dict(cm=2), EUNSUP), (dict(K=32769), EUNSUP), (dict(L=1 << 25), ESHAPE), (dict(L=1 << 21, K=5000), ESHAPE), (dict(L=1 << 25, cm=1), ESHAPE),
+    (dict(B=1 << 22, L=3, cm=1), ESHAPE),
     (dict(K=0), ESHAPE), (dict(B=0), OK), (dict(L=0, K=0), OK), (dict(x=None), ENULL), (dict(q=None), ENULL),
     (dict(s=None), ENULL), (dict(x=ctypes.c_void_p((1 << 40) + 1)), EALIGN), (dict(s=ctypes.c_void_p((6 << 40) + 1)), EALIGN),
     (dict(q=X), EALIAS), (dict(s=X), EALIAS), (dict(s=O), EALIAS)])
