@@ -430,12 +430,9 @@ mamba_status mamba_rms_norm_bwd(const void *dy, const void *h, const float *weig
 mamba_status mamba_quantize_int8(const void *x, int8_t *q, float *scale, int64_t B, int64_t L, int64_t K,
                                  int channel_major, mamba_dtype io, void *stream);
 
-/* Flags of mamba_int8_matmul and of its workspace size: the operand is one
- * matrix, used by every batch. */
+/* Flags of mamba_int8_matmul: the operand is one matrix, used by every batch. */
 #define MAMBA_INT8_SHARED_A 1u
 #define MAMBA_INT8_SHARED_B 2u
-/* For the workspace size only: an operand is not 16-byte aligned. */
-#define MAMBA_INT8_UNALIGNED 4u
 
 /*
  * Product of 8-bit integers with a scale for each row of both operands:
@@ -449,18 +446,13 @@ mamba_status mamba_quantize_int8(const void *x, int8_t *q, float *scale, int64_t
  *                [M, K] and [M]
  *   b, b_scale : [batch, N, K], [batch, N]; with MAMBA_INT8_SHARED_B [N, K], [N]
  *   out        : [batch, M, N] of `out_type`
- *   workspace  : mamba_int8_matmul_workspace_size(...) bytes, 256-byte aligned;
- *                scratch as in the scan.  None is needed when K is a multiple
- *                of 16 and both operands are 16-byte aligned; otherwise they
- *                are first copied there with their rows padded (about the
- *                operands' size; ask with MAMBA_INT8_UNALIGNED when an operand
- *                is not 16-byte aligned)
- * K from 0 (zeros) to 131071; at most 2^23 tiles of 128 x 128 outputs.
+ * K from 0 (zeros) to 131071, operands at any address; K a multiple of 16 with
+ * 16-byte aligned operands is fastest.  At most 2^23 tiles of 128 x 128 outputs
+ * a call.  Needs no workspace.
  */
-size_t mamba_int8_matmul_workspace_size(int64_t batch, int64_t M, int64_t N, int64_t K, unsigned flags);
 mamba_status mamba_int8_matmul(const int8_t *a, const int8_t *b, const float *a_scale, const float *b_scale,
-                               void *out, void *workspace, size_t workspace_bytes, int64_t batch, int64_t M,
-                               int64_t N, int64_t K, mamba_dtype out_type, unsigned flags, void *stream);
+                               void *out, int64_t batch, int64_t M, int64_t N, int64_t K, mamba_dtype out_type,
+                               unsigned flags, void *stream);
 
 /*
  * Profiling hook.  When both are non-NULL hipEvent_t handles (passed as

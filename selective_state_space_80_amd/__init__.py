@@ -25,7 +25,7 @@ Entry points (same names as the C ABI, without the ``mamba_`` prefix):
   rms_norm_int8(x, weight, residual=None, eps=1e-5, out=None, scale=None, residual_out=None)
   rms_norm_bwd(dy, h, weight, dresidual_out=None, eps=1e-5, workspace=None)
   quantize_int8(x, channel_major=False, out=None, scale=None)
-  int8_matmul(a, b, a_scale, b_scale, out_dtype=torch.bfloat16, out=None, workspace=None)
+  int8_matmul(a, b, a_scale, b_scale, out_dtype=torch.bfloat16, out=None)
   selective_scan_check(workspace)        the carry's error word (after a sync)
   set_scan_spin_limit(polls)             diagnostic bound of the carry waits
 Test helper: set_carry_checks(True) checks the carry after every scan call.
@@ -60,7 +60,7 @@ EXPORTED = ["mamba_status_string", "mamba_abi_version", "mamba_conv1d_silu",
             "mamba_selective_scan_check", "mamba_set_scan_spin_limit",
             "mamba_selective_scan_fwd_noalloc", "mamba_rms_norm", "mamba_rms_norm_int8",
             "mamba_rms_norm_bwd_workspace_size", "mamba_rms_norm_bwd", "mamba_quantize_int8",
-            "mamba_int8_matmul_workspace_size", "mamba_int8_matmul"]
+            "mamba_int8_matmul"]
 
 _lib = None
 
@@ -133,10 +133,8 @@ def load_library(path: str = LIBRARY):
     lib.mamba_rms_norm_bwd.argtypes = [P] * 8 + [SZ, I64, I64, F, I32, I32, P]
     lib.mamba_quantize_int8.restype = I32
     lib.mamba_quantize_int8.argtypes = [P] * 3 + [I64, I64, I64, I32, I32, P]
-    lib.mamba_int8_matmul_workspace_size.restype = SZ
-    lib.mamba_int8_matmul_workspace_size.argtypes = [I64] * 4 + [U32]
     lib.mamba_int8_matmul.restype = I32
-    lib.mamba_int8_matmul.argtypes = [P] * 6 + [SZ, I64, I64, I64, I64, I32, U32, P]
+    lib.mamba_int8_matmul.argtypes = [P] * 5 + [I64, I64, I64, I64, I32, U32, P]
     _lib = lib
     return lib
 
@@ -750,14 +748,9 @@ def quantize_int8(x, channel_major=False, out=None, scale=None):
 
 INT8_SHARED_A = 1  # MAMBA_INT8_SHARED_A
 INT8_SHARED_B = 2  # MAMBA_INT8_SHARED_B
-INT8_UNALIGNED = 4  # MAMBA_INT8_UNALIGNED
 
 
-def int8_matmul_workspace_size(batch, M, N, K, flags=0) -> int:
-    return int(load_library().mamba_int8_matmul_workspace_size(batch, M, N, K, flags))
-
-
-def int8_matmul(a, b, a_scale, b_scale, out_dtype=None, out=None, workspace=None):
+def int8_matmul(a, b, a_scale, b_scale, out_dtype=None, out=None):
     """out[..., m, n] = a_scale[m] b_scale[n] sum_k a[m, k] b[n, k], summed
     exactly.  a [M, K] or [B, M, K], b [N, K] or [B, N, K] int8 (a 2-D operand
     is used by every batch of a 3-D one); scales f32 of the operands' leading
@@ -791,15 +784,8 @@ def int8_matmul(a, b, a_scale, b_scale, out_dtype=None, out=None, workspace=None
                           device=dev)
     else:
         _check(out, "out", (*lead, M, N), out_dtype, dev)
-    pa, pb, nbytes = a.data_ptr(), b.data_ptr(), 0
-    if workspace is not None:
-        nbytes = workspace.numel()
-    elif K % 16 or (pa | pb) % 16:
-        nbytes = lib.mamba_int8_matmul_workspace_size(batch, M, N, K, flags | INT8_UNALIGNED)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-    st = lib.mamba_int8_matmul(pa, pb, a_scale.data_ptr(), b_scale.data_ptr(), out.data_ptr(),
-                               _addr(workspace), nbytes, batch, M, N, K, _io_dtype(out), flags,
-                               _raw_stream(a))
+    st = lib.mamba_int8_matmul(a.data_ptr(), b.data_ptr(), a_scale.data_ptr(), b_scale.data_ptr(),
+                               out.data_ptr(), batch, M, N, K, _io_dtype(out), flags, _raw_stream(a))
     if st:
         _raise(st, "mamba_int8_matmul")
     return out

@@ -3,18 +3,16 @@
 // The sum is exact (32-bit integers); it is converted to fp32, scaled, and
 // rounded once to the output type.
 //
-// Two kernels, both fed by loads that go from memory straight into LDS
-// (global_load_lds_dwordx4: no registers, so as many are in flight as LDS
-// holds), both with the operand rows in tiles of 128 bytes (one cache line) of
-// the inner axis:
+// Two kernels, both with the operand rows in LDS in tiles of 128 bytes (one
+// cache line) of the inner axis, both fed by loads that go from memory straight
+// into LDS (DIRECT, global_load_lds_dwordx4: no registers, so as many are in
+// flight as LDS holds), or, where rows do not start at 16-byte boundaries, which
+// those loads need, by way of registers:
 //   tile_kernel  a workgroup's waves share a tile of both operands (256 x 256
 //                or 128 x 128 outputs) and step through the inner axis together
 //   ring_kernel  few output tiles, or few rows on one side: the waves of a
 //                workgroup split the inner axis, each streaming its share
 //                through its own LDS ring, and add their integer sums
-// An inner size that is no multiple of 16, or operands off 16-byte alignment,
-// which the wide LDS loads do not take, are first laid out in the workspace
-// with their rows padded by zeros (pad_rows_kernel).
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -72,10 +70,32 @@ __device__ __forceinline__ uint32_t lds_address(const char *p)
 // chunk index then touch every one of the 64 banks once.
 __device__ __forceinline__ int place(int row, int chunk) { return chunk ^ ((row >> 1) & 7); }
 
+// The 16 bytes that end a row of K bytes (K >= 16) moved down so that its last
+// `rem` come first, zeros behind them.
+__device__ __forceinline__ u32x4 row_end(u32x4 v, int rem)
+{
+    const int shift = 16 - rem, words = shift >> 2;
+    uint32_t w[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+        w[i] = 0;
+#pragma unroll
+        for (int j = i; j < 4; ++j)
+            w[i] = j - i == words ? v[j] : w[i];
+    }
+    u32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        r[i] = __builtin_amdgcn_alignbyte(w[i + 1], w[i], shift & 3);
+    return r;
+}
+
 // A wave's loads of 8 * N rows of a tile.  A load takes 8 rows, 8 lanes each;
 // rows past the operand's end repeat its last (their products are not stored).
-template <int N> struct RowLoads {
+// Past the inner axis' end LDS gets zeros.
+template <int N, bool DIRECT> struct RowLoads {
     uint32_t off[N];
+    u32x4 held[DIRECT ? 1 : N];
     __device__ __forceinline__ void set(int first_row, int step_rows, int rows, int K)
     {
         const int lane = threadIdx.x & 63;
@@ -85,13 +105,15 @@ template <int N> struct RowLoads {
             off[i] = (uint32_t)((row < rows ? row : rows - 1) * K + place(row, lane & 7) * 16);
         }
     }
+    // DIRECT: a whole step into LDS.
     __device__ __forceinline__ void whole(uint32_t lds, int step_bytes, const int8_t *base) const
     {
 #pragma unroll
         for (int i = 0; i < N; ++i)
             load_lds(lds + i * step_bytes, base, off[i]);
     }
-    // the last step of an inner axis that is no multiple of kStep: `left` bytes
+    // DIRECT: the last step of an inner axis that is no multiple of kStep, of
+    // which `left` bytes are left.
     __device__ __forceinline__ void partial(uint32_t lds, int step_bytes, const int8_t *base, int first_row,
                                             int step_rows, int left) const
     {
@@ -102,6 +124,47 @@ template <int N> struct RowLoads {
             const int8_t *p = place(row, lane & 7) * 16 < left ? base + off[i] : (const int8_t *)&kZeros;
             load_lds(lds + i * step_bytes, p);
         }
+    }
+    // By way of registers: fetch a step of which `left` bytes are left, then
+    // put it into LDS.
+    __device__ __forceinline__ void fetch(const int8_t *base, int first_row, int step_rows, int left, int K)
+    {
+        const int lane = threadIdx.x & 63;
+        if (left >= kStep) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                __builtin_memcpy(&held[i], base + off[i], 16);
+        } else if (K >= 16) {
+            // a chunk that passes the row's end is read so as to end with it
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int r = left - place(first_row + i * step_rows + (lane >> 3), lane & 7) * 16;
+                u32x4 v;
+                __builtin_memcpy(&v, base + (int64_t)off[i] + (r < 16 ? r - 16 : 0), 16);
+                const u32x4 end = row_end(v, left & 15);
+                held[i] = r >= 16 ? v : (r > 0 ? end : u32x4{0, 0, 0, 0});
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int r = left - place(first_row + i * step_rows + (lane >> 3), lane & 7) * 16;
+                uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+                for (int j = 0; j < r; ++j) {
+                    const uint64_t byte = (uint64_t)(uint8_t)base[off[i] + j] << (8 * (j & 7));
+                    lo |= j < 8 ? byte : 0;
+                    hi |= j < 8 ? 0 : byte;
+                }
+                held[i] = u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+            }
+        }
+    }
+    __device__ __forceinline__ void put(char *to, int step_bytes) const
+    {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            *(u32x4 *)(to + i * step_bytes + lane * 16) = held[i];
     }
 };
 
@@ -139,7 +202,7 @@ __device__ __forceinline__ Share xcd_share(int64_t tiles, int xcd)
 // caches, issued without branches, and not waited for by the next tile's first
 // step (8 x 5120 x 2048 x 2560: 178 us, by way of the caches 204; before also
 // guarded, waited for, and with the scales loaded there 212).
-template <int WM, int WN, int FM, int FN, int STAGES, bool BF16, bool STREAM>
+template <int WM, int WN, int FM, int FN, int STAGES, bool DIRECT, bool BF16, bool STREAM>
 __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const MatmulParams p)
 {
     constexpr int TM = WM * FM * 32, TN = WN * FN * 32, NW = WM * WN;
@@ -179,9 +242,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const MatmulParam
         return t;
     };
 
-    // the loads' cursor: STAGES steps ahead of the products
-    RowLoads<LA> loads_a;
-    RowLoads<LB> loads_b;
+    // the loads' cursor: STAGES steps ahead of the products, one more by way of registers
+    RowLoads<LA, DIRECT> loads_a;
+    RowLoads<LB, DIRECT> loads_b;
     const int8_t *next_a = nullptr, *next_b = nullptr;
     int64_t load_tile = slot;
     int load_step = 0, ahead = 0;  // ahead: stages issued and not yet waited for
@@ -192,20 +255,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const MatmulParam
         loads_a.set(wave * 8, NW * 8, (int)(p.M - t.m0 < TM ? p.M - t.m0 : TM), p.K);
         loads_b.set(wave * 8, NW * 8, (int)(p.N - t.n0 < TN ? p.N - t.n0 : TN), p.K);
     };
-    const uint32_t lds = lds_address(smem) + wave * 1024;
-    auto issue = [&](int stage) {
-        if (load_tile >= share.count)
-            return;
-        ++ahead;
-        const uint32_t to = lds + stage * kStage;
-        const int left = p.K - load_step * kStep;
-        if (left >= kStep) {
-            loads_a.whole(to, NW * 1024, next_a);
-            loads_b.whole(to + TM * kStep, NW * 1024, next_b);
-        } else {
-            loads_a.partial(to, NW * 1024, next_a, wave * 8, NW * 8, left);
-            loads_b.partial(to + TM * kStep, NW * 1024, next_b, wave * 8, NW * 8, left);
-        }
+    auto advance = [&]() {
         next_a += kStep;
         next_b += kStep;
         if (++load_step == p.steps) {
@@ -213,6 +263,39 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const MatmulParam
             load_tile += stride;
             if (load_tile < share.count)
                 start_tile();
+        }
+    };
+    bool holds = false;  // a step waits in registers
+    auto fetch = [&]() {
+        holds = load_tile < share.count;
+        if (!holds)
+            return;
+        const int left = p.K - load_step * kStep;
+        loads_a.fetch(next_a, wave * 8, NW * 8, left, p.K);
+        loads_b.fetch(next_b, wave * 8, NW * 8, left, p.K);
+        advance();
+    };
+    const uint32_t lds = lds_address(smem) + wave * 1024;
+    auto issue = [&](int stage) {
+        if constexpr (DIRECT) {
+            if (load_tile >= share.count)
+                return;
+            ++ahead;
+            const uint32_t to = lds + stage * kStage;
+            const int left = p.K - load_step * kStep;
+            if (left >= kStep) {
+                loads_a.whole(to, NW * 1024, next_a);
+                loads_b.whole(to + TM * kStep, NW * 1024, next_b);
+            } else {
+                loads_a.partial(to, NW * 1024, next_a, wave * 8, NW * 8, left);
+                loads_b.partial(to + TM * kStep, NW * 1024, next_b, wave * 8, NW * 8, left);
+            }
+            advance();
+        } else if (holds) {
+            char *to = smem + stage * kStage + wave * 1024;
+            loads_a.put(to, NW * 1024);
+            loads_b.put(to + TM * kStep, NW * 1024);
+            fetch();
         }
     };
 
@@ -229,15 +312,19 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const MatmulParam
     };
 
     start_tile();
+    if constexpr (!DIRECT)
+        fetch();
 #pragma unroll
     for (int i = 0; i < STAGES; ++i)
         issue(i);
-    if (ahead == STAGES)
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((STAGES - 1) * (LA + LB)) : "memory");
-    else
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    --ahead;
-    asm volatile("s_barrier" ::: "memory");
+    if constexpr (DIRECT) {
+        if (ahead == STAGES)
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"((STAGES - 1) * (LA + LB)) : "memory");
+        else
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        --ahead;
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     i32x4 fa[2][FM], fb[2][FN];
     fragments(fa[0], fb[0], 0, 0);
     int stage = 0;
@@ -265,7 +352,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const MatmulParam
                 if (round < 3) {
                     fragments(fa[(round + 1) & 1], fb[(round + 1) & 1], stage, round + 1);
                 } else {
-                    if (s == p.steps - 1) {  // the scales have arrived long since: the compiler's wait for them
+                    if (DIRECT && s == p.steps - 1) {  // the scales have arrived long since: the compiler's wait for them
 #pragma unroll
                         for (int i = 0; i < SA; ++i)
                             asm volatile("" : "+v"(sa[i]));
@@ -279,14 +366,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const MatmulParam
                     // a tile's first step of a two-stage kernel the stores of
                     // the tile before.  Where their number is not known,
                     // everything is waited for.
-                    if (STAGES > 2 && !first && ahead == STAGES - 1)
-                        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((STAGES - 2) * (LA + LB)) : "memory");
-                    else if (STAGES == 2 && first && stores_known)
-                        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kStores) : "memory");
-                    else
-                        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-                    if (ahead > 0)
-                        --ahead;
+                    if constexpr (DIRECT) {
+                        if (STAGES > 2 && !first && ahead == STAGES - 1)
+                            asm volatile("s_waitcnt vmcnt(%0)" ::"n"((STAGES - 2) * (LA + LB)) : "memory");
+                        else if (STAGES == 2 && first && stores_known)
+                            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kStores) : "memory");
+                        else
+                            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                        if (ahead > 0)
+                            --ahead;
+                    }
                     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
                     fragments(fa[0], fb[0], next, 0);  // after the last step: read, not used
                     issue(stage);
@@ -404,7 +493,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const MatmulParam
 // without a common pause.  What bounds it is the rate at which one CU takes
 // lines into LDS (a single workgroup on an idle card: 97 bytes a ns, all of
 // them together about 60) and, for one token, the launch.
-template <int FM, int FN, int STAGES, bool BF16> __global__ __launch_bounds__(512) void ring_kernel(const MatmulParams p)
+template <int FM, int FN, int STAGES, bool DIRECT, bool BF16>
+__global__ __launch_bounds__(512) void ring_kernel(const MatmulParams p)
 {
     constexpr int NW = 8, TM = FM * 16, TN = FN * 16, kStage = (TM + TN) * kStep, kLoads = 2 * (FM + FN);
     __shared__ __attribute__((aligned(16))) char smem[NW * STAGES * kStage];
@@ -418,14 +508,14 @@ template <int FM, int FN, int STAGES, bool BF16> __global__ __launch_bounds__(51
     const int64_t m0 = (int64_t)(rest % p.tiles_m) * TM, n0 = (int64_t)(rest / p.tiles_m) * TN;
     const int8_t *a = p.a + (batch * p.a_batch + m0) * p.K, *b = p.b + (batch * p.b_batch + n0) * p.K;
     const int rows_a = (int)(p.M - m0 < TM ? p.M - m0 : TM), rows_b = (int)(p.N - n0 < TN ? p.N - n0 : TN);
-    RowLoads<2 * FM> loads_a;
-    RowLoads<2 * FN> loads_b;
+    RowLoads<2 * FM, DIRECT> loads_a;
+    RowLoads<2 * FN, DIRECT> loads_b;
     loads_a.set(0, 8, rows_a, p.K);
     loads_b.set(0, 8, rows_b, p.K);
 
     const int each = (p.steps + NW - 1) / NW, from = wave * each;
     const int to = from + each < p.steps ? from + each : p.steps;
-    const char *mine = smem + wave * STAGES * kStage;
+    char *mine = smem + wave * STAGES * kStage;
     const uint32_t lds = lds_address(mine);
     auto issue = [&](int step, int stage) {
         const uint32_t l = lds + stage * kStage;
@@ -439,10 +529,19 @@ template <int FM, int FN, int STAGES, bool BF16> __global__ __launch_bounds__(51
             loads_b.partial(l + TM * kStep, 1024, sb, 0, 8, left);
         }
     };
+    auto fetch = [&](int step) {
+        const int left = p.K - step * kStep;
+        loads_a.fetch(a + (int64_t)step * kStep, 0, 8, left, p.K);
+        loads_b.fetch(b + (int64_t)step * kStep, 0, 8, left, p.K);
+    };
+    if constexpr (DIRECT) {
 #pragma unroll
-    for (int i = 0; i < STAGES; ++i)
-        if (from + i < to)
-            issue(from + i, i);
+        for (int i = 0; i < STAGES; ++i)
+            if (from + i < to)
+                issue(from + i, i);
+    } else if (from < to) {
+        fetch(from);
+    }
     for (int i = threadIdx.x; i < TM * TN; i += 64 * NW)
         sum[i / 64][i % 64] = 0;
     // fragments: a lane holds 16 bytes of row lane % 16, quarter lane / 16
@@ -455,11 +554,16 @@ template <int FM, int FN, int STAGES, bool BF16> __global__ __launch_bounds__(51
             acc[i][j] = i32x4{0, 0, 0, 0};
     int stage = 0;
     for (int s = from; s < to; ++s) {
-        // this stage has arrived when only the younger ones' loads are pending
-        if (s + STAGES <= to)
+        if constexpr (!DIRECT) {  // the next step is fetched while this one is worked on
+            loads_a.put(mine, 1024);
+            loads_b.put(mine + TM * kStep, 1024);
+            if (s + 1 < to)
+                fetch(s + 1);
+        } else if (s + STAGES <= to) {  // arrived when only the younger stages' loads are pending
             asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads * (STAGES - 1)) : "memory");
-        else
+        } else {
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
         i32x4 fa[2][FM], fb[2][FN];
 #pragma unroll
         for (int round = 0; round < 2; ++round) {
@@ -471,9 +575,11 @@ template <int FM, int FN, int STAGES, bool BF16> __global__ __launch_bounds__(51
             for (int j = 0; j < FN; ++j)
                 fb[round][j] = *(const i32x4 *)(f + (TM + j * 16) * kStep);
         }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read: the stage may be overwritten
-        if (s + STAGES < to)
-            issue(s + STAGES, stage);
+        if constexpr (DIRECT) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read: the stage may be overwritten
+            if (s + STAGES < to)
+                issue(s + STAGES, stage);
+        }
 #pragma unroll
         for (int round = 0; round < 2; ++round)
 #pragma unroll
@@ -524,42 +630,6 @@ template <int FM, int FN, int STAGES, bool BF16> __global__ __launch_bounds__(51
     }
 }
 
-// ---- rows of any size and alignment -------------------------------------------------
-
-// [rows, K] at any byte to [rows, pitch], pitch = K rounded up to 16, both
-// operands in one launch: one 16-byte chunk of the result a thread.
-struct PadParams {
-    const int8_t *src[2];
-    int8_t *dst[2];
-    int64_t chunks[2];
-    int K, per_row;
-};
-__global__ __launch_bounds__(256) void pad_rows_kernel(const PadParams p)
-{
-    const int64_t stride = (int64_t)gridDim.x * 256;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.chunks[0] + p.chunks[1]; i += stride) {
-        const bool second = i >= p.chunks[0];
-        const int64_t chunk = second ? i - p.chunks[0] : i;
-        // a 64-bit division costs several times a 32-bit one
-        const int64_t row = chunk >> 32 ? chunk / p.per_row : (uint32_t)chunk / (uint32_t)p.per_row;
-        const int k = (int)(chunk - row * p.per_row) * 16;
-        const int8_t *from = (second ? p.src[1] : p.src[0]) + row * p.K + k;
-        u32x4 v = {0, 0, 0, 0};
-        if (k + 16 <= p.K) {
-            __builtin_memcpy(&v, from, 16);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                if (k + j < p.K)
-                    v[j / 4] |= (uint32_t)(uint8_t)from[j] << (8 * (j % 4));
-        }
-        *(u32x4 *)((second ? p.dst[1] : p.dst[0]) + chunk * 16) = v;
-    }
-}
-
-int64_t padded(int64_t K) { return (K + 15) / 16 * 16; }
-size_t padded_bytes(int64_t rows, int64_t K) { return ((size_t)(rows * padded(K)) + 255) / 256 * 256; }
-
 // ---- choice --------------------------------------------------------------------------
 //
 // Which tile: the one whose time, by this model, is least, in us:
@@ -601,11 +671,12 @@ int64_t tiles_of(const FormCost &f, int64_t batch, int64_t M, int64_t N)
     return batch * ((M + f.tm - 1) / f.tm) * ((N + f.tn - 1) / f.tn);
 }
 
-Form choose(int64_t batch, int64_t M, int64_t N, int64_t K)
+// By way of registers there are none left for 256 x 256 outputs.
+Form choose(int64_t batch, int64_t M, int64_t N, int64_t K, bool direct)
 {
-    Form best = kTile256;
-    double least = 0.;
-    for (int f = 0; f < kForms; ++f) {
+    Form best = kTile128;
+    double least = -1.;
+    for (int f = direct ? kTile256 : kTile128; f < kForms; ++f) {
         const FormCost &c = kCosts[f];
         const int64_t tiles = tiles_of(c, batch, M, N);
         if (f >= kRing44 && tiles > kMostRingTiles)
@@ -613,7 +684,7 @@ Form choose(int64_t batch, int64_t M, int64_t N, int64_t K)
         const double rounds = (double)((tiles + c.slots - 1) / c.slots), steps = (double)((K + kStep - 1) / kStep);
         const double alone = rounds * c.alone, busy = (double)tiles / c.slots * c.busy;
         const double cost = steps * (alone > busy ? alone : busy) + rounds * c.each + c.once;
-        if (f == 0 || cost < least) {
+        if (least < 0. || cost < least) {
             best = (Form)f;
             least = cost;
         }
@@ -621,7 +692,7 @@ Form choose(int64_t batch, int64_t M, int64_t N, int64_t K)
     return best;
 }
 
-template <int WM, int WN, int FM, int FN, int STAGES>
+template <int WM, int WN, int FM, int FN, int STAGES, bool DIRECT>
 hipError_t tile(const MatmulParams &p, int slots, bool bf16, hipStream_t s)
 {
     const dim3 grid((unsigned)(p.tiles < slots ? p.tiles : slots)), block(64 * WM * WN);
@@ -631,23 +702,27 @@ hipError_t tile(const MatmulParams &p, int slots, bool bf16, hipStream_t s)
     // (16384 x 5128: 88 us past the caches, 56 by them; 5121: 99 and 58).
     const bool stream = (p.N * (bf16 ? 2 : 4)) % 64 == 0 && (uintptr_t)p.out % 64 == 0;
     if (bf16 && stream)
-        tile_kernel<WM, WN, FM, FN, STAGES, true, true><<<grid, block, 0, s>>>(p);
+        tile_kernel<WM, WN, FM, FN, STAGES, DIRECT, true, true><<<grid, block, 0, s>>>(p);
     else if (bf16)
-        tile_kernel<WM, WN, FM, FN, STAGES, true, false><<<grid, block, 0, s>>>(p);
+        tile_kernel<WM, WN, FM, FN, STAGES, DIRECT, true, false><<<grid, block, 0, s>>>(p);
     else if (stream)
-        tile_kernel<WM, WN, FM, FN, STAGES, false, true><<<grid, block, 0, s>>>(p);
+        tile_kernel<WM, WN, FM, FN, STAGES, DIRECT, false, true><<<grid, block, 0, s>>>(p);
     else
-        tile_kernel<WM, WN, FM, FN, STAGES, false, false><<<grid, block, 0, s>>>(p);
+        tile_kernel<WM, WN, FM, FN, STAGES, DIRECT, false, false><<<grid, block, 0, s>>>(p);
     return hipGetLastError();
 }
 
-template <int FM, int FN, int STAGES> hipError_t ring(const MatmulParams &p, bool bf16, hipStream_t s)
+template <int FM, int FN, int STAGES> hipError_t ring(const MatmulParams &p, bool direct, bool bf16, hipStream_t s)
 {
-    const dim3 grid((unsigned)p.tiles);
-    if (bf16)
-        ring_kernel<FM, FN, STAGES, true><<<grid, dim3(512), 0, s>>>(p);
+    const dim3 grid((unsigned)p.tiles), block(512);
+    if (direct && bf16)
+        ring_kernel<FM, FN, STAGES, true, true><<<grid, block, 0, s>>>(p);
+    else if (direct)
+        ring_kernel<FM, FN, STAGES, true, false><<<grid, block, 0, s>>>(p);
+    else if (bf16)
+        ring_kernel<FM, FN, 1, false, true><<<grid, block, 0, s>>>(p);
     else
-        ring_kernel<FM, FN, STAGES, false><<<grid, dim3(512), 0, s>>>(p);
+        ring_kernel<FM, FN, 1, false, false><<<grid, block, 0, s>>>(p);
     return hipGetLastError();
 }
 
@@ -655,57 +730,43 @@ bool off16(const void *p) { return (uintptr_t)p % 16 != 0; }
 
 }  // namespace
 
-size_t int8_matmul_workspace(int64_t rows_a, int64_t rows_b, int64_t K, bool unaligned)
-{
-    return K % 16 != 0 || unaligned ? padded_bytes(rows_a, K) + padded_bytes(rows_b, K) : 0;
-}
-
 hipError_t launch_int8_matmul(const Int8MatmulArgs &a, hipStream_t s)
 {
-    const int64_t rows_a = a.M * (a.a_shared ? 1 : a.batch), rows_b = a.N * (a.b_shared ? 1 : a.batch);
+    // one right operand for every batch: the batches' rows follow one another
+    const bool joined = a.b_shared && !a.a_shared;
+    const int64_t batch = joined ? 1 : a.batch, M = joined ? a.batch * a.M : a.M;
+    const bool direct = a.K % 16 == 0 && !off16(a.a) && !off16(a.b);
+    const Form f = choose(batch, M, a.N, a.K, direct);
     MatmulParams p{};
     p.a = a.a;
     p.b = a.b;
-    int64_t K = a.K;
-    if (K > 0 && (K % 16 != 0 || off16(a.a) || off16(a.b))) {
-        int8_t *pa = (int8_t *)a.workspace, *pb = pa + padded_bytes(rows_a, K);
-        const int64_t per_row = padded(K) / 16, chunks = (rows_a + rows_b) * per_row;
-        const PadParams pad{{a.a, a.b}, {pa, pb}, {rows_a * per_row, rows_b * per_row}, (int)K, (int)per_row};
-        const int64_t blocks = (chunks + 255) / 256 < (1 << 16) ? (chunks + 255) / 256 : 1 << 16;
-        pad_rows_kernel<<<dim3((unsigned)blocks), dim3(256), 0, s>>>(pad);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess)
-            return e;
-        p.a = pa;
-        p.b = pb;
-        K = padded(K);
-    }
-    const Form f = choose(a.batch, a.M, a.N, K);
     p.a_scale = a.a_scale;
     p.b_scale = a.b_scale;
     p.out = a.out;
-    p.M = a.M;
+    p.M = M;
     p.N = a.N;
-    p.K = (int)K;
-    p.steps = K > 0 ? (int)((K + kStep - 1) / kStep) : 1;
-    p.a_batch = a.a_shared ? 0 : a.M;
+    p.K = (int)a.K;
+    p.steps = a.K > 0 ? (int)((a.K + kStep - 1) / kStep) : 1;
+    p.a_batch = a.a_shared ? 0 : M;
     p.b_batch = a.b_shared ? 0 : a.N;
-    p.tiles_m = (int)((a.M + kCosts[f].tm - 1) / kCosts[f].tm);
+    p.tiles_m = (int)((M + kCosts[f].tm - 1) / kCosts[f].tm);
     p.tiles_n = (int)((a.N + kCosts[f].tn - 1) / kCosts[f].tn);
-    p.tiles = tiles_of(kCosts[f], a.batch, a.M, a.N);
+    p.tiles = tiles_of(kCosts[f], batch, M, a.N);
     switch (f) {
-    case kTile256: return tile<2, 4, 4, 2, 2>(p, kCus, a.bf16, s);
-    case kTile128: return tile<2, 2, 2, 2, 2>(p, 2 * kCus, a.bf16, s);
-    case kTile128Deep: return tile<4, 2, 1, 2, 4>(p, kCus, a.bf16, s);
-    case kRing44: return ring<4, 4, 1>(p, a.bf16, s);
-    case kRing43: return ring<4, 3, 1>(p, a.bf16, s);
-    case kRing34: return ring<3, 4, 1>(p, a.bf16, s);
-    case kRing42: return ring<4, 2, 1>(p, a.bf16, s);
-    case kRing24: return ring<2, 4, 1>(p, a.bf16, s);
-    case kRing22: return ring<2, 2, 2>(p, a.bf16, s);
-    case kRing12: return ring<1, 2, 2>(p, a.bf16, s);
-    case kRing21: return ring<2, 1, 2>(p, a.bf16, s);
-    default: return ring<1, 1, 2>(p, a.bf16, s);
+    case kTile256: return tile<2, 4, 4, 2, 2, true>(p, kCus, a.bf16, s);
+    case kTile128:
+        return direct ? tile<2, 2, 2, 2, 2, true>(p, 2 * kCus, a.bf16, s) : tile<2, 2, 2, 2, 2, false>(p, 2 * kCus, a.bf16, s);
+    case kTile128Deep:
+        return direct ? tile<4, 2, 1, 2, 4, true>(p, kCus, a.bf16, s) : tile<4, 2, 1, 2, 4, false>(p, kCus, a.bf16, s);
+    case kRing44: return ring<4, 4, 1>(p, direct, a.bf16, s);
+    case kRing43: return ring<4, 3, 1>(p, direct, a.bf16, s);
+    case kRing34: return ring<3, 4, 1>(p, direct, a.bf16, s);
+    case kRing42: return ring<4, 2, 1>(p, direct, a.bf16, s);
+    case kRing24: return ring<2, 4, 1>(p, direct, a.bf16, s);
+    case kRing22: return ring<2, 2, 2>(p, direct, a.bf16, s);
+    case kRing12: return ring<1, 2, 2>(p, direct, a.bf16, s);
+    case kRing21: return ring<2, 1, 2>(p, direct, a.bf16, s);
+    default: return ring<1, 1, 2>(p, direct, a.bf16, s);
     }
 }
 

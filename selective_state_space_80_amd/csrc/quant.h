@@ -58,12 +58,9 @@ struct Int8MatmulArgs {
     const int8_t *a, *b;              // [batch or 1, M, K], [batch or 1, N, K]
     const float *a_scale, *b_scale;   // [batch or 1, M], [batch or 1, N]
     void *out;                        // [batch, M, N]
-    void *workspace;                  // int8_matmul_workspace bytes
     int64_t batch, M, N, K;
     bool a_shared, b_shared, bf16;
 };
-// `unaligned`: an operand is not 16-byte aligned.
-size_t int8_matmul_workspace(int64_t rows_a, int64_t rows_b, int64_t K, bool unaligned);
 hipError_t launch_int8_matmul(const Int8MatmulArgs &a, hipStream_t s);
 
 }  // namespace mamba

@@ -66,7 +66,7 @@ mamba_status norm_entry(const void *x, const void *residual, const float *weight
     return launched(mamba::launch_rms_norm(a, (hipStream_t)stream));
 }
 
-constexpr unsigned kMatmulFlags = MAMBA_INT8_SHARED_A | MAMBA_INT8_SHARED_B | MAMBA_INT8_UNALIGNED;
+constexpr unsigned kMatmulFlags = MAMBA_INT8_SHARED_A | MAMBA_INT8_SHARED_B;
 
 int64_t operand_rows(int64_t batch, int64_t rows, unsigned shared) { return shared ? rows : batch * rows; }
 
@@ -174,19 +174,9 @@ mamba_status mamba_quantize_int8(const void *x, int8_t *q, float *scale, int64_t
     return launched(mamba::launch_rms_norm(a, (hipStream_t)stream));
 }
 
-size_t mamba_int8_matmul_workspace_size(int64_t batch, int64_t M, int64_t N, int64_t K, unsigned flags)
-{
-    if (!sizes_ok(batch, M, N) || K < 0 || K > mamba::kMaxInner || (flags & ~kMatmulFlags) != 0 ||
-        !sizes_ok(batch, M, K) || !sizes_ok(batch, N, K) || batch * M * N == 0 || K == 0)
-        return 0;
-    return mamba::int8_matmul_workspace(operand_rows(batch, M, flags & MAMBA_INT8_SHARED_A),
-                                        operand_rows(batch, N, flags & MAMBA_INT8_SHARED_B), K,
-                                        (flags & MAMBA_INT8_UNALIGNED) != 0);
-}
-
 mamba_status mamba_int8_matmul(const int8_t *a, const int8_t *b, const float *a_scale, const float *b_scale,
-                               void *out, void *workspace, size_t workspace_bytes, int64_t batch, int64_t M,
-                               int64_t N, int64_t K, mamba_dtype out_type, unsigned flags, void *stream)
+                               void *out, int64_t batch, int64_t M, int64_t N, int64_t K, mamba_dtype out_type,
+                               unsigned flags, void *stream)
 {
     if (!valid_dtype(out_type))
         return MAMBA_ERR_DTYPE;
@@ -205,22 +195,16 @@ mamba_status mamba_int8_matmul(const int8_t *a, const int8_t *b, const float *a_
         return MAMBA_ERR_ALIGN;
     const int64_t rows_a = operand_rows(batch, M, flags & MAMBA_INT8_SHARED_A),
                   rows_b = operand_rows(batch, N, flags & MAMBA_INT8_SHARED_B);
-    // whether an operand needs the workspace shows in its address, with or without the flag
-    const size_t need = K == 0 ? 0 : mamba::int8_matmul_workspace(rows_a, rows_b, K, !aligned(a, 16) || !aligned(b, 16));
-    if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
-        return MAMBA_ERR_WORKSPACE;
-    const Range ro = rng(out, (size_t)(batch * M * N) * esize(out_type)), rw = rng(workspace, need);
+    const Range ro = rng(out, (size_t)(batch * M * N) * esize(out_type));
     const Range ins[] = {rng(a, (size_t)(rows_a * K)), rng(b, (size_t)(rows_b * K)),
                          rng(a_scale, (size_t)rows_a * 4), rng(b_scale, (size_t)rows_b * 4)};
     for (const Range &r : ins)
-        if (overlap(ro, r) || overlap(rw, r))
+        if (overlap(ro, r))
             return MAMBA_ERR_ALIAS;
-    if (overlap(ro, rw))
-        return MAMBA_ERR_ALIAS;
     mamba_status st = device_ok();
     if (st != MAMBA_OK)
         return st;
-    mamba::Int8MatmulArgs args{a, b, a_scale, b_scale, out, workspace, batch, M, N, K,
+    mamba::Int8MatmulArgs args{a, b, a_scale, b_scale, out, batch, M, N, K,
                                (flags & MAMBA_INT8_SHARED_A) != 0, (flags & MAMBA_INT8_SHARED_B) != 0,
                                out_type == MAMBA_BF16};
     return launched(mamba::launch_int8_matmul(args, (hipStream_t)stream));
