@@ -146,18 +146,25 @@ def status_string(status: int) -> str:
         return STATUS_NAMES.get(int(status), "unknown")
 
 
+_torch_module = None
+_io_types = {}  # torch dtype -> mamba_dtype, filled when torch is first used
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _io_types.update({torch.float32: MAMBA_F32, torch.bfloat16: MAMBA_BF16})
+        _torch_module = torch
+    return _torch_module
 
 
 def _io_dtype(t) -> int:
-    torch = _torch()
-    if t.dtype == torch.float32:
-        return MAMBA_F32
-    if t.dtype == torch.bfloat16:
-        return MAMBA_BF16
-    raise TypeError(f"I/O tensors must be float32 or bfloat16, got {t.dtype}")
+    _torch()
+    io = _io_types.get(t.dtype)
+    if io is None:
+        raise TypeError(f"I/O tensors must be float32 or bfloat16, got {t.dtype}")
+    return io
 
 
 def _ptr(t):
@@ -588,13 +595,15 @@ def ssd_scan_fwd(x, dt, A, Bm, Cm, dt_bias=None, Dskip=None, z=None, h0=None,
 def _is(t, shape, dtype, index):
     """A contiguous tensor of this shape and dtype on GPU `index` (the quick
     form of _check, which says what is wrong with one that is not)."""
-    return (t.shape == shape and t.dtype == dtype and t.get_device() == index
+    return (t.dtype is dtype and t.shape == shape and t.get_device() == index
             and t.is_contiguous())
 
 
-def _rows(x):
+def _rows(shape):
+    if len(shape) == 2:
+        return shape[0]
     rows = 1
-    for n in x.shape[:-1]:
+    for n in shape[:-1]:
         rows *= n
     return rows
 
@@ -603,9 +612,9 @@ def _norm_arguments(x, weight, residual, residual_out):
     """Checks shared by the two forward norms; returns (rows, D, residual's
     element type, residual_out)."""
     torch = _torch()
-    if x.dim() < 1:
-        raise ValueError("x has no axis to normalise")
     shape, index = x.shape, x.get_device()
+    if not shape:
+        raise ValueError("x has no axis to normalise")
     D = shape[-1]
     if not (x.is_contiguous() and _is(weight, (D,), torch.float32, index)):
         _check(x, "x", shape)
@@ -613,9 +622,9 @@ def _norm_arguments(x, weight, residual, residual_out):
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out needs residual")
-        return _rows(x), D, 0, None
+        return _rows(shape), D, 0, None
     res_t = residual.dtype
-    if res_t != torch.float32 and res_t != x.dtype:
+    if res_t is not torch.float32 and res_t is not x.dtype:
         raise TypeError(f"residual must be float32 or {x.dtype}, got {res_t}")
     if not _is(residual, shape, res_t, index):
         _check(residual, "residual", shape, device=x.device)
@@ -623,7 +632,7 @@ def _norm_arguments(x, weight, residual, residual_out):
         residual_out = torch.empty_like(residual)
     elif not _is(residual_out, shape, res_t, index):
         _check(residual_out, "residual_out", shape, res_t, x.device)
-    return _rows(x), D, _io_dtype(residual), residual_out
+    return _rows(shape), D, _io_dtype(residual), residual_out
 
 
 def rms_norm(x, weight, residual=None, eps=1e-5, out=None, residual_out=None):
@@ -658,7 +667,7 @@ def rms_norm_int8(x, weight, residual=None, eps=1e-5, out=None, scale=None, resi
     else:
         _check(out, "out", x.shape, torch.int8, x.device)
     if scale is None:
-        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        scale = weight.new_empty(x.shape[:-1])
     else:
         _check(scale, "scale", x.shape[:-1], torch.float32, x.device)
     st = lib.mamba_rms_norm_int8(x.data_ptr(), _addr(residual), weight.data_ptr(), out.data_ptr(),
@@ -694,7 +703,7 @@ def rms_norm_bwd(dy, h, weight, dresidual_out=None, eps=1e-5, workspace=None):
         _check(weight, "weight", (D,), torch.float32, dev)
     if dresidual_out is not None and not _is(dresidual_out, shape, h_t, index):
         _check(dresidual_out, "dresidual_out", shape, h_t, dev)
-    M = _rows(dy)
+    M = _rows(shape)
     dx = torch.empty_like(dy)
     dresidual = None if h_t == dy.dtype else torch.empty_like(h)
     dweight = torch.empty_like(weight)
@@ -730,13 +739,14 @@ def quantize_int8(x, channel_major=False, out=None, scale=None):
         if len(shape) < 1:
             raise ValueError("x has no axis to quantise")
         lead, K = shape[:-1], shape[-1]
-        B, L = 1, _rows(x)
+        B, L = 1, _rows(shape)
     if out is None:
-        out = torch.empty((*lead, K), dtype=torch.int8, device=dev)
+        out = (x.new_empty((*lead, K), dtype=torch.int8) if channel_major
+               else torch.empty_like(x, dtype=torch.int8))
     else:
         _check(out, "out", (*lead, K), torch.int8, dev)
     if scale is None:
-        scale = torch.empty(lead, dtype=torch.float32, device=dev)
+        scale = x.new_empty(lead, dtype=torch.float32)
     else:
         _check(scale, "scale", lead, torch.float32, dev)
     st = lib.mamba_quantize_int8(x.data_ptr(), out.data_ptr(), scale.data_ptr(), B, L, K,
@@ -759,31 +769,31 @@ def int8_matmul(a, b, a_scale, b_scale, out_dtype=None, out=None):
     a projection; with the weight as `a`, its channel-major form."""
     torch = _torch()
     lib = load_library()
-    if a.dim() not in (2, 3) or b.dim() not in (2, 3):
-        raise ValueError(f"a and b are 2-D or 3-D, got {a.dim()}-D and {b.dim()}-D")
-    dev = a.device
-    M, K = a.shape[-2:]
-    N = b.shape[-2]
-    if a.dim() == 2 and b.dim() == 2:
-        batch, lead, flags = 1, (), 0
+    a_shape, b_shape = a.shape, b.shape
+    a_dim, b_dim = len(a_shape), len(b_shape)
+    if a_dim not in (2, 3) or b_dim not in (2, 3):
+        raise ValueError(f"a and b are 2-D or 3-D, got {a_dim}-D and {b_dim}-D")
+    M, K, N = a_shape[-2], a_shape[-1], b_shape[-2]
+    if a_dim == 2 and b_dim == 2:
+        batch, flags = 1, 0
+        a_rows, b_rows, out_shape = (M,), (N,), (M, N)
     else:
-        batch = a.shape[0] if a.dim() == 3 else b.shape[0]
-        lead = (batch,)
-        flags = ((INT8_SHARED_A if a.dim() == 2 else 0) | (INT8_SHARED_B if b.dim() == 2 else 0))
+        batch = a_shape[0] if a_dim == 3 else b_shape[0]
+        flags = (INT8_SHARED_A if a_dim == 2 else 0) | (INT8_SHARED_B if b_dim == 2 else 0)
+        a_rows = (M,) if a_dim == 2 else (batch, M)
+        b_rows = (N,) if b_dim == 2 else (batch, N)
+        out_shape = (batch, M, N)
     index, i8, f32 = a.get_device(), torch.int8, torch.float32
-    a_lead = lead if a.dim() == 3 else ()
-    b_lead = lead if b.dim() == 3 else ()
-    if not (a.dtype == i8 and a.is_contiguous() and _is(b, (*b_lead, N, K), i8, index)
-            and _is(a_scale, (*a_lead, M), f32, index) and _is(b_scale, (*b_lead, N), f32, index)):
-        _check(a, "a", (*a_lead, M, K), i8)
-        _check(b, "b", (*b_lead, N, K), i8, dev)
-        _check(a_scale, "a_scale", (*a_lead, M), f32, dev)
-        _check(b_scale, "b_scale", (*b_lead, N), f32, dev)
+    if not (a.dtype is i8 and a.is_contiguous() and _is(b, (*b_rows, K), i8, index)
+            and _is(a_scale, a_rows, f32, index) and _is(b_scale, b_rows, f32, index)):
+        _check(a, "a", (*a_rows, K), i8)
+        _check(b, "b", (*b_rows, K), i8, a.device)
+        _check(a_scale, "a_scale", a_rows, f32, a.device)
+        _check(b_scale, "b_scale", b_rows, f32, a.device)
     if out is None:
-        out = torch.empty((*lead, M, N), dtype=torch.bfloat16 if out_dtype is None else out_dtype,
-                          device=dev)
+        out = a.new_empty(out_shape, dtype=torch.bfloat16 if out_dtype is None else out_dtype)
     else:
-        _check(out, "out", (*lead, M, N), out_dtype, dev)
+        _check(out, "out", out_shape, out_dtype, a.device)
     st = lib.mamba_int8_matmul(a.data_ptr(), b.data_ptr(), a_scale.data_ptr(), b_scale.data_ptr(),
                                out.data_ptr(), batch, M, N, K, _io_dtype(out), flags, _raw_stream(a))
     if st:
