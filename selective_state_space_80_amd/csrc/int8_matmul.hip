@@ -196,7 +196,7 @@ __device__ __forceinline__ Share xcd_share(int64_t tiles, int xcd)
 // matrix units to 62 % at 1.85 GHz on random data (2.45 POP/s at 8192^3, where
 // the library's 8-bit product reaches 2.14).  With zeros as data the clock
 // stays at 2.4 GHz; without any loads, on random data, the products alone
-// reach 2.75.  LDS has no bank conflicts and is read a quarter of the time.
+// reach 2.75.  LDS is read a quarter of the time and without bank conflicts.
 // Of a tile's end, 5 us of the model below, most is arithmetic (3.5
 // instructions an output) and the stores' way to memory: whole lines past the
 // caches, issued without branches, and not waited for by the next tile's first
