@@ -50,9 +50,12 @@ __device__ const u32x4 kZeros = {0, 0, 0, 0};
 // 16 bytes a lane from memory to LDS: lane l's go to lds + 16 l.  The first
 // form takes a scalar base and a 32-bit offset a lane, the second a pointer a
 // lane.  Completion is counted by vmcnt; the kernels wait for it themselves.
+// The load may not follow its m0 at once (1 wait state), nor a vector
+// instruction that wrote its scalar base (5), which the compiler does not see
+// to inside an asm statement.
 __device__ __forceinline__ void load_lds(uint32_t lds, const int8_t *base, uint32_t offset)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base)
                  : "memory");
 }
 __device__ __forceinline__ void load_lds(uint32_t lds, const int8_t *ptr)

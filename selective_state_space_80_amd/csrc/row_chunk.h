@@ -124,7 +124,7 @@ __device__ __forceinline__ RowScale row_scale(uint32_t top)
 {
     RowScale r;
     const float t = __uint_as_float(top);
-    r.raise = t < 0x1p-120f ? 0x1p64f : 1.f;
+    r.raise = top != 0 && t < 0x1p-120f ? 0x1p64f : 1.f;
     r.scale = t / 127.f;
     r.mul = top == 0 ? 0.f : 127.f / (t * r.raise);
     r.mask = 0xffffffffu;
