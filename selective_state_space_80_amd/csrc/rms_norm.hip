@@ -201,6 +201,10 @@ template <bool XBF, int RES, int MODE> hipError_t pick(const NormParams &p, hipS
         default: return start<XBF, RES, MODE, 64, 8, false>(p, 256, s);
         }
     }
+    // Of a shared row a lane takes one chunk up to 512, then two: workgroups of
+    // 1024 lanes leave a CU too few rows at once (bf16, in us: 16384 x 5120 105
+    // with two and 130 with one; 8192 x 8192 84 and 93).  Four only where two
+    // no longer cover the row.
     const int nc = chunks <= 512 ? 1 : chunks <= 2048 ? 2 : 4;
     const int lanes = (chunks + nc - 1) / nc;
     const int threads = (lanes + 63) / 64 * 64;

@@ -256,6 +256,12 @@ template <bool XBF, bool HF32, bool DRES> hipError_t pick(const BwdParams &p, in
         return start<XBF, HF32, DRES, 64, 1, false>(p, groups, 256, s);
     if (chunks <= 128)
         return start<XBF, HF32, DRES, 64, 2, false>(p, groups, 256, s);
+    // More chunks a lane mean fewer waves with more registers and sums each, so
+    // the fewest that the row allows (with dres, four sets of tensors in turn so that
+    // they come from memory, in us: 16384 x 2560 68 with one and 84 with
+    // two, 4096 x 10240 83 with two and 101 with four), except that rows of 513
+    // to 1024 chunks take two, as in the forward pass (4096 x 8192 57 with two and
+    // 61 with one; 8192 x 5120 72 and 71).
     const int nc = chunks <= 512 ? 1 : chunks <= 2048 ? 2 : 4;
     const int lanes = (chunks + nc - 1) / nc;
     const int threads = (lanes + 63) / 64 * 64;
