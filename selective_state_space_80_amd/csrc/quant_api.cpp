@@ -148,7 +148,8 @@ mamba_status mamba_quantize_int8(const void *x, int8_t *q, float *scale, int64_t
         return MAMBA_ERR_SHAPE;
     if ((channel_major != 0 && channel_major != 1) || (!channel_major && K > mamba::kMaxNormWidth))
         return MAMBA_ERR_UNSUPPORTED;
-    // channel-major: a block has 16 tokens or more (fewer only in launches of few blocks)
+    // channel-major: a block has 16 tokens or more; fewer only in launches of few blocks
+    // and of so many channels that as many blocks would need more memory than there is
     if (channel_major ? L >= kMaxBlocks * 16 || B * ((L + 15) / 16) >= kMaxBlocks : B * L >= max_rows(K))
         return MAMBA_ERR_SHAPE;
     if (B * L == 0)

@@ -12,11 +12,16 @@
 // store, and 16 lanes' stores are 64 neighbouring bytes: the transposition
 // needs no LDS.
 //
-// Bound by memory.  8 x 5120 x 2048 bf16 (252 MB) takes 45 us (5.5 TB/s) with
+// Fewer tiles, or more channels than the registers of 64-byte tiles hold, take
+// tiles of 32 or 16 bytes (PARTS); sequences shorter than 16 bytes have a kernel
+// of their own.
+//
+// Bound by memory.  8 x 5120 x 2048 bf16 (252 MB) takes 44 us (5.7 TB/s) with
 // the input in the last-level cache, where a scan has just left it, and 73 us
 // from memory: there is room for one workgroup a CU, so its loads do not
 // overlap its stores (64 without the stores, 70 and 99 us before neighbouring
-// tiles shared an XCD's L2).  1 x 1536 x 131072 bf16 (604 MB) takes 143 us.
+// tiles shared an XCD's L2).  1 x 1536 x 131072 bf16 (604 MB) takes 143 us;
+// 64 x 5120 x 4 bf16 3.5 us, bound by its launch and its two dependent waits.
 #include <hip/hip_runtime.h>
 
 #include "quant.h"
@@ -49,9 +54,9 @@ template <bool BF16> struct Tokens {
     }
 };
 
-// Sequences shorter than 16 bytes, and fewer than four channels (SHORT), are
-// read token by token, the index held below the `left` there are; otherwise the
-// last 16 bytes are moved back to end with the sequence.
+// Of fewer than four channels (SHORT), tokens are read one by one, the index
+// held below the `left` there are; otherwise the last 16 bytes are moved back
+// to end with the sequence.
 template <bool BF16, bool SHORT>
 __device__ __forceinline__ Tokens<BF16> load_tokens(const typename Elem<BF16>::T *channel, int left)
 {
@@ -84,15 +89,23 @@ template <bool BF16> __device__ __forceinline__ uint32_t max_abs(uint32_t top, u
     }
 }
 
+// q of four neighbouring channels of one token.
+__device__ __forceinline__ uint32_t pack4(const uint32_t (&byte)[4])
+{
+    const uint32_t lo = __builtin_amdgcn_perm(byte[1], byte[0], 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(byte[3], byte[2], 0x0c0c0400u);
+    return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+}
+
 // HELD groups of channels stay in registers; 0: they are more than that, and
 // the second pass reads them again.
-template <bool BF16, int PARTS, int HELD, bool SHORT>
-__global__ __launch_bounds__(kMostThreads / 4 * PARTS) void quantize_channel_kernel(const ChannelParams p)
+template <bool BF16, int PARTS, int THREADS, int HELD, bool SHORT>
+__global__ __launch_bounds__(THREADS) void quantize_channel_kernel(const ChannelParams p)
 {
     using T = typename Elem<BF16>::T;
     using Tok = Tokens<BF16>;
     constexpr int kTok = Tok::kCount, kTile = PARTS * kTok;
-    __shared__ uint32_t tops[kMostThreads / 256 * PARTS][PARTS][4];
+    __shared__ uint32_t tops[THREADS / 64][PARTS][4];
     __shared__ RowScale rows[kTile];
     __shared__ int special;  // a row is raised, or not finite
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n_waves = blockDim.x >> 6;
@@ -158,11 +171,13 @@ __global__ __launch_bounds__(kMostThreads / 4 * PARTS) void quantize_channel_ker
                     top[i] = max_abs<BF16>(top[i], t[r].v[i]);
         }
     }
-    // over the lanes of the same tokens (lane % 4), then over the waves
+    // over the lanes of the same tokens (lane % PARTS), then over the waves
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if constexpr (PARTS == 2)
-            top[i] = max_abs<BF16>(top[i], dpp<0x122>(top[i]));  // row rotated by 2
+        if constexpr (PARTS == 1)
+            top[i] = max_abs<BF16>(top[i], dpp<0x121>(top[i]));  // row rotated by 1
+        if constexpr (PARTS <= 2)
+            top[i] = max_abs<BF16>(top[i], dpp<0x122>(top[i]));  // by 2
         top[i] = max_abs<BF16>(top[i], dpp<0x124>(top[i]));  // by 4
         top[i] = max_abs<BF16>(top[i], dpp<0x128>(top[i]));  // by 8
         top[i] = max_abs<BF16>(top[i], (uint32_t)__shfl_xor((int)top[i], 16));
@@ -212,9 +227,7 @@ __global__ __launch_bounds__(kMostThreads / 4 * PARTS) void quantize_channel_ker
                     v *= rows[part * kTok + i].raise;
                 byte[r] = __float_as_uint(fmaf(v, mul[i], 12582912.f));
             }
-            const uint32_t lo = __builtin_amdgcn_perm(byte[1], byte[0], 0x0c0c0400u);
-            const uint32_t hi = __builtin_amdgcn_perm(byte[3], byte[2], 0x0c0c0400u);
-            uint32_t w = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+            uint32_t w = pack4(byte);
             if (any_special)
                 w &= rows[part * kTok + i].mask;
             int8_t *o = q + i * p.K + c;
@@ -241,42 +254,186 @@ __global__ __launch_bounds__(kMostThreads / 4 * PARTS) void quantize_channel_ker
     }
 }
 
-template <bool BF16, int PARTS> hipError_t start(const QuantChannelArgs &a, hipStream_t s)
+// Sequences of L tokens that are shorter than 16 bytes: a workgroup takes one,
+// and a thread all tokens of four neighbouring channels, which lie one after
+// another.  Two groups of channels stay in registers; where there are more
+// (MANY), the second pass reads them again.
+template <bool BF16, int L, bool MANY>
+__global__ __launch_bounds__(kMostThreads) void quantize_short_kernel(const ChannelParams p)
 {
-    constexpr int kTok = Tokens<BF16>::kCount, kMostGroup = kMostThreads;
+    using T = typename Elem<BF16>::T;
+    constexpr int kHeld = 2, kWords = (BF16 ? 2 : 4) * L;
+    struct Piece {
+        uint32_t v[kWords];
+        __device__ __forceinline__ float get(int e) const
+        {
+            if constexpr (BF16)
+                return __uint_as_float(e % 2 ? v[e / 2] & 0xffff0000u : v[e / 2] << 16);
+            else
+                return __uint_as_float(v[e]);
+        }
+    };
+    __shared__ uint32_t tops[kMostThreads / 64][L];
+    __shared__ RowScale rows[L];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n_waves = blockDim.x >> 6;
+    const int64_t b = blockIdx.x;
+    const int64_t group = (int64_t)blockDim.x * kChan;
+    const T *x = (const T *)p.x + b * p.K * L;
+    // the last four channels are moved back to end with K
+    auto channel = [&](int64_t g) {
+        const int64_t c = g * group + (int64_t)threadIdx.x * kChan;
+        return c + kChan <= p.K ? c : p.K - kChan;
+    };
+    auto load = [&](Piece &t, int64_t g) { __builtin_memcpy(t.v, x + channel(g) * L, kWords * 4); };
+    const int64_t groups = (p.K + group - 1) / group;
+
+    uint32_t top[L];
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+        top[i] = 0;
+    auto take = [&](const Piece &t) {
+#pragma unroll
+        for (int e = 0; e < kChan * L; ++e)
+            top[e % L] = umax(top[e % L], abs_bits(t.get(e)));
+    };
+    Piece held[kHeld];
+#pragma unroll
+    for (int g = 0; g < kHeld; ++g)
+        load(held[g], g);
+#pragma unroll
+    for (int g = 0; g < kHeld; ++g)
+        take(held[g]);
+    if constexpr (MANY) {
+#pragma unroll 2
+        for (int64_t g = kHeld; g < groups; ++g) {
+            Piece t;
+            load(t, g);
+            take(t);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+        const uint32_t t = lane_max<64>(top[i]);
+        if (lane == 0)
+            tops[wave][i] = t;
+    }
+    __syncthreads();
+    if (threadIdx.x < L) {
+        uint32_t t = 0;
+        for (int w = 0; w < n_waves; ++w)
+            t = umax(t, tops[w][threadIdx.x]);
+        const RowScale rs = row_scale(t);
+        rows[threadIdx.x] = rs;
+        p.scale[b * L + threadIdx.x] = rs.scale;
+    }
+    __syncthreads();
+    int8_t *q = p.q + b * L * p.K;
+    auto put = [&](const Piece &t, int64_t g) {
+        const int64_t c = channel(g);
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            uint32_t byte[kChan];
+#pragma unroll
+            for (int r = 0; r < kChan; ++r)
+                byte[r] = __float_as_uint(fmaf(t.get(r * L + i) * rows[i].raise, rows[i].mul, 12582912.f));
+            const uint32_t w = pack4(byte) & rows[i].mask;
+            __builtin_memcpy(q + i * p.K + c, &w, 4);
+        }
+    };
+#pragma unroll
+    for (int g = 0; g < kHeld; ++g)
+        put(held[g], g);
+    if constexpr (MANY) {
+        for (int64_t g = kHeld; g < groups; ++g) {
+            Piece t;
+            load(t, g);
+            put(t, g);
+        }
+    }
+}
+
+template <bool BF16, int L> hipError_t start_short(const QuantChannelArgs &a, hipStream_t s)
+{
+    if constexpr (L < Tokens<BF16>::kCount - 1) {
+        if (a.L != L)
+            return start_short<BF16, L + 1>(a, s);
+    }
+    const ChannelParams p{a.x, a.q, a.scale, a.L, a.K, 1};
+    const int64_t quads = (a.K + kChan - 1) / kChan;
+    const bool many = quads > 2 * kMostThreads;
+    const int64_t threads = many ? kMostThreads : ((quads + 1) / 2 + 63) / 64 * 64;
+    const dim3 grid((unsigned)a.B), block((unsigned)threads);
+    if (many)
+        quantize_short_kernel<BF16, L, true><<<grid, block, 0, s>>>(p);
+    else if constexpr (L > 1)  // single tokens of fewer channels are rows of the token-major form
+        quantize_short_kernel<BF16, L, false><<<grid, block, 0, s>>>(p);
+    return hipGetLastError();
+}
+
+// The form that holds `groups` groups, of those that calls reach.
+template <bool BF16, int PARTS, int THREADS, int HELD>
+void start_held(int64_t groups, dim3 grid, dim3 block, const ChannelParams &p, hipStream_t s)
+{
+    constexpr int kFewest = THREADS / PARTS * kChan == kMostThreads ? 1 : kMaxHeld / 2 + 1;
+    if constexpr (HELD > kFewest) {
+        if (groups < HELD)
+            return start_held<BF16, PARTS, THREADS, HELD - 1>(groups, grid, block, p, s);
+    }
+    quantize_channel_kernel<BF16, PARTS, THREADS, HELD, false><<<grid, block, 0, s>>>(p);
+}
+
+template <bool BF16, int PARTS, int THREADS> hipError_t start(const QuantChannelArgs &a, hipStream_t s)
+{
+    constexpr int kTok = Tokens<BF16>::kCount, kMostGroup = THREADS / PARTS * kChan;
     const int64_t tiles = (a.L + PARTS * kTok - 1) / (PARTS * kTok);
     const ChannelParams p{a.x, a.q, a.scale, a.L, a.K, tiles};
     // as few groups as there can be, then as few waves as those need
     const int64_t groups = (a.K + kMostGroup - 1) / kMostGroup;
     const int64_t threads = (a.K + groups * kChan - 1) / (groups * kChan) * PARTS;
     const dim3 grid((unsigned)(a.B * tiles)), block((unsigned)((threads + 63) / 64 * 64));
-    if (a.L < kTok || a.K < kChan) {
-        quantize_channel_kernel<BF16, PARTS, 0, true><<<grid, block, 0, s>>>(p);
-        return hipGetLastError();
-    }
-    switch (groups) {
-    case 1: quantize_channel_kernel<BF16, PARTS, 1, false><<<grid, block, 0, s>>>(p); break;
-    case 2: quantize_channel_kernel<BF16, PARTS, 2, false><<<grid, block, 0, s>>>(p); break;
-    case 3: quantize_channel_kernel<BF16, PARTS, 3, false><<<grid, block, 0, s>>>(p); break;
-    case 4: quantize_channel_kernel<BF16, PARTS, 4, false><<<grid, block, 0, s>>>(p); break;
-    case 5: quantize_channel_kernel<BF16, PARTS, 5, false><<<grid, block, 0, s>>>(p); break;
-    case kMaxHeld: quantize_channel_kernel<BF16, PARTS, kMaxHeld, false><<<grid, block, 0, s>>>(p); break;
-    default: quantize_channel_kernel<BF16, PARTS, 0, false><<<grid, block, 0, s>>>(p); break;
+    if (groups <= kMaxHeld) {
+        start_held<BF16, PARTS, THREADS, kMaxHeld>(groups, grid, block, p, s);
+    } else if constexpr (PARTS == 4) {
+        quantize_channel_kernel<BF16, PARTS, THREADS, 0, false><<<grid, block, 0, s>>>(p);
     }
     return hipGetLastError();
+}
+
+template <bool BF16> hipError_t dispatch(const QuantChannelArgs &a, hipStream_t s)
+{
+    constexpr int kTok = Tokens<BF16>::kCount;
+    constexpr int64_t kHeldChannels = kMaxHeld * kMostThreads;
+    const int64_t tiles = a.B * ((a.L + 4 * kTok - 1) / (4 * kTok));
+    if (a.K < kChan) {
+        const ChannelParams p{a.x, a.q, a.scale, a.L, a.K, (a.L + 4 * kTok - 1) / (4 * kTok)};
+        quantize_channel_kernel<BF16, 4, kMostThreads, 0, true><<<dim3((unsigned)tiles), dim3(64), 0, s>>>(p);
+        return hipGetLastError();
+    }
+    // Whole tiles take over from 16 bytes on (64 x 5120 x 7 bf16 4.6 us so and
+    // 64 x 5120 x 8 6.1; x 7 token by token 31.6).
+    if (a.L < kTok)
+        return start_short<BF16, 1>(a, s);
+    // Few tiles leave most CUs idle: below half a tile a CU, tiles of 16 bytes by a
+    // quarter of the threads (from memory, bf16 in us: 1 x 5120 x 1000 11.3, in tiles
+    // of 32 bytes 14.1; 2 x 5120 x 1024 13.2 and 17.2; but 1 x 5120 x 8000, 250
+    // tiles, 44 so and 26 in tiles of 64 bytes).
+    if (a.K <= kHeldChannels)
+        return tiles < 128 ? start<BF16, 1, kMostThreads / 4>(a, s) : start<BF16, 4, kMostThreads>(a, s);
+    // More channels are held by smaller tiles of as many threads, up to the most
+    // that registers hold; read twice instead, 1 x 20000 x 1000 bf16 takes 63 us
+    // (30 so), 8 x 8192 x 2048 168 (148), 2 x 16384 x 2048 77 (48; fp32 126 and 132).
+    if (a.K <= 2 * kHeldChannels)
+        return start<BF16, 2, kMostThreads>(a, s);
+    if (a.K <= 4 * kHeldChannels)
+        return start<BF16, 1, kMostThreads>(a, s);
+    return start<BF16, 4, kMostThreads>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_quantize_channel_major(const QuantChannelArgs &a, hipStream_t s)
 {
-    // With fewer tiles than half the CUs, tiles of half the tokens by half the
-    // threads: 1 x 5120 x 1000 bf16 13.9 us instead of 16.6, 64 x 5120 x 8 8.1
-    // instead of 10.0; the other way 8 x 5120 x 2048 73 instead of 80.
-    const int64_t per_tile = 4 * (a.bf16 ? Tokens<true>::kCount : Tokens<false>::kCount);
-    if (a.B * ((a.L + per_tile - 1) / per_tile) < 128)
-        return a.bf16 ? start<true, 2>(a, s) : start<false, 2>(a, s);
-    return a.bf16 ? start<true, 4>(a, s) : start<false, 4>(a, s);
+    return a.bf16 ? dispatch<true>(a, s) : dispatch<false>(a, s);
 }
 
 }  // namespace mamba

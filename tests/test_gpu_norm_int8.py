@@ -204,6 +204,44 @@ def test_quantize_channel_major(B, K, L, io):
         assert torch.equal(q, q2) and torch.equal(s, s2)
 
 
+@pytest.mark.parametrize("L", [2, 3, 4, 5, 6, 7])
+@pytest.mark.parametrize("B,K", [(1, 1), (3, 4), (2, 5), (4, 259), (2, 4093), (130, 1536), (2, 5120), (1, 8201),
+                                 (1, 40001)])
+@pytest.mark.parametrize("io", TYPES)
+def test_quantize_channel_major_of_few_tokens(B, K, L, io):
+    import torch
+    import selective_state_space_80_amd as mamba
+    x = _draw((B, K, L), io, 52 + K + L, 2.0)
+    q, s = mamba.quantize_int8(x, channel_major=True)
+    y = x.transpose(1, 2).contiguous()
+    _check_int8(q, s, y.double(), 0.0, f"quantize channel-major {B} {K} {L} {io}")
+    if K <= 32768:
+        q2, s2 = mamba.quantize_int8(y)
+        assert torch.equal(q, q2) and torch.equal(s, s2)
+
+
+@pytest.mark.parametrize("B,K,L", [(40, 100, 3), (40, 5000, 5), (3, 9001, 6), (200, 70, 9), (200, 1030, 21),
+                                   (3, 6145, 100), (2, 8192, 515), (2, 12289, 75), (1, 20000, 130),
+                                   (1, 24577, 70), (2, 32768, 33)])
+@pytest.mark.parametrize("io", TYPES)
+def test_quantize_channel_major_special_tokens(B, K, L, io):
+    """Tokens of zeros, of the smallest numbers, and with a NaN or an infinity
+    anywhere, among ordinary ones, in every tiling: the bits of the token-major call."""
+    import torch
+    import selective_state_space_80_amd as mamba
+    y = _draw((B * L, K), io, 53 + K + L)
+    n = torch.arange(B * L, device="cuda")
+    y[n % 11 == 1] = 0.0
+    y[n % 11 == 3] *= 1e-38
+    y[n % 11 == 5, K - 1] = float("nan")
+    y[n % 11 == 7, K // 3] = float("inf")
+    y[n % 11 == 9] = torch.finfo(_t(io)).min
+    y = y.view(B, L, K)
+    q, s = mamba.quantize_int8(y.transpose(1, 2).contiguous(), channel_major=True)
+    q2, s2 = mamba.quantize_int8(y)
+    assert torch.equal(q, q2) and torch.equal(s.view(torch.int32), s2.view(torch.int32))
+
+
 @pytest.mark.parametrize("K", [5, 100, 2560, 6000])
 @pytest.mark.parametrize("io", TYPES)
 @pytest.mark.parametrize("form", ["token", "channel", "norm"])
