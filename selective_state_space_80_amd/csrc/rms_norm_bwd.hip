@@ -1,7 +1,7 @@
 // Gradient of the root-mean-square norm with the residual's addition.
 //
 // With h the stored sum, r = 1 / sqrt(mean(h^2) + eps) and y = h r w:
-//   dh = r (w dy) - h r^3 mean(w dy h) + dres_out      (dx, and the residual's gradient)
+//   dh = r (w dy - (h r) r mean(w dy h)) + dres_out      (dx, and the residual's gradient)
 //   dw = sum over rows of dy h r
 // Both row sums (h^2 and w dy h) need no r, so one pass over the row gives
 // them together; dh follows from the registers.  dw is summed over the rows a
@@ -139,7 +139,7 @@ __global__ __launch_bounds__(LANES ? 256 : NC == 1 ? 512 : 1024) void rms_norm_b
             parity ^= 1;
         }
         const float r = 1.f / sqrtf(fmaf(s, p.inv_d, p.eps));
-        const float k3 = r * r * r * (t * p.inv_d);
+        const float c = t * r * p.inv_d;
         const bool past = kRows > 1 && row + sub >= p.M;
         const int64_t mine = kRows > 1 ? row + sub : row;
 #pragma unroll
@@ -153,8 +153,9 @@ __global__ __launch_bounds__(LANES ? 256 : NC == 1 ? 512 : 1024) void rms_norm_b
             float dh[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                acc[j][i] = fmaf(g[k][i] * r, h[k][i], acc[j][i]);
-                dh[i] = fmaf(r * w[k][i], g[k][i], -k3 * h[k][i]);
+                const float hr = h[k][i] * r;  // normalised: r^3 passes the fp32 range before it does
+                acc[j][i] = fmaf(g[k][i], hr, acc[j][i]);
+                dh[i] = r * fmaf(g[k][i], w[k][i], -c * hr);
                 if constexpr (DRES)
                     dh[i] += d[k][i];
             }

@@ -162,6 +162,26 @@ def test_norm_gradient_against_differences():
         assert abs(g["dweight"][j].item() - want) <= 5e-5, j
 
 
+@pytest.mark.parametrize("D", [5, 60, 700, 2560, 9000, 20000])
+def test_norm_gradient_of_small_rows(D):
+    """Rows so small that 1/rms has no cube in fp32, and zero rows beside them."""
+    import torch
+    import selective_state_space_80_amd as mamba
+    M, eps = 6, 1e-29
+    h, dy = _draw((M, D), "f32", 35 + D, 1e-14), _draw((M, D), "f32", 36 + D)
+    h[2] = 0.0
+    w = 1.0 + 0.1 * _draw((D,), "f32", 37 + D)
+    g = mamba.rms_norm_bwd(dy, h, w, eps=eps)
+    hd, gd, wd = h.double(), dy.double(), w.double()
+    r = 1.0 / (hd.square().mean(-1, keepdim=True) + eps).sqrt()
+    along = wd * gd * hd
+    dh = r * wd * gd - r ** 3 * hd * along.mean(-1, keepdim=True)
+    size = (r * wd * gd).abs() + r ** 3 * hd.abs() * along.abs().mean(-1, keepdim=True)
+    assert ((g["dx"].double() - dh).abs() <= GRAD * size + 1e-37).all()
+    terms = gd * hd * r
+    _close(g["dweight"], terms.sum(0), GRAD, "dweight", terms.abs().sum(0))
+
+
 def test_norm_gradient_of_nothing():
     import torch
     import selective_state_space_80_amd as mamba
