@@ -501,7 +501,6 @@ __global__ __launch_bounds__(512) void ring_kernel(const MatmulParams p)
 {
     constexpr int NW = 8, TM = FM * 16, TN = FN * 16, kStage = (TM + TN) * kStep, kLoads = 2 * (FM + FN);
     __shared__ __attribute__((aligned(16))) char smem[NW * STAGES * kStage];
-    __shared__ int sum[FM * FN * 4][64];  // as the products' lanes hold them: added without bank conflicts
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Share share = xcd_share(p.tiles, blockIdx.x % kXcds);
@@ -545,8 +544,6 @@ __global__ __launch_bounds__(512) void ring_kernel(const MatmulParams p)
     } else if (from < to) {
         fetch(from);
     }
-    for (int i = threadIdx.x; i < TM * TN; i += 64 * NW)
-        sum[i / 64][i % 64] = 0;
     // fragments: a lane holds 16 bytes of row lane % 16, quarter lane / 16
     const int fr = lane & 15, quarter = lane >> 4;
     i32x4 acc[FM][FN];
@@ -592,14 +589,20 @@ __global__ __launch_bounds__(512) void ring_kernel(const MatmulParams p)
                     acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[round][j], fa[round][i], acc[i][j], 0, 0, 0);
         stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
-    __syncthreads();
+    // Each wave's sums go where its steps lay: blocks of 16 x 16, of which a lane
+    // holds four consecutive n of one m.  `spread` lets 16 lanes write one quarter
+    // of a block, and 16 lanes read consecutive n, from different banks.
+    constexpr int kWaveBytes = STAGES * kStage;
+    static_assert(TM * TN * 4 <= kWaveBytes, "a wave's sums take its ring's place");
+    auto spread = [](int i, int j, int q, int r) {
+        const int x = FN <= 2 ? (j * 4 + q) * (4 / FN) : j * 4 + q;
+        return ((i * FN + j) * 64 + q * 16 + (r ^ x)) * 16;
+    };
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                atomicAdd(&sum[(i * FN + j) * 4 + e][lane], acc[i][j][e]);
+            *(i32x4 *)(mine + spread(i, j, quarter, fr)) = acc[i][j];
     __syncthreads();
     // four consecutive n of one m a thread
     using T = typename Elem<BF16>::T;
@@ -610,12 +613,15 @@ __global__ __launch_bounds__(512) void ring_kernel(const MatmulParams p)
         if (m >= rows_a || n >= rows_b)
             continue;
         const float sa = a_scale[m];
+        const char *part = smem + spread(m / 16, n / 16, n % 16 / 4, m % 16);
+        i32x4 sum = *(const i32x4 *)part;
+#pragma unroll
+        for (int w = 1; w < NW; ++w)
+            sum += *(const i32x4 *)(part + w * kWaveBytes);
         float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int from = (m / 16 * FN + n / 16) * 4 + e;
-            v[e] = (float)sum[from][n % 16 / 4 * 16 + m % 16] * sa * b_scale[n + e < rows_b ? n + e : rows_b - 1];
-        }
+        for (int e = 0; e < 4; ++e)
+            v[e] = (float)sum[e] * sa * b_scale[n + e < rows_b ? n + e : rows_b - 1];
         T *o = out + (int64_t)m * p.N + n;
         if (n + 4 <= rows_b) {
             if constexpr (BF16) {
@@ -659,7 +665,7 @@ struct FormCost {
 };
 constexpr FormCost ring_cost(int tm, int tn)
 {
-    return {tm, tn, kCus, .00124 * (tm + tn), .00166 * (tm + tn), 1.1 + .0008 * tm * tn, 1.6};
+    return {tm, tn, kCus, .00124 * (tm + tn), .00166 * (tm + tn), 1.1 + .00068 * tm * tn, 1.6};
 }
 constexpr FormCost kCosts[kForms] = {{256, 256, kCus, 1.14, 1.64, 5.35, 1.25},
                                      {128, 128, 2 * kCus, 0.69, 1.03, 2.31, 1.54},
