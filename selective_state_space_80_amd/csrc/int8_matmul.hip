@@ -646,32 +646,35 @@ __global__ __launch_bounds__(512) void ring_kernel(const MatmulParams p)
 // rounds: output tiles a workgroup slot takes after one another; alone: a step
 // of 128 bytes of the inner axis on an otherwise free card; busy: with every
 // slot taken, where power and the shared caches hold the rate; each: a tile's
-// end.  The constants are fitted to 49 shapes from 1 x 5120 x 2560 to
-// 16384 x 16384 x 2560, each timed in every form that suits it; the form chosen
-// is the fastest or within 7 % of it at all of them.  Both sides of some of the
-// choices, in us:
+// end.  The constants are fitted to 260 shapes drawn from 8 x 16 to 16384 x 8192 with
+// 64 to 8192 of the inner axis, each timed in every form; the form chosen takes
+// 0.5 % more than the fastest on average, 1.2 % at the ninetieth percentile, and
+// 22 % at the worst (6010 x 130 x 1616: 14.9, 12.2).  Of two that tie, the one
+// longer along n.  Both sides of some of the choices, in us:
 //   8 x 5120 x 2048 x 2560   256 x 256 tiles 178, 128 x 128 217
-//   4096 x 1536 x 768        256 x 256 tiles 12.5, 128 x 128 9.5
-//   1024 x 2560 x 5120       128 x 128 tiles of two stages 30.8, of four 23.7
-//   300 x 8192 x 256         the same 5.4 and 5.6; rings of 64 x 64 16.3
-//   256 x 2560 x 5120        128 x 128 tiles 23.4, rings of 64 x 64 13.1, of 64 x 48 11.2
-//   64 x 2560 x 5120         rings of 64 x 64 13.5, of 32 x 32 6.7
-//   2048 x 64 x 5120         rings of 32 x 32 7.3, of 16 x 32 6.0
-//   16 x 2560 x 5120         rings of 32 x 32 6.1, of 16 x 32 5.7, of 16 x 16 4.7
-enum Form { kTile256, kTile128, kTile128Deep, kRing44, kRing43, kRing34, kRing42, kRing24, kRing22, kRing12, kRing21, kRing11, kForms };
+//   4096 x 1536 x 768        256 x 256 tiles 13.3, 128 x 128 10.7
+//   1024 x 2560 x 5120       128 x 128 tiles of two stages 31.8, of four 25.4, rings of 64 x 64 37.0
+//   16384 x 2560 x 192       128 x 128 tiles of two stages 26.0, of four 30.8
+//   512 x 1536 x 768         128 x 128 tiles 7.0, rings of 64 x 64 6.0, of 64 x 48 5.5
+//   256 x 2560 x 5120        rings of 64 x 64 12.8, of 64 x 48 11.9, of 48 x 64 11.4
+//   64 x 2560 x 5120         rings of 32 x 64 9.6, of 32 x 32 7.3, of 16 x 32 10.0
+//   64 x 5120 x 128          rings of 32 x 64 3.8, of 32 x 32 4.7, 128 x 128 tiles 4.8
+//   2048 x 64 x 5120         rings of 32 x 32 7.5, of 16 x 32 6.7, of 32 x 16 9.0
+//   16 x 2560 x 5120         rings of 32 x 32 6.7, of 16 x 32 6.2, of 16 x 16 5.3
+enum Form { kTile256, kTile128, kTile128Deep, kRing44, kRing34, kRing43, kRing24, kRing42, kRing22, kRing12, kRing21, kRing11, kForms };
 struct FormCost {
     int tm, tn, slots;
     double alone, busy, each, once;
 };
-constexpr FormCost ring_cost(int tm, int tn)
+constexpr FormCost ring_cost(int tm, int tn)  // their loads bound them, alone or not
 {
-    return {tm, tn, kCus, .00124 * (tm + tn), .00166 * (tm + tn), 1.1 + .00068 * tm * tn, 1.6};
+    return {tm, tn, kCus, .00178 * (tm + tn), .00178 * (tm + tn), 1.04 + .00055 * tm * tn, 1.3};
 }
-constexpr FormCost kCosts[kForms] = {{256, 256, kCus, 1.14, 1.64, 5.35, 1.25},
-                                     {128, 128, 2 * kCus, 0.69, 1.03, 2.31, 1.54},
-                                     {128, 128, kCus, 0.53, 0.61, 1.41, 2.26},
-                                     ring_cost(64, 64), ring_cost(64, 48), ring_cost(48, 64),
-                                     ring_cost(64, 32), ring_cost(32, 64), ring_cost(32, 32),
+constexpr FormCost kCosts[kForms] = {{256, 256, kCus, 1.30, 1.50, 8.80, 1.30},
+                                     {128, 128, 2 * kCus, 0.80, 1.15, 2.50, 2.50},
+                                     {128, 128, kCus, 0.51, 0.69, 2.10, 2.60},
+                                     ring_cost(64, 64), ring_cost(48, 64), ring_cost(64, 48),
+                                     ring_cost(32, 64), ring_cost(64, 32), ring_cost(32, 32),
                                      ring_cost(16, 32), ring_cost(32, 16), ring_cost(16, 16)};
 constexpr int64_t kMostRingTiles = 1 << 16;  // of 512 threads
 
