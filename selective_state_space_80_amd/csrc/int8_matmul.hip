@@ -666,16 +666,28 @@ struct FormCost {
     int tm, tn, slots;
     double alone, busy, each, once;
 };
-constexpr FormCost ring_cost(int tm, int tn)  // their loads bound them, alone or not
+// A ring's loads bound it, alone or not.
+constexpr FormCost ring_cost(int tm, int tn, bool direct)
 {
-    return {tm, tn, kCus, .00178 * (tm + tn), .00178 * (tm + tn), 1.04 + .00055 * tm * tn, 1.3};
+    return direct ? FormCost{tm, tn, kCus, .00178 * (tm + tn), .00178 * (tm + tn), 1.04 + .00055 * tm * tn, 1.3}
+                  : FormCost{tm, tn, kCus, .00281 * (tm + tn), .00281 * (tm + tn), 0.39 + .00088 * tm * tn, 2.1};
 }
-constexpr FormCost kCosts[kForms] = {{256, 256, kCus, 1.30, 1.50, 8.80, 1.30},
-                                     {128, 128, 2 * kCus, 0.80, 1.15, 2.50, 2.50},
-                                     {128, 128, kCus, 0.51, 0.69, 2.10, 2.60},
-                                     ring_cost(64, 64), ring_cost(48, 64), ring_cost(64, 48),
-                                     ring_cost(32, 64), ring_cost(64, 32), ring_cost(32, 32),
-                                     ring_cost(16, 32), ring_cost(32, 16), ring_cost(16, 16)};
+struct FormCosts {
+    FormCost of[kForms];
+};
+constexpr FormCosts costs(FormCost tile256, FormCost tile128, FormCost tile128_deep, bool direct)
+{
+    return {{tile256, tile128, tile128_deep,
+             ring_cost(64, 64, direct), ring_cost(48, 64, direct), ring_cost(64, 48, direct),
+             ring_cost(32, 64, direct), ring_cost(64, 32, direct), ring_cost(32, 32, direct),
+             ring_cost(16, 32, direct), ring_cost(32, 16, direct), ring_cost(16, 16, direct)}};
+}
+// By way of registers (fitted to 120 more shapes), of which 256 x 256 outputs leave none.
+constexpr FormCosts kCosts[2] = {costs({}, {128, 128, 2 * kCus, 0.94, 1.69, 3.48, 3.85},
+                                       {128, 128, kCus, 0.69, 0.90, 3.11, 2.92}, false),
+                                 costs({256, 256, kCus, 1.30, 1.50, 8.80, 1.30},
+                                       {128, 128, 2 * kCus, 0.80, 1.15, 2.50, 2.50},
+                                       {128, 128, kCus, 0.51, 0.69, 2.10, 2.60}, true)};
 constexpr int64_t kMostRingTiles = 1 << 16;  // of 512 threads
 
 int64_t tiles_of(const FormCost &f, int64_t batch, int64_t M, int64_t N)
@@ -683,13 +695,12 @@ int64_t tiles_of(const FormCost &f, int64_t batch, int64_t M, int64_t N)
     return batch * ((M + f.tm - 1) / f.tm) * ((N + f.tn - 1) / f.tn);
 }
 
-// By way of registers there are none left for 256 x 256 outputs.
 Form choose(int64_t batch, int64_t M, int64_t N, int64_t K, bool direct)
 {
     Form best = kTile128;
     double least = -1.;
     for (int f = direct ? kTile256 : kTile128; f < kForms; ++f) {
-        const FormCost &c = kCosts[f];
+        const FormCost &c = kCosts[direct].of[f];
         const int64_t tiles = tiles_of(c, batch, M, N);
         if (f >= kRing44 && tiles > kMostRingTiles)
             continue;
@@ -749,6 +760,7 @@ hipError_t launch_int8_matmul(const Int8MatmulArgs &a, hipStream_t s)
     const int64_t batch = joined ? 1 : a.batch, M = joined ? a.batch * a.M : a.M;
     const bool direct = a.K % 16 == 0 && !off16(a.a) && !off16(a.b);
     const Form f = choose(batch, M, a.N, a.K, direct);
+    const FormCost &c = kCosts[direct].of[f];
     MatmulParams p{};
     p.a = a.a;
     p.b = a.b;
@@ -761,9 +773,9 @@ hipError_t launch_int8_matmul(const Int8MatmulArgs &a, hipStream_t s)
     p.steps = a.K > 0 ? (int)((a.K + kStep - 1) / kStep) : 1;
     p.a_batch = a.a_shared ? 0 : M;
     p.b_batch = a.b_shared ? 0 : a.N;
-    p.tiles_m = (int)((M + kCosts[f].tm - 1) / kCosts[f].tm);
-    p.tiles_n = (int)((a.N + kCosts[f].tn - 1) / kCosts[f].tn);
-    p.tiles = tiles_of(kCosts[f], batch, M, a.N);
+    p.tiles_m = (int)((M + c.tm - 1) / c.tm);
+    p.tiles_n = (int)((a.N + c.tn - 1) / c.tn);
+    p.tiles = tiles_of(c, batch, M, a.N);
     switch (f) {
     case kTile256: return tile<2, 4, 4, 2, 2, true>(p, kCus, a.bf16, s);
     case kTile128:
