@@ -17,10 +17,9 @@
 // of their own.
 //
 // Bound by memory.  8 x 5120 x 2048 bf16 (252 MB) takes 44 us (5.7 TB/s) with
-// the input in the last-level cache, where a scan has just left it, and 73 us
+// the input in the last-level cache, where a scan has just left it, and 62 us
 // from memory: there is room for one workgroup a CU, so its loads do not
-// overlap its stores (64 without the stores, 70 and 99 us before neighbouring
-// tiles shared an XCD's L2).  1 x 1536 x 131072 bf16 (604 MB) takes 143 us;
+// overlap its stores.  1 x 1536 x 131072 bf16 (604 MB) takes 133 us;
 // 64 x 5120 x 4 bf16 3.5 us, bound by its launch and its two dependent waits.
 #include <hip/hip_runtime.h>
 
@@ -97,6 +96,31 @@ __device__ __forceinline__ uint32_t pack4(const uint32_t (&byte)[4])
     return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
 }
 
+// Which tile a workgroup takes.  Neighbouring tiles read parts of the same cache
+// lines, so each of the 8 XCDs (workgroups go to them in turn) takes a
+// contiguous share.  What is in flight should also touch every memory channel
+// alike.  They alternate within 4 KB, and a tile reads the same few bytes of
+// each: so each XCD starts an eighth of its share after the one before, and
+// where rows repeat every 4 KB, the 64-byte tiles (about 32 of an XCD run at
+// once) go first by every second pair and then by the others.  8 x 5120 x 2048
+// bf16 67 us without either, 69 with the first, 62 with both; fp32 111, 98,
+// 102; 2 x 5120 x 4096 fp32 60, 56, 47; 8 x 8192 x 2048, in 32-byte tiles, 149
+// and 128 (132 with both).
+template <int PARTS> __device__ __forceinline__ int64_t tile_of(int64_t row_bytes)
+{
+    const int64_t all = gridDim.x, xcd = blockIdx.x % 8, more = all % 8;
+    const int64_t share = all / 8 + (xcd < more ? 1 : 0);
+    int64_t i = blockIdx.x / 8;
+    if (PARTS == 4 && row_bytes % 4096 == 0 && (i | 63) < share) {
+        const int64_t pair = i % 32 / 2, half = i % 64 / 32;
+        i = i / 64 * 64 + pair * 4 + half * 2 + i % 2;
+    }
+    i += share / 8 * xcd;
+    if (i >= share)
+        i -= share;
+    return xcd * (all / 8) + (xcd < more ? xcd : more) + i;
+}
+
 // HELD groups of channels stay in registers; 0: they are more than that, and
 // the second pass reads them again.
 template <bool BF16, int PARTS, int THREADS, int HELD, bool SHORT>
@@ -112,10 +136,7 @@ __global__ __launch_bounds__(THREADS) void quantize_channel_kernel(const Channel
     const int64_t group = blockDim.x / PARTS * kChan;  // channels
     const int part = lane & (PARTS - 1);          // which 16 bytes of the tokens
     const int64_t c0 = (int64_t)(threadIdx.x / PARTS) * kChan;  // first of its channels
-    // Neighbouring tiles read the two halves of the same cache lines: each of
-    // the 8 XCDs (workgroups go to them in turn) takes a contiguous share.
-    const int64_t all = gridDim.x, xcd = blockIdx.x % 8, more = all % 8;
-    const int64_t tile = xcd * (all / 8) + (xcd < more ? xcd : more) + blockIdx.x / 8;
+    const int64_t tile = tile_of<PARTS>(p.L * (int64_t)sizeof(T));
     const int64_t b = tile / p.tiles, l0 = (tile % p.tiles) * kTile;
     const int64_t to = l0 + part * kTok;
     const int64_t l = SHORT ? (to < p.L ? to : p.L - 1) : (to + kTok <= p.L ? to : p.L - kTok);
@@ -421,7 +442,7 @@ template <bool BF16> hipError_t dispatch(const QuantChannelArgs &a, hipStream_t 
         return tiles < 128 ? start<BF16, 1, kMostThreads / 4>(a, s) : start<BF16, 4, kMostThreads>(a, s);
     // More channels are held by smaller tiles of as many threads, up to the most
     // that registers hold; read twice instead, 1 x 20000 x 1000 bf16 takes 63 us
-    // (30 so), 8 x 8192 x 2048 168 (148), 2 x 16384 x 2048 77 (48; fp32 126 and 132).
+    // (30 so), 8 x 8192 x 2048 168 (127), 2 x 16384 x 2048 77 (48; fp32 126 and 128).
     if (a.K <= 2 * kHeldChannels)
         return start<BF16, 2, kMostThreads>(a, s);
     if (a.K <= 4 * kHeldChannels)
