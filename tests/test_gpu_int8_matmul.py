@@ -98,6 +98,25 @@ def test_forms(batch, M, N, K):
     _check(a, b, sa, sb, f"matmul batch={batch} {M}x{N}x{K}")
 
 
+# Drawn sizes, two for each form that the choice makes of them: rows at 16-byte
+# boundaries (256 x 256, 128 x 128, the same deep, then the rings from 64 x 64 down)
+# and off them.
+@pytest.mark.parametrize("M,N,K", [
+    (10858, 835, 1072), (1920, 7468, 560), (7304, 559, 320), (934, 7594, 800), (450, 7985, 1424),
+    (3597, 571, 144), (1988, 396, 64), (4299, 169, 1280), (847, 1602, 2720), (2617, 213, 80), (7577, 88, 1632),
+    (1547, 466, 1712), (9, 8923, 272), (33, 4164, 1136), (8564, 5, 4064), (5120, 79, 64), (52, 2757, 2416),
+    (158, 924, 3712), (90, 1074, 1024), (2932, 24, 2064), (7243, 2, 560), (5988, 5, 96), (520, 106, 288),
+    (10, 2667, 48),
+    (5815, 1817, 62), (2620, 2328, 1077), (2963, 751, 3003), (262, 6656, 4043), (110, 6404, 75),
+    (3141, 258, 1844), (2631, 193, 658), (40, 8845, 138), (4360, 130, 1243), (59, 10764, 63), (2124, 157, 122),
+    (246, 1178, 1752), (8759, 30, 44), (2078, 198, 110), (6702, 24, 91), (293, 514, 33), (4, 8763, 1251),
+    (3078, 29, 131), (10872, 6, 100), (8026, 2, 2394), (53, 5, 113), (3, 431, 199)])
+def test_drawn_sizes_of_every_form(M, N, K):
+    a, sa = _operand((M, K), M + K)
+    b, sb = _operand((N, K), N + K)
+    _check(a, b, sa, sb, f"matmul {M}x{N}x{K}")
+
+
 def test_extremes():
     """The largest sums an inner size of 131071 allows stay exact."""
     import torch
