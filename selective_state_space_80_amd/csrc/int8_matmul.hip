@@ -8,8 +8,8 @@
 // into LDS (DIRECT, global_load_lds_dwordx4: no registers, so as many are in
 // flight as LDS holds), or, where rows do not start at 16-byte boundaries, which
 // those loads need, by way of registers:
-//   tile_kernel  a workgroup's waves share a tile of both operands (256 x 256
-//                or 128 x 128 outputs) and step through the inner axis together
+//   tile_kernel  a workgroup's waves share a tile of both operands (256 x 256,
+//                128 x 128 or 128 x 64 outputs) and step through the inner axis together
 //   ring_kernel  few output tiles, or few rows on one side: the waves of a
 //                workgroup split the inner axis, each streaming its share
 //                through its own LDS ring, and add their integer sums
@@ -646,22 +646,24 @@ __global__ __launch_bounds__(512) void ring_kernel(const MatmulParams p)
 // rounds: output tiles a workgroup slot takes after one another; alone: a step
 // of 128 bytes of the inner axis on an otherwise free card; busy: with every
 // slot taken, where power and the shared caches hold the rate; each: a tile's
-// end.  The constants are fitted to 260 shapes drawn from 8 x 16 to 16384 x 8192 with
+// end.  The constants are fitted to 520 shapes drawn from 8 x 16 to 16384 x 8192 with
 // 64 to 8192 of the inner axis, each timed in every form; the form chosen takes
-// 0.5 % more than the fastest on average, 1.2 % at the ninetieth percentile, and
-// 22 % at the worst (6010 x 130 x 1616: 14.9, 12.2).  Of two that tie, the one
+// 0.4 % more than the fastest on average, 1.5 % at the ninetieth percentile, and
+// 16 % at the worst (2048 x 512 x 768: 7.4, 6.4).  Of two that tie, the one
 // longer along n.  Both sides of some of the choices, in us:
 //   8 x 5120 x 2048 x 2560   256 x 256 tiles 178, 128 x 128 217
 //   4096 x 1536 x 768        256 x 256 tiles 13.3, 128 x 128 10.7
 //   1024 x 2560 x 5120       128 x 128 tiles of two stages 31.8, of four 25.4, rings of 64 x 64 37.0
 //   16384 x 2560 x 192       128 x 128 tiles of two stages 26.0, of four 30.8
+//   1500 x 768 x 2560        128 x 128 tiles of four stages 15.3, 128 x 64 11.3, rings of 48 x 64 15.2
+//   1024 x 2048 x 1024       128 x 128 tiles of four stages 8.8, 128 x 64 7.1
 //   512 x 1536 x 768         128 x 128 tiles 7.0, rings of 64 x 64 6.0, of 64 x 48 5.5
 //   256 x 2560 x 5120        rings of 64 x 64 12.8, of 64 x 48 11.9, of 48 x 64 11.4
 //   64 x 2560 x 5120         rings of 32 x 64 9.6, of 32 x 32 7.3, of 16 x 32 10.0
 //   64 x 5120 x 128          rings of 32 x 64 3.8, of 32 x 32 4.7, 128 x 128 tiles 4.8
 //   2048 x 64 x 5120         rings of 32 x 32 7.5, of 16 x 32 6.7, of 32 x 16 9.0
 //   16 x 2560 x 5120         rings of 32 x 32 6.7, of 16 x 32 6.2, of 16 x 16 5.3
-enum Form { kTile256, kTile128, kTile128Deep, kRing44, kRing34, kRing43, kRing24, kRing42, kRing22, kRing12, kRing21, kRing11, kForms };
+enum Form { kTile256, kTile128, kTile128Deep, kTile64, kRing44, kRing34, kRing43, kRing24, kRing42, kRing22, kRing12, kRing21, kRing11, kForms };
 struct FormCost {
     int tm, tn, slots;
     double alone, busy, each, once;
@@ -675,19 +677,19 @@ constexpr FormCost ring_cost(int tm, int tn, bool direct)
 struct FormCosts {
     FormCost of[kForms];
 };
-constexpr FormCosts costs(FormCost tile256, FormCost tile128, FormCost tile128_deep, bool direct)
+constexpr FormCosts costs(FormCost tile256, FormCost tile128, FormCost tile128_deep, FormCost tile64, bool direct)
 {
-    return {{tile256, tile128, tile128_deep,
+    return {{tile256, tile128, tile128_deep, tile64,
              ring_cost(64, 64, direct), ring_cost(48, 64, direct), ring_cost(64, 48, direct),
              ring_cost(32, 64, direct), ring_cost(64, 32, direct), ring_cost(32, 32, direct),
              ring_cost(16, 32, direct), ring_cost(32, 16, direct), ring_cost(16, 16, direct)}};
 }
-// By way of registers (fitted to 120 more shapes), of which 256 x 256 outputs leave none.
+// By way of registers (fitted to 270 more shapes), of which 256 x 256 outputs leave none.
 constexpr FormCosts kCosts[2] = {costs({}, {128, 128, 2 * kCus, 0.94, 1.69, 3.48, 3.85},
-                                       {128, 128, kCus, 0.69, 0.90, 3.11, 2.92}, false),
+                                       {128, 128, kCus, 0.69, 0.90, 3.11, 2.92}, {128, 64, kCus, 0.66, 0.69, 2.17, 2.98}, false),
                                  costs({256, 256, kCus, 1.30, 1.50, 8.80, 1.30},
                                        {128, 128, 2 * kCus, 0.80, 1.15, 2.50, 2.50},
-                                       {128, 128, kCus, 0.51, 0.69, 2.10, 2.60}, true)};
+                                       {128, 128, kCus, 0.51, 0.69, 2.10, 2.60}, {128, 64, kCus, 0.41, 0.48, 1.75, 2.86}, true)};
 constexpr int64_t kMostRingTiles = 1 << 16;  // of 512 threads
 
 int64_t tiles_of(const FormCost &f, int64_t batch, int64_t M, int64_t N)
@@ -782,6 +784,8 @@ hipError_t launch_int8_matmul(const Int8MatmulArgs &a, hipStream_t s)
         return direct ? tile<2, 2, 2, 2, 2, true>(p, 2 * kCus, a.bf16, s) : tile<2, 2, 2, 2, 2, false>(p, 2 * kCus, a.bf16, s);
     case kTile128Deep:
         return direct ? tile<4, 2, 1, 2, 4, true>(p, kCus, a.bf16, s) : tile<4, 2, 1, 2, 4, false>(p, kCus, a.bf16, s);
+    case kTile64:
+        return direct ? tile<4, 1, 1, 2, 3, true>(p, kCus, a.bf16, s) : tile<4, 1, 1, 2, 3, false>(p, kCus, a.bf16, s);
     case kRing44: return ring<4, 4, 1>(p, direct, a.bf16, s);
     case kRing43: return ring<4, 3, 1>(p, direct, a.bf16, s);
     case kRing34: return ring<3, 4, 1>(p, direct, a.bf16, s);

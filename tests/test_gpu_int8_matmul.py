@@ -98,9 +98,9 @@ def test_forms(batch, M, N, K):
     _check(a, b, sa, sb, f"matmul batch={batch} {M}x{N}x{K}")
 
 
-# Drawn sizes, two for each form that the choice makes of them: rows at 16-byte
+# Drawn sizes, some for each form that the choice makes of them: rows at 16-byte
 # boundaries (256 x 256, 128 x 128, the same deep, then the rings from 64 x 64 down)
-# and off them.
+# and off them, then tiles of 128 x 64 on and off.
 @pytest.mark.parametrize("M,N,K", [
     (10858, 835, 1072), (1920, 7468, 560), (7304, 559, 320), (934, 7594, 800), (450, 7985, 1424),
     (3597, 571, 144), (1988, 396, 64), (4299, 169, 1280), (847, 1602, 2720), (2617, 213, 80), (7577, 88, 1632),
@@ -110,7 +110,8 @@ def test_forms(batch, M, N, K):
     (5815, 1817, 62), (2620, 2328, 1077), (2963, 751, 3003), (262, 6656, 4043), (110, 6404, 75),
     (3141, 258, 1844), (2631, 193, 658), (40, 8845, 138), (4360, 130, 1243), (59, 10764, 63), (2124, 157, 122),
     (246, 1178, 1752), (8759, 30, 44), (2078, 198, 110), (6702, 24, 91), (293, 514, 33), (4, 8763, 1251),
-    (3078, 29, 131), (10872, 6, 100), (8026, 2, 2394), (53, 5, 113), (3, 431, 199)])
+    (3078, 29, 131), (10872, 6, 100), (8026, 2, 2394), (53, 5, 113), (3, 431, 199),
+    (441, 3392, 2656), (225, 6784, 32), (1535, 2540, 736), (2182, 584, 2142), (5660, 164, 125)])
 def test_drawn_sizes_of_every_form(M, N, K):
     a, sa = _operand((M, K), M + K)
     b, sb = _operand((N, K), N + K)
