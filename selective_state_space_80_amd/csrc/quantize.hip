@@ -88,14 +88,6 @@ template <bool BF16> __device__ __forceinline__ uint32_t max_abs(uint32_t top, u
     }
 }
 
-// q of four neighbouring channels of one token.
-__device__ __forceinline__ uint32_t pack4(const uint32_t (&byte)[4])
-{
-    const uint32_t lo = __builtin_amdgcn_perm(byte[1], byte[0], 0x0c0c0400u);
-    const uint32_t hi = __builtin_amdgcn_perm(byte[3], byte[2], 0x0c0c0400u);
-    return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
-}
-
 // Which tile a workgroup takes.  Neighbouring tiles read parts of the same cache
 // lines, so each of the 8 XCDs (workgroups go to them in turn) takes a
 // contiguous share.  What is in flight should also touch every memory channel
@@ -130,7 +122,7 @@ __global__ __launch_bounds__(THREADS) void quantize_channel_kernel(const Channel
     using Tok = Tokens<BF16>;
     constexpr int kTok = Tok::kCount, kTile = PARTS * kTok;
     __shared__ uint32_t tops[THREADS / 64][PARTS][4];
-    __shared__ RowScale rows[kTile];
+    __shared__ RowScale<BF16> rows[kTile];
     __shared__ int special;  // a row is raised, or not finite
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n_waves = blockDim.x >> 6;
     const int64_t group = blockDim.x / PARTS * kChan;  // channels
@@ -214,7 +206,7 @@ __global__ __launch_bounds__(THREADS) void quantize_channel_kernel(const Channel
             t = max_abs<BF16>(t, tops[w][pt][BF16 ? i / 2 : i]);
         if constexpr (BF16)
             t = (i % 2 ? t >> 16 : t & 0xffffu) << 16;
-        const RowScale rs = row_scale(t);
+        const RowScale<BF16> rs(t);
         rows[threadIdx.x] = rs;
         if (rs.raise != 1.f || rs.mask == 0)
             atomicOr(&special, 1);
@@ -226,10 +218,15 @@ __global__ __launch_bounds__(THREADS) void quantize_channel_kernel(const Channel
     __syncthreads();
     if (!live)
         return;
-    float mul[kTok];
+    // Where the registers are full, a token's fp64 multiplier is read when it is
+    // needed (8 x 6144 x 2048 fp32: 125 us; held, other values spill, 131).
+    constexpr bool kReread = !BF16 && HELD == kMaxHeld;
+    RowScale<BF16> row[kTok];
+    if constexpr (!kReread) {
 #pragma unroll
-    for (int i = 0; i < kTok; ++i)
-        mul[i] = rows[part * kTok + i].mul;
+        for (int i = 0; i < kTok; ++i)
+            row[i].mul = rows[part * kTok + i].mul;
+    }
     const bool any_special = special != 0;
     int8_t *q = p.q + (b * p.L + l) * p.K;
     auto put = [&](const Tok(&t)[kChan], int64_t g) {
@@ -240,13 +237,18 @@ __global__ __launch_bounds__(THREADS) void quantize_channel_kernel(const Channel
         for (int i = 0; i < kTok; ++i) {
             if (SHORT && i >= left)
                 continue;
+            if constexpr (kReread) {
+                int at = part * kTok + i;
+                asm volatile("" : "+v"(at));
+                row[i].mul = rows[at].mul;
+            }
             uint32_t byte[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 float v = t[r].get(i);
                 if (any_special)
                     v *= rows[part * kTok + i].raise;
-                byte[r] = __float_as_uint(fmaf(v, mul[i], 12582912.f));
+                byte[r] = row[i].nearest(v);
             }
             uint32_t w = pack4(byte);
             if (any_special)
@@ -295,7 +297,7 @@ __global__ __launch_bounds__(kMostThreads) void quantize_short_kernel(const Chan
         }
     };
     __shared__ uint32_t tops[kMostThreads / 64][L];
-    __shared__ RowScale rows[L];
+    __shared__ RowScale<BF16> rows[L];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n_waves = blockDim.x >> 6;
     const int64_t b = blockIdx.x;
     const int64_t group = (int64_t)blockDim.x * kChan;
@@ -343,7 +345,7 @@ __global__ __launch_bounds__(kMostThreads) void quantize_short_kernel(const Chan
         uint32_t t = 0;
         for (int w = 0; w < n_waves; ++w)
             t = umax(t, tops[w][threadIdx.x]);
-        const RowScale rs = row_scale(t);
+        const RowScale<BF16> rs(t);
         rows[threadIdx.x] = rs;
         p.scale[b * L + threadIdx.x] = rs.scale;
     }
@@ -356,7 +358,7 @@ __global__ __launch_bounds__(kMostThreads) void quantize_short_kernel(const Chan
             uint32_t byte[kChan];
 #pragma unroll
             for (int r = 0; r < kChan; ++r)
-                byte[r] = __float_as_uint(fmaf(t.get(r * L + i) * rows[i].raise, rows[i].mul, 12582912.f));
+                byte[r] = rows[i].nearest(t.get(r * L + i) * rows[i].raise);
             const uint32_t w = pack4(byte) & rows[i].mask;
             __builtin_memcpy(q + i * p.K + c, &w, 4);
         }

@@ -140,7 +140,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void rms_norm_kernel(const Norm
             for (int k = 0; k < n_waves; ++k)
                 top = umax(top, __float_as_uint(red[1][k]));
         }
-        const RowScale rs = row_scale(top);
+        const RowScale<XBF && MODE == kQuant> rs(top);  // the norm's values are fp32
         if (tid == 0 && !past)
             p.scale[row] = rs.scale;
         if (rs.raise != 1.f) {
@@ -153,7 +153,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void rms_norm_kernel(const Norm
         int8_t *qo = (int8_t *)p.out + row * D;
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
-            const u32x2 q = pack_int8(h[j], rs.mul, rs.mask);
+            const u32x2 q = pack_int8(h[j], rs);
             if (!at[j].live)
                 continue;
             if constexpr (TINY) {

@@ -112,47 +112,84 @@ inline int row_lanes(int64_t D) { return D <= 64 ? 8 : D <= 128 ? 16 : D <= 256 
 // above infinity, so one unsigned maximum also tells a row that is not finite.
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// Scale and multiplier of a row whose largest |value| has the bits `top`.
+// q = the integer nearest to v * 127 / top, ties to even, in [-127, 127], for a
+// row whose largest |value| is top.  Adding 1.5 * 2^23 to an fp32 number (2^52 in
+// fp64) rounds it to an integer, whose low byte is then that integer in two's
+// complement.  127 / top is no fp32 or fp64 number, so the product with its
+// rounded value can miss a tie.  A first rounding to a fixed fraction, coarser
+// than the miss but finer than the distance of any other quotient from a tie,
+// puts it back:
+//   bf16 values: v / top = a / (b 2^s) with integers a, b < 256.  A quotient that
+//     is no tie is at least 1 / (b 2^s) > 1.54e-5 from one (254 a and odd
+//     multiples of b 2^s are even for s > 0; for s = 0, 1 / 2b).  The fp32 product
+//     misses by at most 127 * 2^-24 = 0.76e-5; rounded to multiples of 2^-15,
+//     numbers within 1.53e-5 of a tie become it.
+//   fp32 values: a, b < 2^24, the distance is at least 2^-33; the fp64 product
+//     misses by at most 2^-38, and is rounded to multiples of 2^-36.
+// One more instruction than a single rounding in bf16, two more for fp32 values
+// (8 x 5120 x 2048 channel-major: bf16 69.4 us, 68.9 with the single rounding;
+// fp32 104.8, 103.4; 131072 rows of 64, the norm's fp32 values, 7.6 and 7.1).
+//
 // A zero row has scale 0; a row that is not finite has scale NaN and q = 0, so
-// that everything computed from it is NaN.  Below 2^-120 the multiplier
-// 127 / top would pass the fp32 range: such rows are raised by 2^64 first.
-struct RowScale {
-    float scale, mul, raise;
+// that everything computed from it is NaN.
+template <bool BF16> struct RowScale;
+template <> struct RowScale<true> {
+    float scale, mul;
+    float raise;  // below 2^-120 the multiplier would pass the fp32 range: such rows are raised by 2^64
     uint32_t mask;
-};
-__device__ __forceinline__ RowScale row_scale(uint32_t top)
-{
-    RowScale r;
-    const float t = __uint_as_float(top);
-    r.raise = top != 0 && t < 0x1p-120f ? 0x1p64f : 1.f;
-    r.scale = t / 127.f;
-    r.mul = top == 0 ? 0.f : 127.f / (t * r.raise);
-    r.mask = 0xffffffffu;
-    if (top >= 0x7f800000u) {
-        r.scale = __uint_as_float(0x7fc00000u);
-        r.mul = 0.f;
-        r.mask = 0u;
+    __device__ __forceinline__ RowScale() = default;
+    __device__ __forceinline__ explicit RowScale(uint32_t top)
+    {
+        const bool finite = top < 0x7f800000u;
+        const float t = __uint_as_float(top);
+        raise = top != 0 && t < 0x1p-120f ? 0x1p64f : 1.f;
+        scale = finite ? t / 127.f : __uint_as_float(0x7fc00000u);
+        mul = top == 0 || !finite ? 0.f : 127.f / (t * raise);
+        mask = finite ? 0xffffffffu : 0u;
     }
-    return r;
-}
+    __device__ __forceinline__ uint32_t nearest(float v) const
+    {
+        constexpr float kFraction = 384.f, kInteger = 12582912.f;  // 1.5 * 2^8, 2^23
+        return __float_as_uint(fmaf(v, mul, kFraction) + (kInteger - kFraction));
+    }
+};
+template <> struct RowScale<false> {
+    static constexpr float raise = 1.f;  // fp64 has room
+    double mul;
+    float scale;
+    uint32_t mask;
+    __device__ __forceinline__ RowScale() = default;
+    __device__ __forceinline__ explicit RowScale(uint32_t top)
+    {
+        const bool finite = top < 0x7f800000u;
+        const float t = __uint_as_float(top);
+        scale = finite ? t / 127.f : __uint_as_float(0x7fc00000u);
+        const float up = t < 0x1p-64f ? 0x1p64f : 1.f;
+        const double m = (double)(127.f / (t * up)) * (double)up;  // the fp32 quotient, and its remainder's: 46 bits
+        mul = top == 0 || !finite ? 0. : fma(fma(-m, (double)t, 127.), m * (1. / 127.), m);
+        mask = finite ? 0xffffffffu : 0u;
+    }
+    __device__ __forceinline__ uint32_t nearest(float v) const
+    {
+        constexpr double kFraction = 0x1.8p16, kInteger = 0x1.8p52;
+        return (uint32_t)__double_as_longlong(fma((double)v, mul, kFraction) + (kInteger - kFraction));
+    }
+};
 
-// Eight integers in [-127, 127] as bytes.  v * mul + 1.5 * 2^23 is rounded to
-// an integer by the addition itself (to nearest, ties to even), whose low byte
-// is then that integer in two's complement.
-__device__ __forceinline__ u32x2 pack_int8(const float (&v)[8], float mul, uint32_t mask)
+// Bytes of four integers.
+__device__ __forceinline__ uint32_t pack4(const uint32_t *b)
+{
+    const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400u);
+    return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+}
+template <bool BF16> __device__ __forceinline__ u32x2 pack_int8(const float (&v)[8], const RowScale<BF16> &row)
 {
     uint32_t b[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        b[i] = __float_as_uint(fmaf(v[i], mul, 12582912.f));
-    u32x2 q;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t lo = __builtin_amdgcn_perm(b[4 * i + 1], b[4 * i], 0x0c0c0400u);
-        const uint32_t hi = __builtin_amdgcn_perm(b[4 * i + 3], b[4 * i + 2], 0x0c0c0400u);
-        q[i] = __builtin_amdgcn_perm(hi, lo, 0x05040100u) & mask;
-    }
-    return q;
+        b[i] = row.nearest(v[i]);
+    return u32x2{pack4(b), pack4(b + 4)} & row.mask;
 }
 
 // Where a lane's chunk of 8 elements lies in a row of D, and which of them are
