@@ -369,8 +369,8 @@ mamba_status mamba_ssd_scan_fwd(const void *x, const void *dt, const float *dt_b
  *   weight                 : [D] float, required
  *   eps                    : finite, >= 0 (else MAMBA_ERR_SHAPE)
  * D in 1..32768 (MAMBA_MAX_NORM_WIDTH), M < 2^26 for D up to 4096 and below
- * 2^22 beyond.  The square sum is an fp32
- * sum: rows whose sum of squares passes the fp32 range give zeros or NaN.
+ * 2^22 beyond.  Rows whose sum of squares passes the fp32 range, on either
+ * side, are taken by a power of two first; a zero row with eps = 0 gives zeros.
  * Except for that in-place update, outputs must not overlap inputs or each
  * other.
  */
@@ -409,7 +409,10 @@ mamba_status mamba_rms_norm_int8(const void *x, const void *residual, const floa
  *   weight, dweight             : [D] float, required
  *   workspace                   : mamba_rms_norm_bwd_workspace_size(M, D) bytes,
  *                                 256-byte aligned; scratch as in the scan
- * Sums are taken in a fixed order.  With M = 0, dweight is zero.
+ * Sums are taken in a fixed order.  With M = 0, dweight is zero.  Rows whose
+ * sum of squares passes the fp32 range are taken by a power of two first; where
+ * 1/rms itself passes it (rows of denormals with eps = 0), dh is infinite or
+ * NaN; a zero row with eps = 0 has dh = dresidual_out.
  */
 size_t mamba_rms_norm_bwd_workspace_size(int64_t M, int64_t D);
 mamba_status mamba_rms_norm_bwd(const void *dy, const void *h, const float *weight, const void *dresidual_out,

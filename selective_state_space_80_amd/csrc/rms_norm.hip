@@ -6,6 +6,8 @@
 //   residual_out = h rounded to the residual's type
 //   out = y rounded to x's type, or   scale = max|y| / 127,  q = rne(y * 127 / max|y|).
 // y is formed from the unrounded h: the only roundings are the outputs'.
+// Where the sum of squares leaves the fp32 range (large rows; small ones without
+// eps), h is taken by a power of two and summed again (range_factor).
 //
 // Every element is read once and written once: a row stays in the registers of
 // the lanes that loaded it (8-element chunks, 16 or 32 bytes a lane), the row's
@@ -45,7 +47,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void rms_norm_kernel(const Norm
 {
     using XT = typename Elem<XBF>::T;
     using RT = typename Elem<RES == 2>::T;
-    __shared__ float red[2][16];
+    __shared__ float red[3][16];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     constexpr int kRows = LANES ? 64 / LANES : 1;  // of a wave
@@ -91,19 +93,23 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void rms_norm_kernel(const Norm
 #pragma unroll
         for (int j = 0; j < NC; ++j)
             load_chunk<false, TINY>(p.w, at[j], D, w[j]);
-        float s = 0.f;
+        auto square_sum = [&](float(&slots)[16]) {
+            float s = 0.f;
 #pragma unroll
-        for (int j = 0; j < NC; ++j)
-            s += own_sum<TINY>(at[j], D, ragged, [&](int i) { return h[j][i] * h[j][i]; });
-        s = lane_sum<LANES ? LANES : 64>(s);
-        if constexpr (!LANES) {
-            if (lane == 0)
-                red[0][wave] = s;
-            __syncthreads();
-            s = red[0][0];
-            for (int k = 1; k < n_waves; ++k)
-                s += red[0][k];
-        }
+            for (int j = 0; j < NC; ++j)
+                s += own_sum<TINY>(at[j], D, ragged, [&](int i) { return h[j][i] * h[j][i]; });
+            s = lane_sum<LANES ? LANES : 64>(s);
+            if constexpr (!LANES) {
+                if (lane == 0)
+                    slots[wave] = s;
+                __syncthreads();
+                s = slots[0];
+                for (int k = 1; k < n_waves; ++k)
+                    s += slots[k];
+            }
+            return s;
+        };
+        float s = square_sum(red[0]), eps = p.eps;
         // every element of the row has been read: the residual may be overwritten
         if constexpr (RES != 0) {
             if (p.res_out) {
@@ -113,7 +119,19 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void rms_norm_kernel(const Norm
                     store_chunk<RES == 2, TINY>(ro, at[j], D, h[j]);
             }
         }
-        const float r = 1.f / sqrtf(fmaf(s, p.inv_d, p.eps));
+        const float factor = range_factor(s, eps);  // the same in all lanes of the row
+        if (__builtin_expect(factor != 1.f, 0)) {
+#pragma unroll
+            for (int j = 0; j < NC; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    h[j][i] *= factor;
+            s = square_sum(red[2]);
+            eps = eps * factor * factor;
+            if (s == 0.f && eps == 0.f)
+                eps = 1.f;  // a zero row stays zero
+        }
+        const float r = 1.f / sqrtf(fmaf(s, p.inv_d, eps));
 #pragma unroll
         for (int j = 0; j < NC; ++j)
 #pragma unroll

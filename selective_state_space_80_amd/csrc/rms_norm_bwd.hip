@@ -6,7 +6,9 @@
 // Both row sums (h^2 and w dy h) need no r, so one pass over the row gives
 // them together; dh follows from the registers.  dw is summed over the rows a
 // workgroup takes in its registers, written once per workgroup, and summed
-// over the workgroups in a fixed order by a second kernel.
+// over the workgroups in a fixed order by a second kernel.  Rows whose sum of
+// squares leaves the fp32 range are taken by a power of two, as in the forward
+// kernel.
 //
 // Bound by memory: 16384 x 2560, dy and dx bf16, h and both residual gradients
 // fp32 (671 MB), takes 129 us (5.2 TB/s, the rate of a large copy);
@@ -93,52 +95,96 @@ __global__ __launch_bounds__(LANES ? 256 : NC == 1 ? 512 : 1024) void rms_norm_b
             for (int j = 0; j < NC; ++j) {
                 rh[j].get(h[j]);
                 rg[j].get(g[j]);
-                if constexpr (DRES)
+                if constexpr (DRES && kAhead)
                     rd[j].get(d[j]);
             }
         }
         // What a lean lane needs of chunk j.  The empty statement keeps the
         // compiler from carrying the results of one use to the next in registers.
         const float *weight = p.w;
-        auto unpack = [&](int j) {
+        auto unpack = [&](int j, float factor) {
             if constexpr (kLean) {
                 asm volatile("" : "+s"(weight));
                 rh[j].keep();
                 rg[j].keep();
                 rh[j].get(h[0]);
                 rg[j].get(g[0]);
+                if (__builtin_expect(factor != 1.f, 0)) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        h[0][i] *= factor;
+                }
                 load_chunk<false, TINY>(weight, at[j], D, w[0]);
             }
         };
         if (kAhead && row + step < p.M)
             load_row(row + step);
-        float s = 0.f, t = 0.f;
+        float s, t, factor = 1.f, eps = p.eps;
+        auto sums = [&]() {
+            s = t = 0.f;
 #pragma unroll
-        for (int j = 0; j < NC; ++j) {
-            const int k = kLean ? 0 : j;
-            unpack(j);
-            s += own_sum<TINY>(at[j], D, ragged, [&](int i) { return h[k][i] * h[k][i]; });
-            t += own_sum<TINY>(at[j], D, ragged, [&](int i) { return g[k][i] * w[k][i] * h[k][i]; });
-        }
-        s = lane_sum<LANES ? LANES : 64>(s);
-        t = lane_sum<LANES ? LANES : 64>(t);
-        if constexpr (!LANES) {
-            // two sets of slots in turn: a wave writes the next row's while
-            // others still read this row's
-            if (lane == 0) {
-                red[parity][0][wave] = s;
-                red[parity][1][wave] = t;
+            for (int j = 0; j < NC; ++j) {
+                const int k = kLean ? 0 : j;
+                unpack(j, factor);
+                s += own_sum<TINY>(at[j], D, ragged, [&](int i) { return h[k][i] * h[k][i]; });
+                t += own_sum<TINY>(at[j], D, ragged, [&](int i) { return g[k][i] * w[k][i] * h[k][i]; });
             }
-            __syncthreads();
-            s = red[parity][0][0];
-            t = red[parity][1][0];
-            for (int k = 1; k < n_waves; ++k) {
-                s += red[parity][0][k];
-                t += red[parity][1][k];
+            s = lane_sum<LANES ? LANES : 64>(s);
+            t = lane_sum<LANES ? LANES : 64>(t);
+            if constexpr (!LANES) {
+                // two sets of slots in turn: a wave writes the next sums while
+                // others still read these
+                if (lane == 0) {
+                    red[parity][0][wave] = s;
+                    red[parity][1][wave] = t;
+                }
+                __syncthreads();
+                s = red[parity][0][0];
+                t = red[parity][1][0];
+                for (int k = 1; k < n_waves; ++k) {
+                    s += red[parity][0][k];
+                    t += red[parity][1][k];
+                }
+                parity ^= 1;
             }
-            parity ^= 1;
+        };
+        auto zero_row = [&]() {  // without eps: no gradient through the norm
+            if (s == 0.f && eps == 0.f) {
+                eps = 1.f;
+                factor = 0.f;
+            }
+        };
+        // Rows whose square sum leaves the fp32 range take a second pass.  Lean
+        // lanes loop, so that the registers are laid out for one (fp32: 12 spilled, 50 with two).
+        if constexpr (kLean) {
+#pragma unroll 1
+            for (;;) {
+                sums();
+                if (__builtin_expect(factor != 1.f, 0)) {
+                    zero_row();
+                    break;
+                }
+                factor = range_factor(s, eps);  // the same in all lanes of the row
+                if (__builtin_expect(factor == 1.f, 1))
+                    break;
+                eps = eps * factor * factor;
+            }
+        } else {
+            sums();
+            factor = range_factor(s, eps);
+            if (__builtin_expect(factor != 1.f, 0)) {
+                eps = eps * factor * factor;
+#pragma unroll
+                for (int j = 0; j < NC; ++j)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        h[j][i] *= factor;
+                sums();
+                zero_row();
+            }
         }
-        const float r = 1.f / sqrtf(fmaf(s, p.inv_d, p.eps));
+        // of the elements with the factor, and of the row itself
+        const float r = 1.f / sqrtf(fmaf(s, p.inv_d, eps)), row_r = r * factor;
         const float c = t * r * p.inv_d;
         const bool past = kRows > 1 && row + sub >= p.M;
         const int64_t mine = kRows > 1 ? row + sub : row;
@@ -147,15 +193,17 @@ __global__ __launch_bounds__(LANES ? 256 : NC == 1 ? 512 : 1024) void rms_norm_b
             if (past)
                 continue;
             const int k = kLean ? 0 : j;
-            unpack(j);
+            unpack(j, factor);
             if constexpr (kLean && DRES)
                 load_chunk<HBF, TINY>((const HT *)p.dres_out + mine * D, at[j], D, d[0]);
+            if constexpr (!kLean && DRES && !kAhead)
+                rd[j].get(d[j]);
             float dh[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float hr = h[k][i] * r;  // normalised: r^3 passes the fp32 range before it does
                 acc[j][i] = fmaf(g[k][i], hr, acc[j][i]);
-                dh[i] = r * fmaf(g[k][i], w[k][i], -c * hr);
+                dh[i] = row_r * fmaf(g[k][i], w[k][i], -c * hr);
                 if constexpr (DRES)
                     dh[i] += d[k][i];
             }

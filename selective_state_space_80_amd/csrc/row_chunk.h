@@ -104,6 +104,20 @@ template <int LANES> __device__ __forceinline__ uint32_t lane_max(uint32_t v)
                 umax((uint32_t)__builtin_amdgcn_readlane(b, 32), (uint32_t)__builtin_amdgcn_readlane(b, 48)));
 }
 
+// Factor to take a row's elements by where the sum of their squares, s, leaves
+// the fp32 range; the square sum and eps are then formed again with it.
+//   s infinite: 2^-80.  The largest element is above 2^56, its square above 2^-48
+//     then, and 32768 times the largest square there is is below 2^111.
+//   s and eps below 2^-80: 2^100.  Elements are below 2^-40, the smallest number
+//     there is becomes 2^-49.  (With s above 2^-80 what underflows in it is below
+//     2^-54 of it; with eps above, s matters to 2^-54 of eps at most.)
+__device__ __forceinline__ float range_factor(float s, float eps)
+{
+    if (s == __builtin_inff())
+        return 0x1p-80f;
+    return s < 0x1p-80f && eps < 0x1p-80f ? 0x1p100f : 1.f;
+}
+
 // Lanes that share a row of D elements where a wave holds whole rows: as few
 // as hold it in one chunk each (8 rows of 64 elements a wave), 64 for longer.
 inline int row_lanes(int64_t D) { return D <= 64 ? 8 : D <= 128 ? 16 : D <= 256 ? 32 : 64; }
