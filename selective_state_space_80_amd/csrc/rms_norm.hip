@@ -131,7 +131,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void rms_norm_kernel(const Norm
             if (s == 0.f && eps == 0.f)
                 eps = 1.f;  // a zero row stays zero
         }
-        const float r = 1.f / sqrtf(fmaf(s, p.inv_d, eps));
+        const float r = inv_root(fmaf(s, p.inv_d, eps));
 #pragma unroll
         for (int j = 0; j < NC; ++j)
 #pragma unroll

@@ -184,8 +184,13 @@ __global__ __launch_bounds__(LANES ? 256 : NC == 1 ? 512 : 1024) void rms_norm_b
             }
         }
         // of the elements with the factor, and of the row itself
-        const float r = 1.f / sqrtf(fmaf(s, p.inv_d, eps)), row_r = r * factor;
+        const float r = inv_root(fmaf(s, p.inv_d, eps)), row_r = r * factor;
         const float c = t * r * p.inv_d;
+        if constexpr (DRES && !kAhead && !kLean) {  // the last loads are waited for before the first store
+#pragma unroll
+            for (int j = 0; j < NC; ++j)
+                rd[j].keep();
+        }
         const bool past = kRows > 1 && row + sub >= p.M;
         const int64_t mine = kRows > 1 ? row + sub : row;
 #pragma unroll

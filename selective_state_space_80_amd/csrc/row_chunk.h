@@ -118,6 +118,20 @@ __device__ __forceinline__ float range_factor(float s, float eps)
     return s < 0x1p-80f && eps < 0x1p-80f ? 0x1p100f : 1.f;
 }
 
+// 1 / sqrt(x) rounded once, for a normal x: the hardware's, off by up to a unit in
+// the last place, and one step r + r (1 - x r^2) / 2 of which no part is rounded
+// before it is small.  (The reciprocal of a rounded root rounds twice: up to 0.75
+// units from 1 / sqrt(x) where this is 0.5.)  0 and NaN of infinity and NaN, as
+// 1 / sqrt; x is normal or one of these, since small sums are taken by a power of
+// two.
+__device__ __forceinline__ float inv_root(float x)
+{
+    const float r = __builtin_amdgcn_rsqf(x);
+    const float t = x * r, low = fmaf(x, r, -t);  // x r = t + low
+    const float e = fmaf(-low, r, fmaf(-t, r, 1.f));
+    return x < __builtin_inff() ? fmaf(0.5f * r, e, r) : r;
+}
+
 // Lanes that share a row of D elements where a wave holds whole rows: as few
 // as hold it in one chunk each (8 rows of 64 elements a wave), 64 for longer.
 inline int row_lanes(int64_t D) { return D <= 64 ? 8 : D <= 128 ? 16 : D <= 256 ? 32 : 64; }
