@@ -368,8 +368,8 @@ mamba_status mamba_ssd_scan_fwd(const void *x, const void *dt, const float *dt_b
  *                            residual (updated in place)
  *   weight                 : [D] float, required
  *   eps                    : finite, >= 0 (else MAMBA_ERR_SHAPE)
- * D in 1..32768 (MAMBA_MAX_NORM_WIDTH), M < 2^26 for D up to 4096 and below
- * 2^22 beyond.  Rows whose sum of squares passes the fp32 range, on either
+ * D in 1..32768 (MAMBA_MAX_NORM_WIDTH), M up to 2^26 - 4 for D up to 4096 and
+ * below 2^22 beyond.  Rows whose sum of squares passes the fp32 range, on either
  * side, are taken by a power of two first; a zero row with eps = 0 gives zeros.
  * Except for that in-place update, outputs must not overlap inputs or each
  * other.

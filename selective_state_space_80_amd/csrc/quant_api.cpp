@@ -14,9 +14,10 @@ namespace {
 
 constexpr int64_t kMaxBlocks = int64_t(1) << 22;  // blocks x 1024 threads below 2^32 work-items
 
-// Rows the token-major kernels can be launched on: of up to 4096 elements four
-// or more share a 256-thread block, wider ones have up to 1024 threads each.
-int64_t max_rows(int64_t D) { return D <= 4096 ? kMaxBlocks * 16 : kMaxBlocks; }
+// Rows the token-major kernels can be launched on, with fewer than 2^32 threads:
+// of up to 4096 elements four or more share a 256-thread block, wider ones have
+// up to 1024 threads each.
+int64_t max_rows(int64_t D) { return D <= 4096 ? (kMaxBlocks * 4 - 1) * 4 : kMaxBlocks - 1; }
 
 // Checks of both forward norms.  `out_bytes`: of one element of `out`.
 mamba_status norm_entry(const void *x, const void *residual, const float *weight, void *out, float *scale,
@@ -30,7 +31,7 @@ mamba_status norm_entry(const void *x, const void *residual, const float *weight
     if (D > mamba::kMaxNormWidth || (residual && io == MAMBA_F32 && residual_type == MAMBA_BF16) ||
         (residual_out && !residual))
         return MAMBA_ERR_UNSUPPORTED;
-    if (M >= max_rows(D))
+    if (M > max_rows(D))
         return MAMBA_ERR_SHAPE;
     if (M * D == 0 && !(int8 && M > 0))
         return MAMBA_OK;
@@ -150,7 +151,7 @@ mamba_status mamba_quantize_int8(const void *x, int8_t *q, float *scale, int64_t
         return MAMBA_ERR_UNSUPPORTED;
     // channel-major: a block has 16 tokens or more; fewer only in launches of few blocks
     // and of so many channels that as many blocks would need more memory than there is
-    if (channel_major ? L >= kMaxBlocks * 16 || B * ((L + 15) / 16) >= kMaxBlocks : B * L >= max_rows(K))
+    if (channel_major ? L >= kMaxBlocks * 16 || B * ((L + 15) / 16) >= kMaxBlocks : B * L > max_rows(K))
         return MAMBA_ERR_SHAPE;
     if (B * L == 0)
         return MAMBA_OK;

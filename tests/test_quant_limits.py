@@ -1,0 +1,31 @@
+"""CPU checks of the sizes that the norm, the quantiser and the 8-bit product
+take: what is refused is what no launch can hold, and nothing else.  An accepted
+size goes on to the check for NULL, which stops every call here."""
+import ctypes
+
+import pytest
+
+import selective_state_space_80_amd as mamba
+
+F32, BF16 = mamba.MAMBA_F32, mamba.MAMBA_BF16
+OK, ENULL, ESHAPE = 0, 1, 2
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return mamba.load_library()
+
+
+def _p(k):
+    return ctypes.c_void_p(k << 40)  # never dereferenced
+
+
+# Four rows a workgroup of 256 threads: 2^24 workgroups would have 2^32 threads,
+# one more than a launch takes.
+@pytest.mark.parametrize("M,D,want", [
+    ((1 << 26) - 3, 512, ESHAPE), ((1 << 26) - 1, 4096, ESHAPE), ((1 << 26) - 4, 512, ENULL),
+    ((1 << 26) - 4, 4096, ENULL), ((1 << 22) - 1, 4097, ENULL), (1 << 22, 4097, ESHAPE)])
+def test_rows(lib, M, D, want):
+    assert lib.mamba_rms_norm(None, None, _p(3), _p(4), None, M, D, 1e-5, BF16, F32, None) == want
+    assert lib.mamba_rms_norm_int8(None, None, _p(3), _p(4), _p(5), None, M, D, 1e-5, F32, F32, None) == want
+    assert lib.mamba_quantize_int8(None, _p(2), _p(3), 1, M, D, 0, BF16, None) == want
