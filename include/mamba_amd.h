@@ -450,8 +450,9 @@ mamba_status mamba_quantize_int8(const void *x, int8_t *q, float *scale, int64_t
  *   b, b_scale : [batch, N, K], [batch, N]; with MAMBA_INT8_SHARED_B [N, K], [N]
  *   out        : [batch, M, N] of `out_type`
  * K from 0 (zeros) to 131071, operands at any address; K a multiple of 16 with
- * 16-byte aligned operands is fastest.  At most 2^23 tiles of 128 x 128 outputs
- * a call.  Needs no workspace.
+ * 16-byte aligned operands is fastest.  Fewer than 2^30 tiles of 128 x 64 outputs
+ * a batch (with MAMBA_INT8_SHARED_B alone, of all batches' rows).  Needs no
+ * workspace.
  */
 mamba_status mamba_int8_matmul(const int8_t *a, const int8_t *b, const float *a_scale, const float *b_scale,
                                void *out, int64_t batch, int64_t M, int64_t N, int64_t K, mamba_dtype out_type,

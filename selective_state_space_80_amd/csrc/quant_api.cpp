@@ -69,8 +69,6 @@ mamba_status norm_entry(const void *x, const void *residual, const float *weight
 
 constexpr unsigned kMatmulFlags = MAMBA_INT8_SHARED_A | MAMBA_INT8_SHARED_B;
 
-int64_t operand_rows(int64_t batch, int64_t rows, unsigned shared) { return shared ? rows : batch * rows; }
-
 }  // namespace
 
 extern "C" {
@@ -182,21 +180,24 @@ mamba_status mamba_int8_matmul(const int8_t *a, const int8_t *b, const float *a_
 {
     if (!valid_dtype(out_type))
         return MAMBA_ERR_DTYPE;
-    if (!sizes_ok(batch, M, N) || !sizes_ok(batch, M, K) || !sizes_ok(batch, N, K))
+    const bool a_shared = (flags & MAMBA_INT8_SHARED_A) != 0, b_shared = (flags & MAMBA_INT8_SHARED_B) != 0;
+    if (!sizes_ok(batch, M, N) || !sizes_ok(a_shared ? 1 : batch, M, K) || !sizes_ok(b_shared ? 1 : batch, N, K))
         return MAMBA_ERR_SHAPE;
     if (K > mamba::kMaxInner || (flags & ~kMatmulFlags) != 0)
         return MAMBA_ERR_UNSUPPORTED;
-    // launch grid: one workgroup of at most 512 threads per 128 x 128 outputs
-    if (batch > 0 && ((M + 127) / 128) * ((N + 127) / 128) >= (int64_t(1) << 23) / batch)
-        return MAMBA_ERR_SHAPE;
     if (batch * M * N == 0)
         return MAMBA_OK;
+    // The kernels number a batch's tiles, of 128 x 64 outputs at least where there
+    // are many, in 32 bits, twice a row of them included.  Workgroups go from tile
+    // to tile, so the launch itself sets no limit.
+    const int64_t rows = b_shared && !a_shared ? batch * M : M;  // batches of one right operand are one
+    if ((rows + 127) / 128 * ((N + 63) / 64) >= int64_t(1) << 30)
+        return MAMBA_ERR_SHAPE;
     if (!out || !a_scale || !b_scale || (K > 0 && (!a || !b)))
         return MAMBA_ERR_NULL;
     if (!aligned(a_scale, 4) || !aligned(b_scale, 4) || !aligned(out, esize(out_type)))
         return MAMBA_ERR_ALIGN;
-    const int64_t rows_a = operand_rows(batch, M, flags & MAMBA_INT8_SHARED_A),
-                  rows_b = operand_rows(batch, N, flags & MAMBA_INT8_SHARED_B);
+    const int64_t rows_a = a_shared ? M : batch * M, rows_b = b_shared ? N : batch * N;
     const Range ro = rng(out, (size_t)(batch * M * N) * esize(out_type));
     const Range ins[] = {rng(a, (size_t)(rows_a * K)), rng(b, (size_t)(rows_b * K)),
                          rng(a_scale, (size_t)rows_a * 4), rng(b_scale, (size_t)rows_b * 4)};
@@ -207,8 +208,7 @@ mamba_status mamba_int8_matmul(const int8_t *a, const int8_t *b, const float *a_
     if (st != MAMBA_OK)
         return st;
     mamba::Int8MatmulArgs args{a, b, a_scale, b_scale, out, batch, M, N, K,
-                               (flags & MAMBA_INT8_SHARED_A) != 0, (flags & MAMBA_INT8_SHARED_B) != 0,
-                               out_type == MAMBA_BF16};
+                               a_shared, b_shared, out_type == MAMBA_BF16};
     return launched(mamba::launch_int8_matmul(args, (hipStream_t)stream));
 }
 
