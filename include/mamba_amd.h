@@ -56,6 +56,7 @@
 extern "C" {
 #endif
 
+/* Raised when a signature or its meaning changes, not when functions are added. */
 #define MAMBA_AMD_ABI_VERSION 9
 #define MAMBA_MAX_STATE 16
 #define MAMBA_MAX_CONV_TAPS 8

@@ -81,14 +81,18 @@ def load_library(path: str = LIBRARY):
                            " (the HIP library is required, there is no fallback)")
     lib = ctypes.CDLL(path)
     P, I64, I32, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+    rebuild = "rebuild it (`python -m selective_state_space_80_amd.build`)"
+    # entry points are added without a new version: callers of the others need none
+    missing = [name for name in EXPORTED if not hasattr(lib, name)]
+    if missing:
+        raise RuntimeError(f"{path} lacks {', '.join(missing)}: {rebuild}")
     lib.mamba_status_string.restype = ctypes.c_char_p
     lib.mamba_status_string.argtypes = [I32]
     lib.mamba_abi_version.restype = I32
     lib.mamba_abi_version.argtypes = []
     if lib.mamba_abi_version() != ABI_VERSION:
         raise RuntimeError(f"{path} has ABI version {lib.mamba_abi_version()}, this binding "
-                           f"follows {ABI_VERSION}: rebuild it (`python -m "
-                           "selective_state_space_80_amd.build`)")
+                           f"follows {ABI_VERSION}: {rebuild}")
     lib.mamba_conv1d_silu.restype = I32
     lib.mamba_conv1d_silu.argtypes = [P, P, P, P, I64, I64, I64, I64, I32, P]
     lib.mamba_selective_scan_fwd_workspace_size.restype = SZ
