@@ -460,6 +460,19 @@ mamba_status mamba_int8_matmul(const int8_t *a, const int8_t *b, const float *a_
                                unsigned flags, void *stream);
 
 /*
+ * Diagnostic hook for tests: which kernel mamba_int8_matmul takes for these sizes,
+ * with both operands 16-byte aligned or not (the flags as there).  Needs no GPU.
+ *   form  : 0 tiles of 256 x 256 outputs, 1 of 128 x 128 in two stages, 2 of
+ *           128 x 128 in four, 3 of 128 x 64; then rings of 64 x 64 (4), 48 x 64,
+ *           64 x 48, 32 x 64, 64 x 32, 32 x 32, 16 x 32, 32 x 16, 16 x 16 (12);
+ *           -1 for an empty product
+ *   tiles : output tiles of the whole call
+ *   slots : tiles taken at once (the tile forms' workgroups go on to further ones)
+ */
+mamba_status mamba_int8_matmul_form(int64_t batch, int64_t M, int64_t N, int64_t K, int aligned16, unsigned flags,
+                                    int *form, int64_t *tiles, int *slots);
+
+/*
  * Profiling hook.  When both are non-NULL hipEvent_t handles (passed as
  * void*), later calls made from this host thread record `start` right before
  * and `stop` right after the main scan kernel of mamba_selective_scan_fwd (and

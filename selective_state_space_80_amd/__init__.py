@@ -26,6 +26,7 @@ Entry points (same names as the C ABI, without the ``mamba_`` prefix):
   rms_norm_bwd(dy, h, weight, dresidual_out=None, eps=1e-5, workspace=None)
   quantize_int8(x, channel_major=False, out=None, scale=None)
   int8_matmul(a, b, a_scale, b_scale, out_dtype=torch.bfloat16, out=None)
+  int8_matmul_form(M, N, K, batch=1, aligned=True, flags=0)   diagnostic
   selective_scan_check(workspace)        the carry's error word (after a sync)
   set_scan_spin_limit(polls)             diagnostic bound of the carry waits
 Test helper: set_carry_checks(True) checks the carry after every scan call.
@@ -60,7 +61,7 @@ EXPORTED = ["mamba_status_string", "mamba_abi_version", "mamba_conv1d_silu",
             "mamba_selective_scan_check", "mamba_set_scan_spin_limit",
             "mamba_selective_scan_fwd_noalloc", "mamba_rms_norm", "mamba_rms_norm_int8",
             "mamba_rms_norm_bwd_workspace_size", "mamba_rms_norm_bwd", "mamba_quantize_int8",
-            "mamba_int8_matmul"]
+            "mamba_int8_matmul", "mamba_int8_matmul_form"]
 
 _lib = None
 
@@ -139,6 +140,8 @@ def load_library(path: str = LIBRARY):
     lib.mamba_quantize_int8.argtypes = [P] * 3 + [I64, I64, I64, I32, I32, P]
     lib.mamba_int8_matmul.restype = I32
     lib.mamba_int8_matmul.argtypes = [P] * 5 + [I64, I64, I64, I64, I32, U32, P]
+    lib.mamba_int8_matmul_form.restype = I32
+    lib.mamba_int8_matmul_form.argtypes = [I64] * 4 + [I32, U32, P, P, P]
     _lib = lib
     return lib
 
@@ -803,6 +806,17 @@ def int8_matmul(a, b, a_scale, b_scale, out_dtype=None, out=None):
     if st:
         _raise(st, "mamba_int8_matmul")
     return out
+
+
+def int8_matmul_form(M, N, K, batch=1, aligned=True, flags=0):
+    """Diagnostic: which kernel int8_matmul takes for these sizes, as (form, tiles,
+    slots) of mamba_int8_matmul_form.  Needs no GPU."""
+    form, tiles, slots = ctypes.c_int(), ctypes.c_int64(), ctypes.c_int()
+    st = load_library().mamba_int8_matmul_form(batch, M, N, K, 1 if aligned else 0, flags, ctypes.byref(form),
+                                               ctypes.byref(tiles), ctypes.byref(slots))
+    if st:
+        _raise(st, "mamba_int8_matmul_form")
+    return form.value, tiles.value, slots.value
 
 
 def set_scan_timing_events_raw(start=None, stop=None):

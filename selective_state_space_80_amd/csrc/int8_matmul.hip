@@ -752,40 +752,54 @@ template <int FM, int FN, int STAGES> hipError_t ring(const MatmulParams &p, boo
 }
 
 bool off16(const void *p) { return (uintptr_t)p % 16 != 0; }
+bool is_direct(const Int8MatmulArgs &a) { return a.K % 16 == 0 && !off16(a.a) && !off16(a.b); }
 
 }  // namespace
 
-hipError_t launch_int8_matmul(const Int8MatmulArgs &a, hipStream_t s)
+Int8MatmulForm int8_matmul_form(const Int8MatmulArgs &a)
 {
     // one right operand for every batch: the batches' rows follow one another
     const bool joined = a.b_shared && !a.a_shared;
-    const int64_t batch = joined ? 1 : a.batch, M = joined ? a.batch * a.M : a.M;
-    const bool direct = a.K % 16 == 0 && !off16(a.a) && !off16(a.b);
-    const Form f = choose(batch, M, a.N, a.K, direct);
-    const FormCost &c = kCosts[direct].of[f];
+    Int8MatmulForm r{};
+    r.batch = joined ? 1 : a.batch;
+    r.M = joined ? a.batch * a.M : a.M;
+    const bool direct = is_direct(a);
+    r.form = choose(r.batch, r.M, a.N, a.K, direct);
+    const FormCost &c = kCosts[direct].of[r.form];
+    r.slots = c.slots;
+    r.tile_m = c.tm;
+    r.tile_n = c.tn;
+    r.tiles = tiles_of(c, r.batch, r.M, a.N);
+    return r;
+}
+
+hipError_t launch_int8_matmul(const Int8MatmulArgs &a, hipStream_t s)
+{
+    const bool direct = is_direct(a);
+    const Int8MatmulForm f = int8_matmul_form(a);
     MatmulParams p{};
     p.a = a.a;
     p.b = a.b;
     p.a_scale = a.a_scale;
     p.b_scale = a.b_scale;
     p.out = a.out;
-    p.M = M;
+    p.M = f.M;
     p.N = a.N;
     p.K = (int)a.K;
     p.steps = a.K > 0 ? (int)((a.K + kStep - 1) / kStep) : 1;
-    p.a_batch = a.a_shared ? 0 : M;
+    p.a_batch = a.a_shared ? 0 : f.M;
     p.b_batch = a.b_shared ? 0 : a.N;
-    p.tiles_m = (int)((M + c.tm - 1) / c.tm);
-    p.tiles_n = (int)((a.N + c.tn - 1) / c.tn);
-    p.tiles = tiles_of(c, batch, M, a.N);
-    switch (f) {
-    case kTile256: return tile<2, 4, 4, 2, 2, true>(p, kCus, a.bf16, s);
+    p.tiles_m = (int)((f.M + f.tile_m - 1) / f.tile_m);
+    p.tiles_n = (int)((a.N + f.tile_n - 1) / f.tile_n);
+    p.tiles = f.tiles;
+    switch (f.form) {
+    case kTile256: return tile<2, 4, 4, 2, 2, true>(p, f.slots, a.bf16, s);
     case kTile128:
-        return direct ? tile<2, 2, 2, 2, 2, true>(p, 2 * kCus, a.bf16, s) : tile<2, 2, 2, 2, 2, false>(p, 2 * kCus, a.bf16, s);
+        return direct ? tile<2, 2, 2, 2, 2, true>(p, f.slots, a.bf16, s) : tile<2, 2, 2, 2, 2, false>(p, f.slots, a.bf16, s);
     case kTile128Deep:
-        return direct ? tile<4, 2, 1, 2, 4, true>(p, kCus, a.bf16, s) : tile<4, 2, 1, 2, 4, false>(p, kCus, a.bf16, s);
+        return direct ? tile<4, 2, 1, 2, 4, true>(p, f.slots, a.bf16, s) : tile<4, 2, 1, 2, 4, false>(p, f.slots, a.bf16, s);
     case kTile64:
-        return direct ? tile<4, 1, 1, 2, 3, true>(p, kCus, a.bf16, s) : tile<4, 1, 1, 2, 3, false>(p, kCus, a.bf16, s);
+        return direct ? tile<4, 1, 1, 2, 3, true>(p, f.slots, a.bf16, s) : tile<4, 1, 1, 2, 3, false>(p, f.slots, a.bf16, s);
     case kRing44: return ring<4, 4, 1>(p, direct, a.bf16, s);
     case kRing43: return ring<4, 3, 1>(p, direct, a.bf16, s);
     case kRing34: return ring<3, 4, 1>(p, direct, a.bf16, s);

@@ -63,4 +63,14 @@ struct Int8MatmulArgs {
 };
 hipError_t launch_int8_matmul(const Int8MatmulArgs &a, hipStream_t s);
 
+// Which kernel a product takes (addresses count for their alignment only).
+struct Int8MatmulForm {
+    int form;           // number of the form
+    int slots;          // workgroups that run at once; rings: one a tile
+    int tile_m, tile_n; // outputs of a tile
+    int64_t batch, M;   // of one product, batches of one right operand joined
+    int64_t tiles;
+};
+Int8MatmulForm int8_matmul_form(const Int8MatmulArgs &a);
+
 }  // namespace mamba

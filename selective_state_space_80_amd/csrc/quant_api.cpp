@@ -69,6 +69,20 @@ mamba_status norm_entry(const void *x, const void *residual, const float *weight
 
 constexpr unsigned kMatmulFlags = MAMBA_INT8_SHARED_A | MAMBA_INT8_SHARED_B;
 
+mamba_status matmul_sizes(int64_t batch, int64_t M, int64_t N, int64_t K, unsigned flags)
+{
+    const bool a_shared = (flags & MAMBA_INT8_SHARED_A) != 0, b_shared = (flags & MAMBA_INT8_SHARED_B) != 0;
+    if (!sizes_ok(batch, M, N) || !sizes_ok(a_shared ? 1 : batch, M, K) || !sizes_ok(b_shared ? 1 : batch, N, K))
+        return MAMBA_ERR_SHAPE;
+    if (K > mamba::kMaxInner || (flags & ~kMatmulFlags) != 0)
+        return MAMBA_ERR_UNSUPPORTED;
+    // The kernels number a batch's tiles, of 128 x 64 outputs at least where there
+    // are many, in 32 bits, twice a row of them included.  Workgroups go from tile
+    // to tile, so the launch itself sets no limit.
+    const int64_t rows = b_shared && !a_shared ? batch * M : M;  // batches of one right operand are one
+    return (rows + 127) / 128 * ((N + 63) / 64) < int64_t(1) << 30 ? MAMBA_OK : MAMBA_ERR_SHAPE;
+}
+
 }  // namespace
 
 extern "C" {
@@ -180,19 +194,10 @@ mamba_status mamba_int8_matmul(const int8_t *a, const int8_t *b, const float *a_
 {
     if (!valid_dtype(out_type))
         return MAMBA_ERR_DTYPE;
+    const mamba_status sizes = matmul_sizes(batch, M, N, K, flags);
+    if (sizes != MAMBA_OK || batch * M * N == 0)
+        return sizes;
     const bool a_shared = (flags & MAMBA_INT8_SHARED_A) != 0, b_shared = (flags & MAMBA_INT8_SHARED_B) != 0;
-    if (!sizes_ok(batch, M, N) || !sizes_ok(a_shared ? 1 : batch, M, K) || !sizes_ok(b_shared ? 1 : batch, N, K))
-        return MAMBA_ERR_SHAPE;
-    if (K > mamba::kMaxInner || (flags & ~kMatmulFlags) != 0)
-        return MAMBA_ERR_UNSUPPORTED;
-    if (batch * M * N == 0)
-        return MAMBA_OK;
-    // The kernels number a batch's tiles, of 128 x 64 outputs at least where there
-    // are many, in 32 bits, twice a row of them included.  Workgroups go from tile
-    // to tile, so the launch itself sets no limit.
-    const int64_t rows = b_shared && !a_shared ? batch * M : M;  // batches of one right operand are one
-    if ((rows + 127) / 128 * ((N + 63) / 64) >= int64_t(1) << 30)
-        return MAMBA_ERR_SHAPE;
     if (!out || !a_scale || !b_scale || (K > 0 && (!a || !b)))
         return MAMBA_ERR_NULL;
     if (!aligned(a_scale, 4) || !aligned(b_scale, 4) || !aligned(out, esize(out_type)))
@@ -210,6 +215,33 @@ mamba_status mamba_int8_matmul(const int8_t *a, const int8_t *b, const float *a_
     mamba::Int8MatmulArgs args{a, b, a_scale, b_scale, out, batch, M, N, K,
                                a_shared, b_shared, out_type == MAMBA_BF16};
     return launched(mamba::launch_int8_matmul(args, (hipStream_t)stream));
+}
+
+mamba_status mamba_int8_matmul_form(int64_t batch, int64_t M, int64_t N, int64_t K, int aligned16, unsigned flags,
+                                    int *form, int64_t *tiles, int *slots)
+{
+    const bool a_shared = (flags & MAMBA_INT8_SHARED_A) != 0, b_shared = (flags & MAMBA_INT8_SHARED_B) != 0;
+    if (!form || !tiles || !slots)
+        return MAMBA_ERR_NULL;
+    const mamba_status st = matmul_sizes(batch, M, N, K, flags);
+    if (st != MAMBA_OK || batch * M * N == 0) {
+        *form = -1;
+        *tiles = *slots = 0;
+        return st;
+    }
+    mamba::Int8MatmulArgs args{};
+    args.a = aligned16 ? nullptr : (const int8_t *)1;  // for its alignment
+    args.batch = batch;
+    args.M = M;
+    args.N = N;
+    args.K = K;
+    args.a_shared = a_shared;
+    args.b_shared = b_shared;
+    const mamba::Int8MatmulForm f = mamba::int8_matmul_form(args);
+    *form = f.form;
+    *tiles = f.tiles;
+    *slots = f.slots;
+    return MAMBA_OK;
 }
 
 }  // extern "C"
