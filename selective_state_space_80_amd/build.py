@@ -26,6 +26,8 @@ ARCH = "gfx950"
 # scalar fp32 issue and must not be rewritten into v_pk_* by the compiler.
 HIPCC_FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
                "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+               # a launch bound or an unrolling that the compiler cannot meet ends the build
+               "-Werror=pass-failed",
                "-Wall", "-Wno-unused-function", "-I", INCLUDE, "-I", CSRC]
 
 

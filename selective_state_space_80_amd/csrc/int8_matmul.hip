@@ -205,19 +205,30 @@ __device__ __forceinline__ Share xcd_share(int64_t tiles, int xcd)
 // caches, issued without branches, and not waited for by the next tile's first
 // step (8 x 5120 x 2048 x 2560: 178 us, by way of the caches 204; before also
 // guarded, waited for, and with the scales loaded there 212).
+constexpr int kStaging = 4096;  // of a wave's outputs: 32 rows of 128 bytes
+constexpr int tile_lds(int WM, int WN, int FM, int FN, int STAGES)
+{
+    return STAGES * (WM * FM + WN * FN) * 32 * kStep + WM * WN * kStaging;
+}
+// Waves of a SIMD that the LDS leaves room for: 2, or 1 for tiles of 128 x 64
+// (88 KB, so one workgroup of four waves a CU).
+constexpr int tile_waves(int WM, int WN, int FM, int FN, int STAGES)
+{
+    return 160 * 1024 / tile_lds(WM, WN, FM, FN, STAGES) * WM * WN / 4;
+}
+
 template <int WM, int WN, int FM, int FN, int STAGES, bool DIRECT, bool BF16, bool STREAM>
-__global__ __launch_bounds__(64 * WM * WN, 2) void tile_kernel(const MatmulParams p)
+__global__ __launch_bounds__(64 * WM * WN, tile_waves(WM, WN, FM, FN, STAGES)) void tile_kernel(const MatmulParams p)
 {
     constexpr int TM = WM * FM * 32, TN = WN * FN * 32, NW = WM * WN;
     constexpr int kStage = (TM + TN) * kStep;
     constexpr int LA = TM / 8 / NW, LB = TN / 8 / NW;  // loads of a wave and stage
-    constexpr int kStaging = 4096;                     // of a wave's outputs: 32 rows of 128 bytes
     constexpr int SA = (FM + 1) / 2, SB = (FN + 1) / 2;  // registers of a wave's scales
     constexpr int kWide = BF16 ? 2 : 1;                // blocks of 32 columns in 128 bytes
     constexpr int kPerChunk = BF16 ? 8 : 4;            // elements in 16 bytes
     constexpr int kStores = FM * 4 * (FN / kWide);     // of a wave and a whole tile
     static_assert(FN % kWide == 0, "a wave's columns fill whole lines");
-    __shared__ __attribute__((aligned(16))) char smem[STAGES * kStage + NW * kStaging];
+    __shared__ __attribute__((aligned(16))) char smem[tile_lds(WM, WN, FM, FN, STAGES)];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave % WM, wn = wave / WM;
