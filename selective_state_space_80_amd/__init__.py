@@ -193,6 +193,17 @@ def _check(t, name, shape, dtype=None, device=None, optional=False):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
+def _workspace(workspace, need, device):
+    """(the caller's workspace, or one made here; its bytes)."""
+    if workspace is None:
+        workspace = _torch().empty(max(need, 1), dtype=_torch().uint8, device=device)
+    elif workspace.device != device:  # the kernels would write to it
+        raise ValueError(f"workspace is on {workspace.device}, expected {device}")
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
 def _stream(device):
     return ctypes.c_void_p(_torch().cuda.current_stream(device).cuda_stream)
 
@@ -258,7 +269,8 @@ def selective_scan_check(workspace) -> None:
     """Wait for the workspace's stream, then raise MambaError(MAMBA_ERR_TIMEOUT)
     if a carry wait of the calls that last used it gave up (their affected
     outputs are NaN)."""
-    st = load_library().mamba_selective_scan_check(_ptr(workspace), workspace.numel(),
+    st = load_library().mamba_selective_scan_check(_ptr(workspace),
+                                                   workspace.numel() * workspace.element_size(),
                                                    _stream(workspace.device))
     _raise(st, "mamba_selective_scan_check")
 
@@ -311,19 +323,18 @@ def selective_scan_fwd(x, dt, A, Bm, Cm, dt_bias=None, Dskip=None, z=None, h0=No
     _check(h_last, "h_last", (B, D, N), torch.float32, dev, optional=True)
     io = _io_dtype(x)
     need = int(lib.mamba_selective_scan_fwd_workspace_size(B, D, L, N, io))
-    if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    workspace, workspace_bytes = _workspace(workspace, need, dev)
     flags = (MAMBA_SCAN_REVERSE if reverse else 0) | (MAMBA_SCAN_ACCUMULATE if accumulate else 0)
     if flags:
         st = lib.mamba_selective_scan_fwd_ex(
             _ptr(x), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(Dskip), _ptr(z),
-            _ptr(h0), _ptr(out), _ptr(h_last), _ptr(workspace), workspace.numel(), B, D, L, N, io,
+            _ptr(h0), _ptr(out), _ptr(h_last), _ptr(workspace), workspace_bytes, B, D, L, N, io,
             flags, _stream(dev))
         _raise(st, "mamba_selective_scan_fwd_ex")
     else:
         st = lib.mamba_selective_scan_fwd(
             _ptr(x), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(Dskip), _ptr(z),
-            _ptr(h0), _ptr(out), _ptr(h_last), _ptr(workspace), workspace.numel(), B, D, L, N,
+            _ptr(h0), _ptr(out), _ptr(h_last), _ptr(workspace), workspace_bytes, B, D, L, N,
             io, _stream(dev))
         _raise(st, "mamba_selective_scan_fwd")
     _after_scan(workspace, need)
@@ -406,12 +417,11 @@ def conv1d_selective_scan_fwd(x_raw, conv_w, dt, A, Bm, Cm, conv_bias=None, conv
     _check(conv_state_out, "conv_state_out", (B, D, K - 1), io_t, dev, optional=True)
     io = _io_dtype(x_raw)
     need = int(lib.mamba_selective_scan_fwd_workspace_size(B, D, L, N, io))
-    if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    workspace, workspace_bytes = _workspace(workspace, need, dev)
     st = lib.mamba_conv1d_selective_scan_fwd(
         _ptr(x_raw), _ptr(conv_w), _ptr(conv_bias), K, _ptr(conv_state_in), _ptr(conv_state_out),
         _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(Dskip), _ptr(z), _ptr(h0),
-        _ptr(out), _ptr(h_last), _ptr(workspace), workspace.numel(), B, D, L, N, io,
+        _ptr(out), _ptr(h_last), _ptr(workspace), workspace_bytes, B, D, L, N, io,
         _stream(dev))
     _raise(st, "mamba_conv1d_selective_scan_fwd")
     _after_scan(workspace, need)
@@ -552,13 +562,12 @@ def selective_scan_bwd(x, dt, A, Bm, Cm, dout, dt_bias=None, Dskip=None, z=None,
          "ddt_bias": torch.empty((D,), **f32), "dh0": torch.empty((B, D, N), **f32)}
     io = _io_dtype(x)
     need = int(lib.mamba_selective_scan_bwd_workspace_size(B, D, L, N, io))
-    if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    workspace, workspace_bytes = _workspace(workspace, need, dev)
     st = lib.mamba_selective_scan_bwd(
         _ptr(x), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(Dskip), _ptr(z),
         _ptr(h0), _ptr(dout), _ptr(dh_last), _ptr(g["dx"]), _ptr(g["ddt"]), _ptr(g["dA"]),
         _ptr(g["dB"]), _ptr(g["dC"]), _ptr(g["dD"]), _ptr(g["dz"]), _ptr(g["ddt_bias"]),
-        _ptr(g["dh0"]), _ptr(workspace), workspace.numel(), B, D, L, N, io, _stream(dev))
+        _ptr(g["dh0"]), _ptr(workspace), workspace_bytes, B, D, L, N, io, _stream(dev))
     _raise(st, "mamba_selective_scan_bwd")
     _after_scan(workspace, need)
     return g
@@ -714,14 +723,12 @@ def rms_norm_bwd(dy, h, weight, dresidual_out=None, eps=1e-5, workspace=None):
     dx = torch.empty_like(dy)
     dresidual = None if h_t == dy.dtype else torch.empty_like(h)
     dweight = torch.empty_like(weight)
-    if workspace is None:
-        need = lib.mamba_rms_norm_bwd_workspace_size(M, D)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    need = lib.mamba_rms_norm_bwd_workspace_size(M, D) if workspace is None else 0
+    workspace, workspace_bytes = _workspace(workspace, need, dev)
     st = lib.mamba_rms_norm_bwd(
         dy.data_ptr(), h.data_ptr(), weight.data_ptr(), _addr(dresidual_out), dx.data_ptr(),
-        _addr(dresidual), dweight.data_ptr(), _addr(workspace),
-        0 if workspace is None else workspace.numel(), M, D, eps, _io_dtype(dy), _io_dtype(h),
-        _raw_stream(dy))
+        _addr(dresidual), dweight.data_ptr(), workspace.data_ptr(), workspace_bytes, M, D, eps,
+        _io_dtype(dy), _io_dtype(h), _raw_stream(dy))
     if st:
         _raise(st, "mamba_rms_norm_bwd")
     return {"dx": dx, "dresidual": dx if dresidual is None else dresidual, "dweight": dweight}
