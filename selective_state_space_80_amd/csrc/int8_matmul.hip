@@ -195,16 +195,17 @@ __device__ __forceinline__ Share xcd_share(int64_t tiles, int xcd)
 // there every wave has read this stage (it may be overwritten) and the next
 // stage has arrived.
 //
-// What bounds it is the card's power: 256 x 256 outputs by 8 waves fill the
-// matrix units to 62 % at 1.85 GHz on random data (2.45 POP/s at 8192^3, where
-// the library's 8-bit product reaches 2.14).  With zeros as data the clock
-// stays at 2.4 GHz; without any loads, on random data, the products alone
-// reach 2.75.  LDS is read a quarter of the time and without bank conflicts.
-// Of a tile's end, 5 us of the model below, most is arithmetic (3.5
-// instructions an output) and the stores' way to memory: whole lines past the
-// caches, issued without branches, and not waited for by the next tile's first
-// step (8 x 5120 x 2048 x 2560: 178 us, by way of the caches 204; before also
-// guarded, waited for, and with the scales loaded there 212).
+// What bounds it is the card's power: 256 x 256 outputs by 8 waves keep the
+// matrix units busy for 68 % of the cycles at 8192^3 on random data, at clocks
+// that go down to 1.85 GHz (2.28 to 2.45 POP/s from card to card and run to run,
+// where the library's 8-bit product reaches 2.14).  With zeros as data the clock
+// stays at 2.4 GHz; without any loads, on random data, the products alone reach
+// 2.75.  LDS is read a quarter of the time, nearly without bank conflicts.  Of a
+// tile's end most is arithmetic (3.5 instructions an output) and the stores' way
+// to memory: whole lines past the caches, issued without branches, and not waited
+// for by the next tile's first step (8 x 5120 x 2048 x 2560, on one card: 178 us,
+// by way of the caches 204; before also guarded, waited for, and with the scales
+// loaded there 212; from card to card and with a trace running, 178 to 212).
 constexpr int kStaging = 4096;  // of a wave's outputs: 32 rows of 128 bytes
 constexpr int tile_lds(int WM, int WN, int FM, int FN, int STAGES)
 {

@@ -17,10 +17,11 @@
 // of their own.
 //
 // Bound by memory.  8 x 5120 x 2048 bf16 (252 MB) takes 44 us (5.7 TB/s) with
-// the input in the last-level cache, where a scan has just left it, and 62 us
+// the input in the last-level cache, where a scan has just left it, and 69 us
 // from memory: there is room for one workgroup a CU, so its loads do not
-// overlap its stores.  1 x 1536 x 131072 bf16 (604 MB) takes 133 us;
-// 64 x 5120 x 4 bf16 3.5 us, bound by its launch and its two dependent waits.
+// overlap its stores.  1 x 1536 x 131072 bf16 (604 MB) takes 135 us;
+// 64 x 5120 x 4 bf16 3.6 us, bound by its launch and its two dependent waits.
+// (Times in this file are from memory, inputs taken in turn, unless said.)
 #include <hip/hip_runtime.h>
 
 #include "quant.h"
@@ -95,9 +96,9 @@ template <bool BF16> __device__ __forceinline__ uint32_t max_abs(uint32_t top, u
 // each: so each XCD starts an eighth of its share after the one before, and
 // where rows repeat every 4 KB, the 64-byte tiles (about 32 of an XCD run at
 // once) go first by every second pair and then by the others.  8 x 5120 x 2048
-// bf16 67 us without either, 69 with the first, 62 with both; fp32 111, 98,
-// 102; 2 x 5120 x 4096 fp32 60, 56, 47; 8 x 8192 x 2048, in 32-byte tiles, 149
-// and 128 (132 with both).
+// bf16 74 us without either, 74 with the first, 69 with both; fp32 112, 100,
+// 103; 2 x 5120 x 4096 fp32 64, 60, 54; 8 x 8192 x 2048 bf16, in 32-byte tiles,
+// 147 and 128.
 template <int PARTS> __device__ __forceinline__ int64_t tile_of(int64_t row_bytes)
 {
     const int64_t all = gridDim.x, xcd = blockIdx.x % 8, more = all % 8;
@@ -432,19 +433,20 @@ template <bool BF16> hipError_t dispatch(const QuantChannelArgs &a, hipStream_t 
         quantize_channel_kernel<BF16, 4, kMostThreads, 0, true><<<dim3((unsigned)tiles), dim3(64), 0, s>>>(p);
         return hipGetLastError();
     }
-    // Whole tiles take over from 16 bytes on (64 x 5120 x 7 bf16 4.6 us so and
-    // 64 x 5120 x 8 6.1; x 7 token by token 31.6).
+    // Whole tiles take over from 16 bytes on (64 x 5120 x 7 bf16 5.1 us so and
+    // 64 x 5120 x 8 6.8; x 7 token by token 31.6).
     if (a.L < kTok)
         return start_short<BF16, 1>(a, s);
     // Few tiles leave most CUs idle: below half a tile a CU, tiles of 16 bytes by a
-    // quarter of the threads (from memory, bf16 in us: 1 x 5120 x 1000 11.3, in tiles
-    // of 32 bytes 14.1; 2 x 5120 x 1024 13.2 and 17.2; but 1 x 5120 x 8000, 250
-    // tiles, 44 so and 26 in tiles of 64 bytes).
+    // quarter of the threads (bf16, in us, so and in tiles of 64 bytes: 1 x 5120 x
+    // 1000 11.4 and 16.9; 2 x 5120 x 1024 13.1 and 18.8; 1 x 5120 x 3000 23.4 and
+    // 25.4; but 4000 24.7 and 23.4; 8000 44 and 30).
     if (a.K <= kHeldChannels)
         return tiles < 128 ? start<BF16, 1, kMostThreads / 4>(a, s) : start<BF16, 4, kMostThreads>(a, s);
     // More channels are held by smaller tiles of as many threads, up to the most
-    // that registers hold; read twice instead, 1 x 20000 x 1000 bf16 takes 63 us
-    // (30 so), 8 x 8192 x 2048 168 (127), 2 x 16384 x 2048 77 (48; fp32 126 and 128).
+    // that registers hold; read twice instead, 1 x 20000 x 1000 bf16 takes 109 us
+    // (41 so), 8 x 8192 x 2048 144 (128; fp32 239 and 189), 2 x 16384 x 2048 120
+    // (76; fp32 148 and 133).
     if (a.K <= 2 * kHeldChannels)
         return start<BF16, 2, kMostThreads>(a, s);
     if (a.K <= 4 * kHeldChannels)

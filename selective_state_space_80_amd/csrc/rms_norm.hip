@@ -15,9 +15,9 @@
 //
 // Bound by memory: 16384 x 768 in fp32 with an fp32 residual (201 MB) takes
 // 39 us (5.1 TB/s, the rate of a large copy); 16384 x 2560 bf16 with a bf16
-// residual 59 us, with 8-bit output 46 us (5.7 and 6.4 TB/s, the inputs partly
-// in the last-level cache); 131072 rows of 64 bf16 11 us (26 with a wave to
-// each).  One row of 2560 is bound by its launch.
+// residual 60 us, with 8-bit output 54 us (5.6 and 5.4 TB/s); 131072 rows of 64
+// bf16 6.7 us from the last-level cache (with a wave to each row, more than
+// twice that).  One row of 2560 is bound by its launch.
 #include <hip/hip_runtime.h>
 
 #include "quant.h"
@@ -205,8 +205,12 @@ template <bool XBF, int RES, int MODE> hipError_t pick(const NormParams &p, hipS
     case 32: return start<XBF, RES, MODE, 32, 1, false>(p, 256, s);
     }
     // A wave holds up to 8 chunks a lane (4096 elements); with fewer rows than
-    // fill the card with waves, a workgroup shares a row instead (8-bit
-    // output, in us: 64 x 2560 3.1 so, 3.7 a wave to each; 16384 x 2560 54 and 46).
+    // fill the card with waves, a workgroup shares a row instead.  Both sides, a
+    // workgroup to a row and a wave, bf16 with 8-bit output in us: 256 x 2560 3.4 and
+    // 3.9, 512 4.3 and 4.4, 768 5.1 and 5.0, 1024 5.8 and 5.6, 2048 10.4 and 9.5.  The
+    // bound is a compromise: 768 elements cross at 256 rows (2048 x 768 4.5 and
+    // 4.3), 4096 not up to 4096 rows (1024 x 4096 7.6 and 8.3), nor does fp32
+    // (1024 x 2560 10.9 and 11.1, 4096 33.8 and 35.5).
     const int chunks = (p.D + kChunk - 1) / kChunk;
     const int per_lane = (chunks + 63) / 64;
     if (per_lane <= 1 || (per_lane <= 8 && p.M >= 1024)) {
@@ -220,7 +224,7 @@ template <bool XBF, int RES, int MODE> hipError_t pick(const NormParams &p, hipS
         }
     }
     // Of a shared row a lane takes one chunk up to 512, then two: workgroups of
-    // 1024 lanes leave a CU too few rows at once (bf16, in us: 16384 x 5120 105
+    // 1024 lanes leave a CU too few rows at once (bf16 with 8-bit output, in us: 16384 x 5120 103
     // with two and 130 with one; 8192 x 8192 84 and 93).  Four only where two
     // no longer cover the row.
     const int nc = chunks <= 512 ? 1 : chunks <= 2048 ? 2 : 4;

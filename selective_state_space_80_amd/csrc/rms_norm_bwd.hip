@@ -56,7 +56,9 @@ __global__ __launch_bounds__(LANES ? 256 : NC == 1 ? 512 : 1024) void rms_norm_b
     ChunkAt at[NC];
     // Four chunks a lane leave no registers for the weight, which is then read
     // again for each row, nor for dres_out before it is needed (2048 x 20000,
-    // bf16 with fp32 h: 157 us; with all of it in registers, spilling, 259).
+    // bf16 with fp32 h: 159 us; with all of it in registers, spilling, 259).  Some
+    // values are spilled all the same, 11 or 12 in fp32 and up to 3 in bf16 (2048 x
+    // 20000 in fp32 168 us; 172 when 46 were).
     constexpr bool kLean = NC == 4;
     float w[kLean ? 1 : NC][8], acc[NC][8];
 #pragma unroll
@@ -312,10 +314,10 @@ template <bool XBF, bool HF32, bool DRES> hipError_t pick(const BwdParams &p, in
         return start<XBF, HF32, DRES, 64, 2, false>(p, groups, 256, s);
     // More chunks a lane mean fewer waves with more registers and sums each, so
     // the fewest that the row allows (with dres, four sets of tensors in turn so that
-    // they come from memory, in us: 16384 x 2560 68 with one and 84 with
-    // two, 4096 x 10240 83 with two and 101 with four), except that rows of 513
-    // to 1024 chunks take two, as in the forward pass (4096 x 8192 57 with two and
-    // 61 with one; 8192 x 5120 72 and 71).
+    // they come from memory, in us: 16384 x 2560 67 with one and 84 with
+    // two, 4096 x 10240 81 with two and 101 with four), except that rows of 513
+    // to 1024 chunks take two, as in the forward pass (4096 x 8192 59 with two and
+    // 61 with one; 8192 x 5120 71 and 71).
     const int nc = chunks <= 512 ? 1 : chunks <= 2048 ? 2 : 4;
     const int lanes = (chunks + nc - 1) / nc;
     const int threads = (lanes + 63) / 64 * 64;
