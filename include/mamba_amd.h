@@ -412,8 +412,9 @@ mamba_status mamba_rms_norm_int8(const void *x, const void *residual, const floa
  *                                 256-byte aligned; scratch as in the scan
  * Sums are taken in a fixed order.  With M = 0, dweight is zero.  Rows whose
  * sum of squares passes the fp32 range are taken by a power of two first; where
- * 1/rms itself passes it (rows of denormals with eps = 0), dh is infinite or
- * NaN; a zero row with eps = 0 has dh = dresidual_out.
+ * 1/rms itself passes it (rows of denormals with eps = 0), or the sum of
+ * weight dy h (huge dy), dh is infinite or NaN.  A zero row with eps = 0 has
+ * dh = dresidual_out.
  */
 size_t mamba_rms_norm_bwd_workspace_size(int64_t M, int64_t D);
 mamba_status mamba_rms_norm_bwd(const void *dy, const void *h, const float *weight, const void *dresidual_out,
