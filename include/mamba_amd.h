@@ -11,7 +11,8 @@
  *   mamba_conv1d_update                  single-token conv step with its state
  *   mamba_conv1d_selective_state_update  that conv step and the decode step fused
  * the scan's backward pass (mamba_selective_scan_bwd), the Mamba-2 form of
- * the scan on the matrix cores (mamba_ssd_scan_fwd),
+ * the scan on the matrix cores (mamba_ssd_scan_fwd), a gated linear recurrence
+ * (mamba_gated_scan_fwd, its gradient and its single step),
  * plus workspace sizing and status helpers.
  *
  * Conventions shared by every entry point
@@ -472,6 +473,67 @@ mamba_status mamba_int8_matmul(const int8_t *a, const int8_t *b, const float *a_
  */
 mamba_status mamba_int8_matmul_form(int64_t batch, int64_t M, int64_t N, int64_t K, int aligned16, unsigned flags,
                                     int *form, int64_t *tiles, int *slots);
+
+/*
+ * Gated linear recurrence: a scan whose decay and input are gated by the data,
+ * one state a channel.  With v_t = c softplus(lam) sigmoid(r_t + r_bias):
+ *   a_t = exp(-v_t)
+ *   h_t = a_t h_(t-1) + sqrt(1 - a_t^2) sigmoid(i_t + i_bias) x_t
+ *   y_t = h_t, or h_t SiLU(z_t)
+ *   x, r, i, z, y : [B, D, L] of `io`; z NULL = no output gate
+ *   lam           : [D] float;  r_bias, i_bias : [D] float or NULL (zero)
+ *   h0            : [B, D] float or NULL (zero)
+ *   reset         : [B, L] bytes or NULL; at a step with a non-zero byte a_t = 0,
+ *                   whatever the state before it held (NaN too): the first token
+ *                   of each of the sequences packed in a row
+ *   h_last        : [B, D] float or NULL (not returned)
+ *   checkpoints   : [B, D, mamba_gated_scan_checkpoints(L)] float or NULL: the
+ *                   state before steps 0, 512, 1024, ..., for the backward call
+ * c is finite and not negative.  A step with r = -infinity and a finite x leaves
+ * the state as it is: padded tokens.  A state that becomes infinite is NaN from the
+ * next step that decays it on.  B * D < 2^24.  With L = 0, h_last = h0 (or zeros).
+ */
+int64_t mamba_gated_scan_checkpoints(int64_t L);
+mamba_status mamba_gated_scan_fwd(const void *x, const void *r, const void *i, const float *lam, const float *r_bias,
+                                  const float *i_bias, const void *z, const float *h0, const uint8_t *reset,
+                                  void *y, float *h_last, float *checkpoints, int64_t B, int64_t D, int64_t L,
+                                  float c, mamba_dtype io, void *stream);
+
+/*
+ * Gradients of sum(y * dout) + sum(h_last * dh_last) of mamba_gated_scan_fwd.
+ *   x ... reset          : as in the forward call
+ *   checkpoints          : as the forward call wrote them, or NULL: the forward
+ *                          pass is then run again for them (h0 is read only there)
+ *   dout                 : [B, D, L] of `io`;  dh_last : [B, D] float or NULL (zero)
+ *   dx, dr, di, dz       : [B, D, L] of `io`, required; dz with z only
+ *   dlam, dr_bias, di_bias : [D] float, required: sums over batch and steps, in a
+ *                          fixed order
+ *   dh0                  : [B, D] float, required
+ *   workspace            : mamba_gated_scan_bwd_workspace_size(...) bytes, 256-byte
+ *                          aligned, for checkpoints given (1) or not (0); scratch as
+ *                          in the scan
+ * Where a step keeps everything (v_t = 0), dr_t is zero.  With L = 0 or B = 0 the
+ * parameters' gradients are zero, and dh0 = dh_last (or zeros).
+ */
+size_t mamba_gated_scan_bwd_workspace_size(int64_t B, int64_t D, int64_t L, int with_checkpoints);
+mamba_status mamba_gated_scan_bwd(const void *x, const void *r, const void *i, const float *lam, const float *r_bias,
+                                  const float *i_bias, const void *z, const float *h0, const uint8_t *reset,
+                                  const float *checkpoints, const void *dout, const float *dh_last, void *dx,
+                                  void *dr, void *di, void *dz, float *dlam, float *dr_bias, float *di_bias,
+                                  float *dh0, void *workspace, size_t workspace_bytes, int64_t B, int64_t D,
+                                  int64_t L, float c, mamba_dtype io, void *stream);
+
+/*
+ * One step of the same recurrence (decode).
+ *   h, h_out      : [B, D] float; h_out may be h itself (updated in place) or apart
+ *                   from it (the state before the step is then kept)
+ *   x, r, i, z, y : [B, D] of `io`; z NULL = no output gate
+ *   lam, r_bias, i_bias, c : as above
+ * B * D < 2^31.
+ */
+mamba_status mamba_gated_state_update(const float *h, float *h_out, const void *x, const void *r, const void *i,
+                                      const float *lam, const float *r_bias, const float *i_bias, const void *z,
+                                      void *y, int64_t B, int64_t D, float c, mamba_dtype io, void *stream);
 
 /*
  * Profiling hook.  When both are non-NULL hipEvent_t handles (passed as

@@ -27,6 +27,12 @@ Entry points (same names as the C ABI, without the ``mamba_`` prefix):
   quantize_int8(x, channel_major=False, out=None, scale=None)
   int8_matmul(a, b, a_scale, b_scale, out_dtype=torch.bfloat16, out=None)
   int8_matmul_form(M, N, K, batch=1, aligned=True, flags=0)   diagnostic
+  gated_scan_fwd(x, r, i, lam, r_bias=None, i_bias=None, z=None, h0=None, reset=None, c=8.0,
+                 return_last_state=False, return_checkpoints=False, out=None, ...)
+  gated_scan_bwd(x, r, i, lam, dout, r_bias=None, i_bias=None, z=None, h0=None, reset=None,
+                 dh_last=None, c=8.0, checkpoints=None, workspace=None)
+  gated_scan_bwd_workspace_size(B, D, L, with_checkpoints=True)
+  gated_state_update(h, x, r, i, lam, r_bias=None, i_bias=None, z=None, c=8.0, h_out=None, out=None)
   selective_scan_check(workspace)        the carry's error word (after a sync)
   set_scan_spin_limit(polls)             diagnostic bound of the carry waits
 Test helper: set_carry_checks(True) checks the carry after every scan call.
@@ -61,7 +67,10 @@ EXPORTED = ["mamba_status_string", "mamba_abi_version", "mamba_conv1d_silu",
             "mamba_selective_scan_check", "mamba_set_scan_spin_limit",
             "mamba_selective_scan_fwd_noalloc", "mamba_rms_norm", "mamba_rms_norm_int8",
             "mamba_rms_norm_bwd_workspace_size", "mamba_rms_norm_bwd", "mamba_quantize_int8",
-            "mamba_int8_matmul", "mamba_int8_matmul_form"]
+            "mamba_int8_matmul", "mamba_int8_matmul_form",
+            "mamba_gated_scan_checkpoints", "mamba_gated_scan_fwd",
+            "mamba_gated_scan_bwd_workspace_size", "mamba_gated_scan_bwd",
+            "mamba_gated_state_update"]
 
 _lib = None
 
@@ -142,6 +151,16 @@ def load_library(path: str = LIBRARY):
     lib.mamba_int8_matmul.argtypes = [P] * 5 + [I64, I64, I64, I64, I32, U32, P]
     lib.mamba_int8_matmul_form.restype = I32
     lib.mamba_int8_matmul_form.argtypes = [I64] * 4 + [I32, U32, P, P, P]
+    lib.mamba_gated_scan_checkpoints.restype = I64
+    lib.mamba_gated_scan_checkpoints.argtypes = [I64]
+    lib.mamba_gated_scan_fwd.restype = I32
+    lib.mamba_gated_scan_fwd.argtypes = [P] * 12 + [I64, I64, I64, F, I32, P]
+    lib.mamba_gated_scan_bwd_workspace_size.restype = SZ
+    lib.mamba_gated_scan_bwd_workspace_size.argtypes = [I64, I64, I64, I32]
+    lib.mamba_gated_scan_bwd.restype = I32
+    lib.mamba_gated_scan_bwd.argtypes = [P] * 21 + [SZ, I64, I64, I64, F, I32, P]
+    lib.mamba_gated_state_update.restype = I32
+    lib.mamba_gated_state_update.argtypes = [P] * 10 + [I64, I64, F, I32, P]
     _lib = lib
     return lib
 
@@ -824,6 +843,132 @@ def int8_matmul_form(M, N, K, batch=1, aligned=True, flags=0):
     if st:
         _raise(st, "mamba_int8_matmul_form")
     return form.value, tiles.value, slots.value
+
+
+def _gated_arguments(x, r, i, lam, r_bias, i_bias, z, h0, reset):
+    """Checks shared by the gated recurrence's calls; reset [B, L] for a scan."""
+    torch = _torch()
+    shape, io_t, dev, index = x.shape, x.dtype, x.device, x.get_device()
+    f32 = torch.float32
+    D = shape[1]
+    if not (x.is_contiguous() and _is(r, shape, io_t, index) and _is(i, shape, io_t, index)
+            and _is(lam, (D,), f32, index)):
+        _check(x, "x", shape)
+        _check(r, "r", shape, io_t, dev)
+        _check(i, "i", shape, io_t, dev)
+        _check(lam, "lam", (D,), f32, dev)
+    for t, name in ((r_bias, "r_bias"), (i_bias, "i_bias")):
+        if t is not None and not _is(t, (D,), f32, index):
+            _check(t, name, (D,), f32, dev)
+    if z is not None and not _is(z, shape, io_t, index):
+        _check(z, "z", shape, io_t, dev)
+    if h0 is not None and not _is(h0, shape[:2], f32, index):
+        _check(h0, "h0", shape[:2], f32, dev)
+    if reset is not None:
+        if reset.dtype is not torch.bool and reset.dtype is not torch.uint8:
+            raise TypeError(f"reset must be bool or uint8, got {reset.dtype}")
+        _check(reset, "reset", (shape[0], shape[2]), device=dev)
+
+
+def gated_scan_fwd(x, r, i, lam, r_bias=None, i_bias=None, z=None, h0=None, reset=None, c=8.0,
+                   return_last_state=False, return_checkpoints=False, out=None, h_last=None,
+                   checkpoints=None):
+    """Gated linear recurrence over [B, D, L]: with v = c softplus(lam) sigmoid(r + r_bias) and
+    a = exp(-v), h_t = a_t h_(t-1) + sqrt(1 - a_t^2) sigmoid(i + i_bias) x, y = h or h SiLU(z).
+    x, r, i, z [B,D,L] f32/bf16; lam, r_bias, i_bias [D] f32; h0 [B,D] f32; reset [B,L] bool or
+    uint8: steps at which the state before is dropped (the first token of a packed sequence).
+    A token with r = -inf leaves the state as it is.  Returns y of x's dtype, then h_last [B,D]
+    f32 if return_last_state, then checkpoints [B,D,ceil(L/512)] f32, for gated_scan_bwd, if
+    return_checkpoints."""
+    torch = _torch()
+    lib = load_library()
+    B, D, L = x.shape
+    _gated_arguments(x, r, i, lam, r_bias, i_bias, z, h0, reset)
+    f32 = torch.float32
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _check(out, "out", x.shape, x.dtype, x.device)
+    if h_last is not None:
+        _check(h_last, "h_last", (B, D), f32, x.device)
+    elif return_last_state:
+        h_last = lam.new_empty((B, D))
+    if return_checkpoints or checkpoints is not None:
+        kept = (B, D, lib.mamba_gated_scan_checkpoints(L))
+        if checkpoints is None:
+            checkpoints = lam.new_empty(kept)
+        else:
+            _check(checkpoints, "checkpoints", kept, f32, x.device)
+    st = lib.mamba_gated_scan_fwd(x.data_ptr(), r.data_ptr(), i.data_ptr(), lam.data_ptr(),
+                                  _addr(r_bias), _addr(i_bias), _addr(z), _addr(h0), _addr(reset),
+                                  out.data_ptr(), _addr(h_last), _addr(checkpoints), B, D, L, c,
+                                  _io_dtype(x), _raw_stream(x))
+    if st:
+        _raise(st, "mamba_gated_scan_fwd")
+    got = (out,) + ((h_last,) if return_last_state else ()) + (
+        (checkpoints,) if return_checkpoints else ())
+    return out if len(got) == 1 else got
+
+
+def gated_scan_bwd_workspace_size(B, D, L, with_checkpoints=True) -> int:
+    return int(load_library().mamba_gated_scan_bwd_workspace_size(B, D, L, 1 if with_checkpoints else 0))
+
+
+def gated_scan_bwd(x, r, i, lam, dout, r_bias=None, i_bias=None, z=None, h0=None, reset=None,
+                   dh_last=None, c=8.0, checkpoints=None, workspace=None):
+    """Gradients of sum(y * dout) + sum(h_last * dh_last) of gated_scan_fwd.  checkpoints: as that
+    call returned them (h0 is then not read), or None: its pass is run again for them.  Returns a
+    dict: dx, dr, di, dz (None without z) of x's dtype; dlam, dr_bias, di_bias [D] and dh0 [B,D] f32."""
+    torch = _torch()
+    lib = load_library()
+    B, D, L = x.shape
+    _gated_arguments(x, r, i, lam, r_bias, i_bias, z, h0, reset)
+    dev = x.device
+    _check(dout, "dout", x.shape, x.dtype, dev)
+    _check(dh_last, "dh_last", (B, D), torch.float32, dev, optional=True)
+    if checkpoints is not None:
+        _check(checkpoints, "checkpoints", (B, D, lib.mamba_gated_scan_checkpoints(L)),
+               torch.float32, dev)
+    g = {"dx": torch.empty_like(x), "dr": torch.empty_like(x), "di": torch.empty_like(x),
+         "dz": None if z is None else torch.empty_like(x), "dlam": torch.empty_like(lam),
+         "dr_bias": torch.empty_like(lam), "di_bias": torch.empty_like(lam),
+         "dh0": lam.new_empty((B, D))}
+    need = (lib.mamba_gated_scan_bwd_workspace_size(B, D, L, 0 if checkpoints is None else 1)
+            if workspace is None else 0)
+    workspace, workspace_bytes = _workspace(workspace, need, dev)
+    st = lib.mamba_gated_scan_bwd(
+        x.data_ptr(), r.data_ptr(), i.data_ptr(), lam.data_ptr(), _addr(r_bias), _addr(i_bias),
+        _addr(z), _addr(h0), _addr(reset), _addr(checkpoints), dout.data_ptr(), _addr(dh_last),
+        g["dx"].data_ptr(), g["dr"].data_ptr(), g["di"].data_ptr(), _addr(g["dz"]),
+        g["dlam"].data_ptr(), g["dr_bias"].data_ptr(), g["di_bias"].data_ptr(), g["dh0"].data_ptr(),
+        workspace.data_ptr(), workspace_bytes, B, D, L, c, _io_dtype(x), _raw_stream(x))
+    if st:
+        _raise(st, "mamba_gated_scan_bwd")
+    return g
+
+
+def gated_state_update(h, x, r, i, lam, r_bias=None, i_bias=None, z=None, c=8.0, h_out=None, out=None):
+    """One step of gated_scan_fwd (decode).  h [B,D] f32, updated in place, or left as it is with
+    the new state in h_out; x, r, i, z [B,D] f32/bf16.  Returns y [B,D] of x's dtype."""
+    torch = _torch()
+    lib = load_library()
+    B, D = x.shape
+    _check(h, "h", (B, D), torch.float32, x.device)
+    _gated_arguments(x, r, i, lam, r_bias, i_bias, z, None, None)
+    if h_out is None:
+        h_out = h
+    else:
+        _check(h_out, "h_out", (B, D), torch.float32, x.device)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _check(out, "out", x.shape, x.dtype, x.device)
+    st = lib.mamba_gated_state_update(h.data_ptr(), h_out.data_ptr(), x.data_ptr(), r.data_ptr(),
+                                      i.data_ptr(), lam.data_ptr(), _addr(r_bias), _addr(i_bias),
+                                      _addr(z), out.data_ptr(), B, D, c, _io_dtype(x), _raw_stream(x))
+    if st:
+        _raise(st, "mamba_gated_state_update")
+    return out
 
 
 def set_scan_timing_events_raw(start=None, stop=None):

@@ -1,0 +1,249 @@
+// The step of the gated linear recurrence and the scan of its steps over a wave,
+// shared by its forward and backward kernels.
+//
+//   v = c softplus(lam) sigmoid(r),  a = e^-v,  m = sqrt(1 - a^2)
+//   h <- a h + m sigmoid(i) x
+//
+// Two things are kept from losing their digits where a is next to 1 (long memories).
+// 1 - a^2 is e (2 - e) with the loss e = 1 - a from its series.  And spans of steps are
+// joined with the sum of their exponents, not the product of their a: a's rounding
+// there (6e-8) would add up over the steps of a sequence, as it is it adds up over a
+// lane's eight.
+#pragma once
+
+#include "device_common.h"
+
+namespace mamba {
+
+constexpr int kLaneSteps = 8;  // consecutive steps of a row that a lane takes
+
+typedef uint32_t gated_u32x4 __attribute__((ext_vector_type(4)));
+typedef float gated_f32x4 __attribute__((ext_vector_type(4)));
+
+// Eight consecutive elements of a row as they lie in memory.
+template <bool BF16> struct Eight;
+template <> struct Eight<true> {
+    gated_u32x4 v;
+    __device__ __forceinline__ void load(const uint16_t *p) { __builtin_memcpy(&v, p, 16); }
+    __device__ __forceinline__ float get(int j) const
+    {
+        return j & 1 ? __uint_as_float(v[j >> 1] & 0xffff0000u) : __uint_as_float(v[j >> 1] << 16);
+    }
+    __device__ __forceinline__ void fill(float f)
+    {
+        const uint32_t b = __float_as_uint(f) >> 16;  // 0 and -inf only: exact
+        v = gated_u32x4{b | b << 16, b | b << 16, b | b << 16, b | b << 16};
+    }
+    __device__ __forceinline__ void set_raw(int j, uint16_t bits)
+    {
+        const uint32_t w = v[j >> 1];
+        v[j >> 1] = j & 1 ? (w & 0xffffu) | (uint32_t)bits << 16 : (w & 0xffff0000u) | bits;
+    }
+    // Rounds eight values and stores the first n of them.
+    static __device__ __forceinline__ void store(uint16_t *p, const float (&f)[kLaneSteps], int n)
+    {
+        const gated_u32x4 w = {cvt2(f[0], f[1]), cvt2(f[2], f[3]), cvt2(f[4], f[5]), cvt2(f[6], f[7])};
+        if (n >= kLaneSteps) {
+            __builtin_memcpy(p, &w, 16);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kLaneSteps - 1; ++j)
+                if (j < n)
+                    p[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+        }
+    }
+};
+template <> struct Eight<false> {
+    gated_f32x4 v[2];
+    __device__ __forceinline__ void load(const float *p) { __builtin_memcpy(v, p, 32); }
+    __device__ __forceinline__ float get(int j) const { return v[j >> 2][j & 3]; }
+    __device__ __forceinline__ void fill(float f)
+    {
+        v[0] = gated_f32x4{f, f, f, f};
+        v[1] = v[0];
+    }
+    __device__ __forceinline__ void set_raw(int j, float f) { v[j >> 2][j & 3] = f; }
+    static __device__ __forceinline__ void store(float *p, const float (&f)[kLaneSteps], int n)
+    {
+        if (n >= kLaneSteps) {
+            __builtin_memcpy(p, f, 32);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kLaneSteps - 1; ++j)
+                if (j < n)
+                    p[j] = f[j];
+        }
+    }
+};
+
+// Of a lane's eight steps from t on, those before L.
+__device__ __forceinline__ int steps_left(int64_t L, int64_t t)
+{
+    const int64_t left = L - t;
+    return left <= 0 ? 0 : (left < kLaneSteps ? (int)left : kLaneSteps);
+}
+
+// The first n (at most 8) elements from p on; the others are `rest`.
+template <bool BF16>
+__device__ __forceinline__ void load_some(Eight<BF16> &to, const typename Elem<BF16>::T *p, int n, float rest)
+{
+    if (n >= kLaneSteps) {
+        to.load(p);
+    } else {
+        to.fill(rest);
+#pragma unroll
+        for (int j = 0; j < kLaneSteps - 1; ++j)
+            if (j < n)
+                to.set_raw(j, p[j]);
+    }
+}
+
+// Bit j: step j of the lane's starts a sequence.
+__device__ __forceinline__ uint32_t load_resets(const uint8_t *p, int n)
+{
+    uint32_t bits = 0;
+    if (n >= kLaneSteps) {
+        uint32_t w[2];
+        __builtin_memcpy(w, p, 8);
+#pragma unroll
+        for (int j = 0; j < kLaneSteps; ++j)
+            bits |= ((w[j >> 2] >> (8 * (j & 3))) & 0xffu) != 0 ? 1u << j : 0u;
+    } else {
+#pragma unroll
+        for (int j = 0; j < kLaneSteps - 1; ++j)
+            if (j < n)
+                bits |= p[j] != 0 ? 1u << j : 0u;
+    }
+    return bits;
+}
+
+// 1 / (1 + 2^-(x log2 e + bias)), bias in the same units; 0 at -infinity, 1 at infinity.
+__device__ __forceinline__ float sigmoid_log2(float x, float bias2)
+{
+    return hw_rcp(1.f + hw_exp2(fmaf(x, -kLog2e, -bias2)));
+}
+
+// ln(1 + e^x), once a row and accurately: it scales every v of the row.
+__device__ __forceinline__ float softplus_row(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
+
+// 1 - 2^-u for u >= 0, given a = 2^-u.  Below 1/8 from the series of 1 - e^-v, v = u ln 2, whose
+// truncation stays below 2e-8 relative there; above, the subtraction loses at most
+// three bits of e.
+__device__ __forceinline__ float loss_of(float u, float a)
+{
+    constexpr float l = kLn2, l2 = l * l, l3 = l2 * l, l4 = l3 * l, l5 = l4 * l;
+    float p = l5 / 120.f;
+    p = fmaf(p, u, -l4 / 24.f);
+    p = fmaf(p, u, l3 / 6.f);
+    p = fmaf(p, u, -l2 / 2.f);
+    p = fmaf(p, u, l);
+    return u < 0.125f ? u * p : 1.f - a;
+}
+
+// The value of the lane that the DPP control names, 0 where there is none or the row
+// of 16 is not in ROWS.
+template <int CTRL, int ROWS = 0xf> __device__ __forceinline__ float lane_of(float v)
+{
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xf, false));
+}
+constexpr int kRowShr = 0x110, kRowShl = 0x100, kWaveShr1 = 0x138, kWaveShl1 = 0x130, kBcast15 = 0x142,
+              kBcast31 = 0x143;
+
+__device__ __forceinline__ float read_lane(float v, int lane)
+{
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+
+// A span's map s -> 2^-U s + S.  `after`: this one behind another.  With DROPS a map
+// of U = infinity (a reset) drops even a NaN or an infinity of what lies before it.
+template <bool DROPS> struct Span {
+    float U, S;
+    __device__ __forceinline__ float of(float s) const
+    {
+        const float v = fmaf(hw_exp2(-U), s, S);
+        return DROPS && U == __builtin_inff() ? S : v;
+    }
+    __device__ __forceinline__ void after(const Span &before)
+    {
+        S = of(before.S);
+        U = DROPS && U == __builtin_inff() ? U : U + before.U;
+    }
+};
+
+template <int CTRL, int ROWS = 0xf, bool DROPS>
+__device__ __forceinline__ Span<DROPS> span_of_lane(const Span<DROPS> &m)
+{
+    return {lane_of<CTRL, ROWS>(m.U), lane_of<CTRL, ROWS>(m.S)};
+}
+template <bool DROPS> __device__ __forceinline__ Span<DROPS> read_span(const Span<DROPS> &m, int lane)
+{
+    return {read_lane(m.U, lane), read_lane(m.S, lane)};
+}
+
+// Joins to each lane's span those of the lanes before it (of its group of G lanes);
+// returns the join without the lane's own.
+template <int G, bool DROPS> __device__ __forceinline__ Span<DROPS> join_before(Span<DROPS> &m)
+{
+    const Span<DROPS> none{0.f, 0.f};
+    const int in = threadIdx.x & (G - 1);
+    if constexpr (G >= 16) {
+        m.after(span_of_lane<kRowShr + 1>(m));
+        m.after(span_of_lane<kRowShr + 2>(m));
+        m.after(span_of_lane<kRowShr + 4>(m));
+        m.after(span_of_lane<kRowShr + 8>(m));
+        if constexpr (G >= 32)
+            m.after(span_of_lane<kBcast15, 0xa>(m));
+        if constexpr (G == 64)
+            m.after(span_of_lane<kBcast31, 0xc>(m));
+    } else {
+        static_assert(G == 4, "groups of 4, 16, 32 or 64 lanes");
+        const Span<DROPS> p = span_of_lane<kRowShr + 1>(m);
+        m.after(in >= 1 ? p : none);
+        const Span<DROPS> q = span_of_lane<kRowShr + 2>(m);
+        m.after(in >= 2 ? q : none);
+    }
+    const Span<DROPS> e = span_of_lane<kWaveShr1>(m);
+    return G == 64 || in > 0 ? e : none;
+}
+
+// The same from the other end: the spans of the lanes behind each lane.
+template <int G, bool DROPS> __device__ __forceinline__ Span<DROPS> join_behind(Span<DROPS> &m)
+{
+    const Span<DROPS> none{0.f, 0.f};
+    const int lane = threadIdx.x & 63, in = lane & (G - 1);
+    if constexpr (G >= 16) {
+        m.after(span_of_lane<kRowShl + 1>(m));
+        m.after(span_of_lane<kRowShl + 2>(m));
+        m.after(span_of_lane<kRowShl + 4>(m));
+        m.after(span_of_lane<kRowShl + 8>(m));
+        if constexpr (G >= 32) {  // rows of 16: their spans are in their first lanes
+            const Span<DROPS> r1 = read_span(m, 16), r3 = read_span(m, 48);
+            const int row = lane >> 4;
+            if constexpr (G == 64) {
+                Span<DROPS> r23 = read_span(m, 32);
+                r23.after(r3);
+                Span<DROPS> r123 = r1;
+                r123.after(r23);
+                m.after(row == 0 ? r123 : (row == 1 ? r23 : (row == 2 ? r3 : none)));
+            } else {
+                m.after(row == 0 ? r1 : (row == 2 ? r3 : none));
+            }
+        }
+    } else {
+        static_assert(G == 4, "groups of 4, 16, 32 or 64 lanes");
+        const Span<DROPS> p = span_of_lane<kRowShl + 1>(m);
+        m.after(in <= 2 ? p : none);
+        const Span<DROPS> q = span_of_lane<kRowShl + 2>(m);
+        m.after(in <= 1 ? q : none);
+    }
+    const Span<DROPS> e = span_of_lane<kWaveShl1>(m);
+    return G == 64 || in < G - 1 ? e : none;
+}
+
+// Lanes a row of L steps takes, and how many waves share a row of more than a chunk.
+inline int gated_group(int64_t L)
+{
+    return L <= 4 * kLaneSteps ? 4 : (L <= 16 * kLaneSteps ? 16 : (L <= 32 * kLaneSteps ? 32 : 64));
+}
+
+}  // namespace mamba

@@ -1,0 +1,269 @@
+// Gated linear recurrence, backward.  With g_t the gradient that reaches h_t,
+//   g_t  = dout_t SiLU(z_t) + a_(t+1) g_(t+1)          (dh_last behind the last step)
+//   dx_t = g m s,   di_t = g m x s (1 - s),   s = sigmoid(i)
+//   dv_t = -a (g h_(t-1)) + (a^2 / m) g s x            (0 at a reset)
+//   dr_t = dv v (1 - sigmoid(r)),   dlam = sum dv v sigmoid(lam) / softplus(lam)
+//   dz_t = dout h SiLU'(z),   dh0 = a_0 g_0
+// (m = sqrt(1 - a^2), dm/dv = a^2 / m; v / m -> 0 with v, so dv is taken with its v.)
+// Rows go by as in the forward kernel, from the last chunk to the first.  The states
+// come from the forward call's checkpoints, one a chunk, and the steps after it run
+// again; so a chunk needs nothing from its neighbours but the gradient that enters it
+// from behind, a_(t+1) g_(t+1), and the inputs are read once.
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "gated_common.h"
+#include "gated_scan.h"
+
+namespace mamba {
+namespace {
+
+template <int G, int WAVES, bool BF16, bool GATE, bool RESET>
+__global__ __launch_bounds__(256) void gated_bwd_kernel(const GatedScanBwdArgs p)
+{
+    using T = typename Elem<BF16>::T;
+    using M = Span<RESET>;
+    constexpr int kRows = 256 / G / WAVES;  // of a workgroup
+    constexpr int kSpan = G * kLaneSteps * WAVES;
+    __shared__ float2 maps[2][WAVES];
+    __shared__ float sums[3][WAVES];
+    const int lane = threadIdx.x & (G - 1), wave = threadIdx.x / G % WAVES;
+    const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / (G * WAVES);
+    const int64_t rows = p.f.B * p.f.D;
+    const bool live = row < rows;
+    const int64_t at = live ? row : 0, d = at % p.f.D, L = live ? p.f.L : 0, first_of = at * p.f.L;
+    const T *x = (const T *)p.f.x + first_of, *r = (const T *)p.f.r + first_of, *i = (const T *)p.f.i + first_of;
+    const T *z = GATE ? (const T *)p.f.z + first_of : nullptr, *dout = (const T *)p.dout + first_of;
+    T *dx = (T *)p.dx + first_of, *dr = (T *)p.dr + first_of, *di = (T *)p.di + first_of;
+    T *dz = GATE ? (T *)p.dz + first_of : nullptr;
+    const uint8_t *reset = RESET ? p.f.reset + at / p.f.D * p.f.L : nullptr;
+    const float rate = p.f.c * softplus_row(p.f.lam[d]) * kLog2e;
+    const float rb = p.f.r_bias ? p.f.r_bias[d] * kLog2e : 0.f, ib = p.f.i_bias ? p.f.i_bias[d] * kLog2e : 0.f;
+    const int64_t chunks = (p.f.L + kGatedChunk - 1) / kGatedChunk;
+    float carry = p.dh_last ? p.dh_last[at] : 0.f;  // a g of the step behind
+    float sum_q = 0.f, sum_r = 0.f, sum_i = 0.f;
+
+    Eight<BF16> nx, nr, ni, nz, nd;
+    uint32_t nreset = 0;
+    float nstate = 0.f;
+    auto fetch = [&](int64_t t) {
+        const int n = steps_left(L, t);
+        load_some<BF16>(nr, r + t, n, -__builtin_inff());  // past the end: steps that change nothing
+        load_some<BF16>(nx, x + t, n, 0.f);
+        load_some<BF16>(ni, i + t, n, 0.f);
+        load_some<BF16>(nd, dout + t, n, 0.f);
+        if constexpr (GATE)
+            load_some<BF16>(nz, z + t, n, 0.f);
+        if constexpr (RESET)
+            nreset = load_resets(reset + t, n);
+        const int64_t chunk = t / kGatedChunk;
+        nstate = p.f.checkpoints[at * chunks + (chunk < chunks ? chunk : chunks - 1)];
+    };
+    int64_t base = p.f.L > 0 ? (p.f.L - 1) / kSpan * kSpan : -1;
+    const int64_t mine = ((int64_t)wave * G + lane) * kLaneSteps;
+    if (base >= 0)
+        fetch(base + mine);
+    int turn = 0;
+    for (; base >= 0; base -= kSpan) {
+        const int64_t t = base + mine;
+        const Eight<BF16> cx = nx, cr = nr, ci = ni, cz = nz, cd = nd;
+        const uint32_t first = nreset;
+        const float state = nstate;
+        if (base > 0)
+            fetch(t - kSpan);
+        float a[kLaneSteps], u[kLaneSteps], keep_r[kLaneSteps], gate[kLaneSteps], m2[kLaneSteps], rm[kLaneSteps];
+        float sum = 0.f, h = 0.f;
+        bool dropped = false;
+#pragma unroll
+        for (int j = 0; j < kLaneSteps; ++j) {
+            const float s = sigmoid_log2(cr.get(j), rb);
+            keep_r[j] = 1.f - s;
+            u[j] = rate * s;
+            gate[j] = sigmoid_log2(ci.get(j), ib);
+            a[j] = hw_exp2(-u[j]);
+            const float e = loss_of(u[j], a[j]);
+            m2[j] = e * (2.f - e);
+            // 1 / m; a step that loses nothing (m = 0) has v = 0, which the floor keeps from 0 / 0
+            rm[j] = __builtin_amdgcn_rsqf(fmaxf(m2[j], 1e-37f));
+            const float in = gate[j] * cx.get(j);
+            sum += u[j];
+            h = fmaf(a[j], h, m2[j] * rm[j] * in);
+            if (RESET && (first >> j & 1)) {
+                h = in;
+                dropped = true;
+            }
+        }
+        if (RESET && dropped)
+            sum = __builtin_inff();
+        M m{sum, h};
+        h = join_before<G, RESET>(m).of(state);
+        // h before each step; the output's gradient, through the gate
+        float before[kLaneSteps], grad[kLaneSteps], dgate[kLaneSteps];
+#pragma unroll
+        for (int j = 0; j < kLaneSteps; ++j) {
+            before[j] = h;
+            const float in = gate[j] * cx.get(j);
+            h = fmaf(a[j], h, m2[j] * rm[j] * in);
+            if (RESET && (first >> j & 1))
+                h = in;
+            grad[j] = cd.get(j);
+            if constexpr (GATE) {
+                const float zj = cz.get(j), sz = sigmoid_log2(zj, 0.f);
+                dgate[j] = grad[j] * h * sz * fmaf(zj, 1.f - sz, 1.f);
+                grad[j] *= zj * sz;
+            }
+        }
+        float behind = 0.f;
+#pragma unroll
+        for (int j = kLaneSteps - 1; j >= 0; --j) {
+            const float g = grad[j] + behind;
+            behind = a[j] * g;
+            if (RESET && (first >> j & 1))
+                behind = 0.f;
+        }
+        M back{sum, behind};
+        const M from = join_behind<G, RESET>(back);
+        float enter = carry;
+        if constexpr (WAVES > 1) {
+            if (lane == 0)
+                maps[turn][wave] = float2{back.U, back.S};
+            __syncthreads();
+#pragma unroll
+            for (int w = WAVES - 1; w >= 0; --w) {
+                const M other{maps[turn][w].x, maps[turn][w].y};
+                carry = other.of(carry);
+                if (w - 1 == wave)
+                    enter = carry;
+            }
+            turn ^= 1;
+        } else if constexpr (G == 64) {
+            carry = read_span(back, 0).of(carry);
+        }
+        behind = from.of(enter);
+        float ox[kLaneSteps], orr[kLaneSteps], oi[kLaneSteps];
+#pragma unroll
+        for (int j = kLaneSteps - 1; j >= 0; --j) {
+            const float g = grad[j] + behind;
+            behind = a[j] * g;
+            float m1 = m2[j] * rm[j];
+            const float in = gate[j] * cx.get(j);
+            float q = g * (u[j] * kLn2) * a[j] * fmaf(a[j] * rm[j], in, -before[j]);
+            if (RESET && (first >> j & 1)) {
+                behind = q = 0.f;
+                m1 = 1.f;
+            }
+            ox[j] = g * m1 * gate[j];
+            oi[j] = g * m1 * in * (1.f - gate[j]);
+            orr[j] = q * keep_r[j];
+            sum_q += q;
+            sum_r += orr[j];
+            sum_i += oi[j];
+        }
+        const int n = steps_left(L, t);
+        Eight<BF16>::store(dx + t, ox, n);
+        Eight<BF16>::store(dr + t, orr, n);
+        Eight<BF16>::store(di + t, oi, n);
+        if constexpr (GATE)
+            Eight<BF16>::store(dz + t, dgate, n);
+        if (live && t == 0)
+            p.dh0[row] = behind;
+    }
+    if (p.f.L == 0 && live && lane == 0 && wave == 0)
+        p.dh0[row] = carry;
+    // a row's sums: over its lanes, then its waves
+#pragma unroll
+    for (int s = G / 2; s > 0; s >>= 1) {
+        sum_q += __shfl_xor(sum_q, s);
+        sum_r += __shfl_xor(sum_r, s);
+        sum_i += __shfl_xor(sum_i, s);
+    }
+    if constexpr (WAVES > 1) {
+        if (lane == 0) {
+            sums[0][wave] = sum_q;
+            sums[1][wave] = sum_r;
+            sums[2][wave] = sum_i;
+        }
+        __syncthreads();
+        sum_q = sums[0][0];
+        sum_r = sums[1][0];
+        sum_i = sums[2][0];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) {
+            sum_q += sums[0][w];
+            sum_r += sums[1][w];
+            sum_i += sums[2][w];
+        }
+    }
+    if (live && lane == 0 && wave == 0) {
+        p.partials[row] = sum_q;
+        p.partials[rows + row] = sum_r;
+        p.partials[2 * rows + row] = sum_i;
+    }
+}
+
+// Sums over the batch, in its order.
+__global__ __launch_bounds__(256) void gated_sums_kernel(const GatedScanBwdArgs p)
+{
+    const int64_t d = (int64_t)blockIdx.x * 256 + threadIdx.x, rows = p.f.B * p.f.D;
+    if (d >= p.f.D)
+        return;
+    float q = 0.f, r = 0.f, i = 0.f;
+    for (int64_t at = d; at < rows; at += p.f.D) {
+        q += p.partials[at];
+        r += p.partials[rows + at];
+        i += p.partials[2 * rows + at];
+    }
+    // sigmoid(lam) / softplus(lam), which goes to 1 where both go to 0
+    const float lam = p.f.lam[d], t = expf(-fabsf(lam)), s = (lam < 0.f ? t : 1.f) / (1.f + t);
+    p.dlam[d] = lam < -80.f ? q : q * (s / softplus_row(lam));
+    p.dr_bias[d] = r;
+    p.di_bias[d] = i;
+}
+
+template <int G, int WAVES> hipError_t launch(const GatedScanBwdArgs &a, hipStream_t s)
+{
+    constexpr int kRows = 256 / G / WAVES;
+    const dim3 grid((unsigned)((a.f.B * a.f.D + kRows - 1) / kRows)), block(256);
+    auto with = [&](auto bf16, auto gate, auto reset) {
+        gated_bwd_kernel<G, WAVES, bf16, gate, reset><<<grid, block, 0, s>>>(a);
+    };
+    auto on_reset = [&](auto bf16, auto gate) {
+        if (a.f.reset)
+            with(bf16, gate, std::true_type{});
+        else
+            with(bf16, gate, std::false_type{});
+    };
+    auto on_gate = [&](auto bf16) {
+        if (a.f.z)
+            on_reset(bf16, std::true_type{});
+        else
+            on_reset(bf16, std::false_type{});
+    };
+    if (a.f.bf16)
+        on_gate(std::true_type{});
+    else
+        on_gate(std::false_type{});
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_gated_scan_bwd(const GatedScanBwdArgs &a, hipStream_t s)
+{
+    hipError_t e = hipSuccess;
+    if (a.f.B > 0) {
+        switch (gated_group(a.f.L)) {
+        case 4: e = launch<4, 1>(a, s); break;
+        case 16: e = launch<16, 1>(a, s); break;
+        case 32: e = launch<32, 1>(a, s); break;
+        default: e = a.f.L > kGatedChunk && a.f.B * a.f.D < 4096 ? launch<64, 4>(a, s) : launch<64, 1>(a, s);
+        }
+    }
+    if (e != hipSuccess)
+        return e;
+    gated_sums_kernel<<<dim3((unsigned)((a.f.D + 255) / 256)), dim3(256), 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace mamba

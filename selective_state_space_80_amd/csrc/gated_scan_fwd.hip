@@ -1,0 +1,186 @@
+// Gated linear recurrence, forward: one pass over the inputs (gated_common.h has the
+// step).  A lane takes 8 consecutive steps of a row, so its loads and stores are 16
+// bytes (bf16) and a wave's are contiguous; G lanes share a row, 64 of them going on
+// from chunk to chunk of 512 steps.  Each lane joins its steps to one affine map, the
+// wave joins its lanes' maps by DPP, and every lane then runs its steps again from the
+// state that enters them.  WAVES waves of a workgroup take consecutive chunks of one
+// row, where rows are few.
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "gated_common.h"
+#include "gated_scan.h"
+
+namespace mamba {
+namespace {
+
+template <int G, int WAVES, bool BF16, bool GATE, bool RESET>
+__global__ __launch_bounds__(256) void gated_fwd_kernel(const GatedScanArgs p)
+{
+    using T = typename Elem<BF16>::T;
+    using M = Span<RESET>;
+    constexpr int kRows = 256 / G / WAVES;  // of a workgroup
+    constexpr int kSpan = G * kLaneSteps * WAVES;
+    __shared__ float2 maps[2][WAVES];
+    const int lane = threadIdx.x & (G - 1), wave = threadIdx.x / G % WAVES;
+    const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / (G * WAVES);
+    const bool live = row < p.B * p.D;  // the others' lanes run along, with nothing to load or store
+    const int64_t at = live ? row : 0, d = at % p.D, L = live ? p.L : 0;
+    const T *x = (const T *)p.x + at * p.L, *r = (const T *)p.r + at * p.L, *i = (const T *)p.i + at * p.L;
+    const T *z = GATE ? (const T *)p.z + at * p.L : nullptr;
+    T *y = (T *)p.y + at * p.L;
+    const uint8_t *reset = RESET ? p.reset + at / p.D * p.L : nullptr;
+    const float rate = p.c * softplus_row(p.lam[d]) * kLog2e;  // of the exponents of 2
+    const float rb = p.r_bias ? p.r_bias[d] * kLog2e : 0.f, ib = p.i_bias ? p.i_bias[d] * kLog2e : 0.f;
+    const int64_t chunks = (p.L + kGatedChunk - 1) / kGatedChunk;
+    float carry = p.h0 ? p.h0[at] : 0.f;
+
+    Eight<BF16> nx, nr, ni, nz;
+    uint32_t nreset = 0;
+    auto fetch = [&](int64_t t) {
+        const int n = steps_left(L, t);
+        load_some<BF16>(nr, r + t, n, -__builtin_inff());  // past the end: steps that change nothing
+        load_some<BF16>(nx, x + t, n, 0.f);
+        load_some<BF16>(ni, i + t, n, 0.f);
+        if constexpr (GATE)
+            load_some<BF16>(nz, z + t, n, 0.f);
+        if constexpr (RESET)
+            nreset = load_resets(reset + t, n);
+    };
+    int64_t t = ((int64_t)wave * G + lane) * kLaneSteps;
+    fetch(t);
+    int turn = 0;
+    for (int64_t base = 0; base < p.L; base += kSpan, t += kSpan) {
+        const Eight<BF16> cx = nx, cr = nr, ci = ni, cz = nz;
+        const uint32_t first = nreset;
+        if (base + kSpan < p.L)
+            fetch(t + kSpan);
+        float a[kLaneSteps], b[kLaneSteps], sum = 0.f, h = 0.f;
+        bool dropped = false;
+#pragma unroll
+        for (int j = 0; j < kLaneSteps; ++j) {
+            const float u = rate * sigmoid_log2(cr.get(j), rb);
+            const float in = sigmoid_log2(ci.get(j), ib) * cx.get(j);
+            a[j] = hw_exp2(-u);
+            const float e = loss_of(u, a[j]);
+            b[j] = __builtin_amdgcn_sqrtf(e * (2.f - e)) * in;
+            sum += u;
+            h = fmaf(a[j], h, b[j]);
+            if (RESET && (first >> j & 1)) {
+                h = b[j] = in;
+                dropped = true;
+            }
+        }
+        M m{RESET && dropped ? __builtin_inff() : sum, h};
+        const M before = join_before<G, RESET>(m);
+        float enter = carry;
+        if constexpr (WAVES > 1) {
+            if (lane == G - 1)
+                maps[turn][wave] = float2{m.U, m.S};
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) {
+                const M other{maps[turn][w].x, maps[turn][w].y};
+                carry = other.of(carry);
+                if (w + 1 == wave)
+                    enter = carry;
+            }
+            turn ^= 1;
+        } else if constexpr (G == 64) {
+            carry = read_span(m, 63).of(carry);
+        }
+        if (p.checkpoints && lane == 0 && t < L)
+            p.checkpoints[at * chunks + t / kGatedChunk] = enter;
+        h = before.of(enter);
+        float out[kLaneSteps];
+#pragma unroll
+        for (int j = 0; j < kLaneSteps; ++j) {
+            h = fmaf(a[j], h, b[j]);
+            if (RESET && (first >> j & 1))
+                h = b[j];
+            out[j] = GATE ? h * silu_hw(cz.get(j)) : h;
+        }
+        if (p.y)
+            Eight<BF16>::store(y + t, out, steps_left(L, t));
+        // the steps past the end have left the state as it was
+        if (p.h_last && live && base + kSpan >= p.L && lane == G - 1 && wave == WAVES - 1)
+            p.h_last[row] = h;
+    }
+    if (p.L == 0 && p.h_last && live && lane == 0 && wave == 0)
+        p.h_last[row] = carry;
+}
+
+template <int G, int WAVES> hipError_t launch(const GatedScanArgs &a, hipStream_t s)
+{
+    constexpr int kRows = 256 / G / WAVES;
+    const dim3 grid((unsigned)((a.B * a.D + kRows - 1) / kRows)), block(256);
+    auto with = [&](auto bf16, auto gate, auto reset) {
+        gated_fwd_kernel<G, WAVES, bf16, gate, reset><<<grid, block, 0, s>>>(a);
+    };
+    auto on_reset = [&](auto bf16, auto gate) {
+        if (a.reset)
+            with(bf16, gate, std::true_type{});
+        else
+            with(bf16, gate, std::false_type{});
+    };
+    auto on_gate = [&](auto bf16) {
+        if (a.z)
+            on_reset(bf16, std::true_type{});
+        else
+            on_reset(bf16, std::false_type{});
+    };
+    if (a.bf16)
+        on_gate(std::true_type{});
+    else
+        on_gate(std::false_type{});
+    return hipGetLastError();
+}
+
+// ---- one step ----------------------------------------------------------------------------
+// A thread a state: the parameters of neighbouring channels are neighbours.  What bounds
+// it is the launch for a few sequences, the state's traffic (8 of 16 bytes in bf16) for many.
+template <bool BF16, bool GATE> __global__ __launch_bounds__(256) void gated_step_kernel(const GatedStepArgs p)
+{
+    using T = typename Elem<BF16>::T;
+    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (n >= p.B * p.D)
+        return;
+    const int64_t d = n % p.D;
+    const float rb = p.r_bias ? p.r_bias[d] * kLog2e : 0.f, ib = p.i_bias ? p.i_bias[d] * kLog2e : 0.f;
+    const float u = p.c * softplus_row(p.lam[d]) * kLog2e * sigmoid_log2(Elem<BF16>::load((const T *)p.r + n), rb);
+    const float a = hw_exp2(-u), e = loss_of(u, a), in = sigmoid_log2(Elem<BF16>::load((const T *)p.i + n), ib) *
+                                     Elem<BF16>::load((const T *)p.x + n);
+    float h = p.h[n];
+    h = fmaf(a, h, __builtin_amdgcn_sqrtf(e * (2.f - e)) * in);
+    p.h_out[n] = h;
+    Elem<BF16>::store((T *)p.y + n, GATE ? h * silu_hw(Elem<BF16>::load((const T *)p.z + n)) : h);
+}
+
+}  // namespace
+
+hipError_t launch_gated_scan_fwd(const GatedScanArgs &a, hipStream_t s)
+{
+    switch (gated_group(a.L)) {
+    case 4: return launch<4, 1>(a, s);
+    case 16: return launch<16, 1>(a, s);
+    case 32: return launch<32, 1>(a, s);
+    default: return a.L > kGatedChunk && a.B * a.D < 4096 ? launch<64, 4>(a, s) : launch<64, 1>(a, s);
+    }
+}
+
+hipError_t launch_gated_step(const GatedStepArgs &a, hipStream_t s)
+{
+    const dim3 grid((unsigned)((a.B * a.D + 255) / 256)), block(256);
+    if (a.bf16 && a.z)
+        gated_step_kernel<true, true><<<grid, block, 0, s>>>(a);
+    else if (a.bf16)
+        gated_step_kernel<true, false><<<grid, block, 0, s>>>(a);
+    else if (a.z)
+        gated_step_kernel<false, true><<<grid, block, 0, s>>>(a);
+    else
+        gated_step_kernel<false, false><<<grid, block, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace mamba
