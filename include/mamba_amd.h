@@ -12,7 +12,8 @@
  *   mamba_conv1d_selective_state_update  that conv step and the decode step fused
  * the scan's backward pass (mamba_selective_scan_bwd), the Mamba-2 form of
  * the scan on the matrix cores (mamba_ssd_scan_fwd), a gated linear recurrence
- * (mamba_gated_scan_fwd, its gradient and its single step),
+ * (mamba_gated_scan_fwd, its gradient and its single step), the norm and the
+ * 8-bit and microscaled 4-bit projections around the scans,
  * plus workspace sizing and status helpers.
  *
  * Conventions shared by every entry point
@@ -534,6 +535,52 @@ mamba_status mamba_gated_scan_bwd(const void *x, const void *r, const void *i, c
 mamba_status mamba_gated_state_update(const float *h, float *h_out, const void *x, const void *r, const void *i,
                                       const float *lam, const float *r_bias, const float *i_bias, const void *z,
                                       void *y, int64_t B, int64_t D, float c, mamba_dtype io, void *stream);
+
+/*
+ * Microscaled 4-bit floating point (the OCP MX format MXFP4): along the inner axis
+ * each block of 32 elements shares a power of two, the elements are E2M1, of the
+ * values 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign (bit 3).
+ *   q     : [rows, G * 128] bytes, G = ceil(K / 256): two elements a byte, the first
+ *           in the low half; zeros from K on.  16-byte aligned.
+ *   scale : [G, rows, 8] bytes, by groups of 256 elements: the exponent + 127 of each
+ *           block of 32 (255: NaN).  8-byte aligned.
+ * Quantisation: exponent = floor(log2 max|x|) - 2 (at least -127, also for zero
+ * blocks), elements x / 2^exponent to nearest, ties to even, clipped to 6.  A block
+ * with a NaN or an infinity has scale NaN and zeros, so that everything computed
+ * from it is NaN.
+ *   channel_major 0 : x [B, L, K] of `io`
+ *   channel_major 1 : x [B, K, L] of `io`, as the scans write their output
+ * rows = B * L in both.  K at most 2^23; ceil(rows / 8) * G < 2^23, channel-major
+ * B * ceil(L / 64) * G too.
+ */
+mamba_status mamba_quantize_mxfp4(const void *x, uint8_t *q, uint8_t *scale, int64_t B, int64_t L, int64_t K,
+                                  int channel_major, mamba_dtype io, void *stream);
+
+/*
+ * The values that such rows stand for: out [rows, K] of `io`, exact in both types
+ * but where a product with the scale leaves their range.  Limits as above.
+ */
+mamba_status mamba_dequantize_mxfp4(const uint8_t *q, const uint8_t *scale, void *out, int64_t rows, int64_t K,
+                                    mamba_dtype io, void *stream);
+
+/* Flags of mamba_mxfp4_matmul: the operand is one matrix, used by every batch. */
+#define MAMBA_MXFP4_SHARED_A 1u
+#define MAMBA_MXFP4_SHARED_B 2u
+
+/*
+ * Product of two such operands:
+ *   out[i, m, n] = sum_k A[i, m, k] * B[i, n, k]      (of the values they stand for)
+ * summed in fp32 and rounded once.  As in mamba_int8_matmul a projection takes tokens
+ * and weight rows as they are, either on the left.
+ *   a, a_scale : rows batch * M ([G, batch, M, 8] scales); with MAMBA_MXFP4_SHARED_A M
+ *   b, b_scale : rows batch * N; with MAMBA_MXFP4_SHARED_B N
+ *   out        : [batch, M, N] of `out_type`
+ * K from 0 (zeros) to 2^23: what lies in the rows' last group from K on is multiplied
+ * too, so it has to be zeros.  Needs no workspace.
+ */
+mamba_status mamba_mxfp4_matmul(const uint8_t *a, const uint8_t *b, const uint8_t *a_scale, const uint8_t *b_scale,
+                                void *out, int64_t batch, int64_t M, int64_t N, int64_t K, mamba_dtype out_type,
+                                unsigned flags, void *stream);
 
 /*
  * Profiling hook.  When both are non-NULL hipEvent_t handles (passed as

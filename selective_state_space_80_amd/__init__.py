@@ -33,6 +33,9 @@ Entry points (same names as the C ABI, without the ``mamba_`` prefix):
                  dh_last=None, c=8.0, checkpoints=None, workspace=None)
   gated_scan_bwd_workspace_size(B, D, L, with_checkpoints=True)
   gated_state_update(h, x, r, i, lam, r_bias=None, i_bias=None, z=None, c=8.0, h_out=None, out=None)
+  quantize_mxfp4(x, channel_major=False, out=None, scale=None)
+  dequantize_mxfp4(q, scale, K=None, dtype=torch.bfloat16, out=None)
+  mxfp4_matmul(a, b, a_scale, b_scale, out_dtype=torch.bfloat16, out=None)
   selective_scan_check(workspace)        the carry's error word (after a sync)
   set_scan_spin_limit(polls)             diagnostic bound of the carry waits
 Test helper: set_carry_checks(True) checks the carry after every scan call.
@@ -70,7 +73,8 @@ EXPORTED = ["mamba_status_string", "mamba_abi_version", "mamba_conv1d_silu",
             "mamba_int8_matmul", "mamba_int8_matmul_form",
             "mamba_gated_scan_checkpoints", "mamba_gated_scan_fwd",
             "mamba_gated_scan_bwd_workspace_size", "mamba_gated_scan_bwd",
-            "mamba_gated_state_update"]
+            "mamba_gated_state_update", "mamba_quantize_mxfp4", "mamba_dequantize_mxfp4",
+            "mamba_mxfp4_matmul"]
 
 _lib = None
 
@@ -161,6 +165,12 @@ def load_library(path: str = LIBRARY):
     lib.mamba_gated_scan_bwd.argtypes = [P] * 21 + [SZ, I64, I64, I64, F, I32, P]
     lib.mamba_gated_state_update.restype = I32
     lib.mamba_gated_state_update.argtypes = [P] * 10 + [I64, I64, F, I32, P]
+    lib.mamba_quantize_mxfp4.restype = I32
+    lib.mamba_quantize_mxfp4.argtypes = [P] * 3 + [I64, I64, I64, I32, I32, P]
+    lib.mamba_dequantize_mxfp4.restype = I32
+    lib.mamba_dequantize_mxfp4.argtypes = [P] * 3 + [I64, I64, I32, P]
+    lib.mamba_mxfp4_matmul.restype = I32
+    lib.mamba_mxfp4_matmul.argtypes = [P] * 5 + [I64, I64, I64, I64, I32, U32, P]
     _lib = lib
     return lib
 
@@ -968,6 +978,123 @@ def gated_state_update(h, x, r, i, lam, r_bias=None, i_bias=None, z=None, c=8.0,
                                       _addr(z), out.data_ptr(), B, D, c, _io_dtype(x), _raw_stream(x))
     if st:
         _raise(st, "mamba_gated_state_update")
+    return out
+
+
+MXFP4_GROUP = 256  # elements a packed row is filled up to a multiple of: 128 bytes, 8 scales
+MXFP4_SHARED_A = 1  # MAMBA_MXFP4_SHARED_A
+MXFP4_SHARED_B = 2  # MAMBA_MXFP4_SHARED_B
+
+
+def quantize_mxfp4(x, channel_major=False, out=None, scale=None):
+    """Microscaled 4-bit floating point: along the last axis a power of two for every 32
+    elements, the elements rounded to 0, .5, 1, 1.5, 2, 3, 4, 6 and a sign.  x [..., K] f32/bf16
+    -> q [..., G * 128] uint8 (two elements a byte, zeros from K on) and scale [G, ..., 8] uint8
+    (exponent + 127), G = ceil(K / 256).  channel_major: x is [B, K, L], as the scans write
+    their output, and q [B, L, G * 128], scale [G, B, L, 8].  A block with a NaN or an infinity
+    has scale NaN."""
+    torch = _torch()
+    lib = load_library()
+    dev, shape = x.device, x.shape
+    if not x.is_contiguous():
+        _check(x, "x", shape)
+    if channel_major:
+        if len(shape) != 3:
+            raise ValueError(f"channel-major x is [B, K, L], got {tuple(shape)}")
+        B, K, L = shape
+        lead = (B, L)
+    else:
+        if len(shape) < 1:
+            raise ValueError("x has no axis to quantise")
+        lead, K = shape[:-1], shape[-1]
+        B, L = 1, _rows(shape)
+    groups = -(-K // MXFP4_GROUP)
+    u8 = torch.uint8
+    if out is None:
+        out = x.new_empty((*lead, groups * 128), dtype=u8)
+    else:
+        _check(out, "out", (*lead, groups * 128), u8, dev)
+    if scale is None:
+        scale = x.new_empty((groups, *lead, 8), dtype=u8)
+    else:
+        _check(scale, "scale", (groups, *lead, 8), u8, dev)
+    st = lib.mamba_quantize_mxfp4(x.data_ptr(), out.data_ptr(), scale.data_ptr(), B, L, K,
+                                  1 if channel_major else 0, _io_dtype(x), _raw_stream(x))
+    if st:
+        _raise(st, "mamba_quantize_mxfp4")
+    return out, scale
+
+
+def _mxfp4_operand(q, scale, name, index):
+    """Checks a packed operand and its scales; returns its number of groups."""
+    torch = _torch()
+    shape, u8 = q.shape, torch.uint8
+    if not shape or shape[-1] % 128:
+        raise ValueError(f"{name} has rows of whole groups of 128 bytes, got {tuple(shape)}")
+    groups = shape[-1] // 128
+    if not (q.dtype is u8 and q.get_device() == index and q.is_contiguous()
+            and _is(scale, (groups, *shape[:-1], 8), u8, index)):
+        _check(q, name, shape, u8)
+        _check(scale, f"{name}_scale", (groups, *shape[:-1], 8), u8, q.device)
+        raise ValueError(f"{name} is on {q.device}, expected another device")
+    return groups
+
+
+def dequantize_mxfp4(q, scale, K=None, dtype=None, out=None):
+    """The values of quantize_mxfp4's rows: [..., K] of dtype (bfloat16, the default, or float32).
+    K: the row's elements, all of its groups' where it is not given."""
+    torch = _torch()
+    lib = load_library()
+    groups = _mxfp4_operand(q, scale, "q", q.get_device())
+    if K is None:
+        K = groups * MXFP4_GROUP
+    elif -(-K // MXFP4_GROUP) != groups:
+        raise ValueError(f"rows of {groups} groups do not have {K} elements")
+    shape = (*q.shape[:-1], K)
+    if out is None:
+        out = q.new_empty(shape, dtype=torch.bfloat16 if dtype is None else dtype)
+    else:
+        _check(out, "out", shape, dtype, q.device)
+    st = lib.mamba_dequantize_mxfp4(q.data_ptr(), scale.data_ptr(), out.data_ptr(), _rows(q.shape), K,
+                                    _io_dtype(out), _raw_stream(q))
+    if st:
+        _raise(st, "mamba_dequantize_mxfp4")
+    return out
+
+
+def mxfp4_matmul(a, b, a_scale, b_scale, out_dtype=None, out=None):
+    """out[..., m, n] = sum_k A[m, k] B[n, k] of the values that quantize_mxfp4's rows stand for,
+    summed in fp32.  a [M, G * 128] or [B, M, G * 128], b [N, G * 128] or [B, N, G * 128] uint8 (a
+    2-D operand is used by every batch of a 3-D one); scales [G, M, 8] or [G, B, M, 8] and alike.
+    Returns out [M, N] or [B, M, N] of out_dtype (bfloat16, the default, or float32).  With tokens
+    as `a` and a weight as `b` it is a projection; with the weight as `a`, its channel-major form."""
+    torch = _torch()
+    lib = load_library()
+    a_dim, b_dim = a.dim(), b.dim()
+    if a_dim not in (2, 3) or b_dim not in (2, 3):
+        raise ValueError(f"a and b are 2-D or 3-D, got {a_dim}-D and {b_dim}-D")
+    index = a.get_device()
+    groups = _mxfp4_operand(a, a_scale, "a", index)
+    if _mxfp4_operand(b, b_scale, "b", index) != groups:
+        raise ValueError(f"rows of a and b differ: {a.shape[-1]} and {b.shape[-1]} bytes")
+    M, N = a.shape[-2], b.shape[-2]
+    if a_dim == 2 and b_dim == 2:
+        batch, flags, out_shape = 1, 0, (M, N)
+    else:
+        batch = a.shape[0] if a_dim == 3 else b.shape[0]
+        if a_dim == b_dim and b.shape[0] != batch:
+            raise ValueError(f"a has {batch} batches, b {b.shape[0]}")
+        flags = (MXFP4_SHARED_A if a_dim == 2 else 0) | (MXFP4_SHARED_B if b_dim == 2 else 0)
+        out_shape = (batch, M, N)
+    if out is None:
+        out = a.new_empty(out_shape, dtype=torch.bfloat16 if out_dtype is None else out_dtype)
+    else:
+        _check(out, "out", out_shape, out_dtype, a.device)
+    st = lib.mamba_mxfp4_matmul(a.data_ptr(), b.data_ptr(), a_scale.data_ptr(), b_scale.data_ptr(),
+                                out.data_ptr(), batch, M, N, groups * MXFP4_GROUP, _io_dtype(out), flags,
+                                _raw_stream(a))
+    if st:
+        _raise(st, "mamba_mxfp4_matmul")
     return out
 
 

@@ -20,7 +20,8 @@ PROBE_SOURCE = "valu_probe.hip"
 PROBE_LIBRARY = os.path.join(HERE, "libmamba_probe.so")
 SOURCES = ["api.cpp", "scan_fwd.hip", "scan_bwd.hip", "ssd_fwd.hip", "conv1d_silu.hip", "state_update.hip",
            "quant_api.cpp", "rms_norm.hip", "rms_norm_bwd.hip", "quantize.hip", "int8_matmul.hip",
-           "gated_scan_api.cpp", "gated_scan_fwd.hip", "gated_scan_bwd.hip"]
+           "gated_scan_api.cpp", "gated_scan_fwd.hip", "gated_scan_bwd.hip",
+           "mxfp4_api.cpp", "mxfp4_quantize.hip", "mxfp4_matmul.hip"]
 ARCH = "gfx950"
 
 # Packed-fp32 VALU forms are disabled on purpose: the kernels are written for
