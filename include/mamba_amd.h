@@ -576,11 +576,20 @@ mamba_status mamba_dequantize_mxfp4(const uint8_t *q, const uint8_t *scale, void
  *   b, b_scale : rows batch * N; with MAMBA_MXFP4_SHARED_B N
  *   out        : [batch, M, N] of `out_type`
  * K from 0 (zeros) to 2^23: what lies in the rows' last group from K on is multiplied
- * too, so it has to be zeros.  Needs no workspace.
+ * too, so it has to be zeros.  Fewer than 2^30 tiles of 128 x 64 outputs a batch (with
+ * MAMBA_MXFP4_SHARED_B alone, of all batches' rows).  Needs no workspace.
  */
 mamba_status mamba_mxfp4_matmul(const uint8_t *a, const uint8_t *b, const uint8_t *a_scale, const uint8_t *b_scale,
                                 void *out, int64_t batch, int64_t M, int64_t N, int64_t K, mamba_dtype out_type,
                                 unsigned flags, void *stream);
+
+/*
+ * Diagnostic hook for tests: which kernel mamba_mxfp4_matmul takes for these sizes
+ * (form, tiles and slots as in mamba_int8_matmul_form; -1 for an empty product or one
+ * of no channels).  Needs no GPU.
+ */
+mamba_status mamba_mxfp4_matmul_form(int64_t batch, int64_t M, int64_t N, int64_t K, unsigned flags, int *form,
+                                     int64_t *tiles, int *slots);
 
 /*
  * Profiling hook.  When both are non-NULL hipEvent_t handles (passed as

@@ -36,6 +36,7 @@ Entry points (same names as the C ABI, without the ``mamba_`` prefix):
   quantize_mxfp4(x, channel_major=False, out=None, scale=None)
   dequantize_mxfp4(q, scale, K=None, dtype=torch.bfloat16, out=None)
   mxfp4_matmul(a, b, a_scale, b_scale, out_dtype=torch.bfloat16, out=None)
+  mxfp4_matmul_form(M, N, K, batch=1, flags=0)   diagnostic
   selective_scan_check(workspace)        the carry's error word (after a sync)
   set_scan_spin_limit(polls)             diagnostic bound of the carry waits
 Test helper: set_carry_checks(True) checks the carry after every scan call.
@@ -74,7 +75,7 @@ EXPORTED = ["mamba_status_string", "mamba_abi_version", "mamba_conv1d_silu",
             "mamba_gated_scan_checkpoints", "mamba_gated_scan_fwd",
             "mamba_gated_scan_bwd_workspace_size", "mamba_gated_scan_bwd",
             "mamba_gated_state_update", "mamba_quantize_mxfp4", "mamba_dequantize_mxfp4",
-            "mamba_mxfp4_matmul"]
+            "mamba_mxfp4_matmul", "mamba_mxfp4_matmul_form"]
 
 _lib = None
 
@@ -171,6 +172,8 @@ def load_library(path: str = LIBRARY):
     lib.mamba_dequantize_mxfp4.argtypes = [P] * 3 + [I64, I64, I32, P]
     lib.mamba_mxfp4_matmul.restype = I32
     lib.mamba_mxfp4_matmul.argtypes = [P] * 5 + [I64, I64, I64, I64, I32, U32, P]
+    lib.mamba_mxfp4_matmul_form.restype = I32
+    lib.mamba_mxfp4_matmul_form.argtypes = [I64] * 4 + [U32, P, P, P]
     _lib = lib
     return lib
 
@@ -1096,6 +1099,17 @@ def mxfp4_matmul(a, b, a_scale, b_scale, out_dtype=None, out=None):
     if st:
         _raise(st, "mamba_mxfp4_matmul")
     return out
+
+
+def mxfp4_matmul_form(M, N, K, batch=1, flags=0):
+    """Diagnostic: which kernel mxfp4_matmul takes for these sizes, as (form, tiles, slots) of
+    mamba_mxfp4_matmul_form.  Needs no GPU."""
+    form, tiles, slots = ctypes.c_int(), ctypes.c_int64(), ctypes.c_int()
+    st = load_library().mamba_mxfp4_matmul_form(batch, M, N, K, flags, ctypes.byref(form), ctypes.byref(tiles),
+                                                ctypes.byref(slots))
+    if st:
+        _raise(st, "mamba_mxfp4_matmul_form")
+    return form.value, tiles.value, slots.value
 
 
 def set_scan_timing_events_raw(start=None, stop=None):

@@ -46,6 +46,15 @@ struct MxMatmulArgs {
     int64_t batch, M, N, groups;
     bool a_shared, b_shared, bf16;
 };
+// Which kernel a product takes.
+struct MxMatmulForm {
+    int form;           // number of the form
+    int slots;          // workgroups that run at once; rings: one a tile
+    int tile_m, tile_n; // outputs of a tile
+    int64_t batch, M;   // of one product, batches of one right operand joined
+    int64_t tiles;
+};
+MxMatmulForm mxfp4_matmul_form(const MxMatmulArgs &a);
 hipError_t launch_mxfp4_matmul(const MxMatmulArgs &a, hipStream_t s);
 
 }  // namespace mamba

@@ -31,6 +31,22 @@ mamba_status row_sizes(int64_t B, int64_t L, int64_t K)
 
 constexpr unsigned kFlags = MAMBA_MXFP4_SHARED_A | MAMBA_MXFP4_SHARED_B;
 
+mamba_status matmul_sizes(int64_t batch, int64_t M, int64_t N, int64_t K, unsigned flags)
+{
+    const bool a_shared = (flags & MAMBA_MXFP4_SHARED_A) != 0, b_shared = (flags & MAMBA_MXFP4_SHARED_B) != 0;
+    if (!sizes_ok(batch, M, N) || !sizes_ok(a_shared ? 1 : batch, M, K) || !sizes_ok(b_shared ? 1 : batch, N, K))
+        return MAMBA_ERR_SHAPE;
+    if (K > mamba::kMaxMxInner || (flags & ~kFlags) != 0)
+        return MAMBA_ERR_UNSUPPORTED;
+    const int64_t padded = mamba::mx_groups(K) * mamba::kMxGroup;
+    if (!sizes_ok(a_shared ? 1 : batch, M, padded) || !sizes_ok(b_shared ? 1 : batch, N, padded))
+        return MAMBA_ERR_SHAPE;
+    // The kernels number a batch's tiles, of 128 x 64 outputs at least where there
+    // are many, in 32 bits, twice a row of them included.
+    const int64_t rows = b_shared && !a_shared ? batch * M : M;  // batches of one right operand are one
+    return (rows + 127) / 128 * ((N + 63) / 64) < int64_t(1) << 30 ? MAMBA_OK : MAMBA_ERR_SHAPE;
+}
+
 }  // namespace
 
 extern "C" {
@@ -97,15 +113,10 @@ mamba_status mamba_mxfp4_matmul(const uint8_t *a, const uint8_t *b, const uint8_
 {
     if (!valid_dtype(out_type))
         return MAMBA_ERR_DTYPE;
+    const mamba_status sizes = matmul_sizes(batch, M, N, K, flags);
+    if (sizes != MAMBA_OK || batch * M * N == 0)
+        return sizes;
     const bool a_shared = (flags & MAMBA_MXFP4_SHARED_A) != 0, b_shared = (flags & MAMBA_MXFP4_SHARED_B) != 0;
-    if (!sizes_ok(batch, M, N) || !sizes_ok(a_shared ? 1 : batch, M, K) || !sizes_ok(b_shared ? 1 : batch, N, K))
-        return MAMBA_ERR_SHAPE;
-    if (K > mamba::kMaxMxInner || (flags & ~kFlags) != 0)
-        return MAMBA_ERR_UNSUPPORTED;
-    if (batch * M * N == 0)
-        return MAMBA_OK;
-    if (batch * ((M + 31) / 32) * ((N + 127) / 128) >= kMaxBlocks)
-        return MAMBA_ERR_SHAPE;
     if (!out || (K > 0 && (!a || !b || !a_scale || !b_scale)))
         return MAMBA_ERR_NULL;
     if (!aligned(a, 16) || !aligned(b, 16) || !aligned(a_scale, 8) || !aligned(b_scale, 8) ||
@@ -124,6 +135,31 @@ mamba_status mamba_mxfp4_matmul(const uint8_t *a, const uint8_t *b, const uint8_
     const mamba::MxMatmulArgs args{a, a_scale, b, b_scale, out, batch, M, N, mamba::mx_groups(K),
                                    a_shared, b_shared, out_type == MAMBA_BF16};
     return launched(mamba::launch_mxfp4_matmul(args, (hipStream_t)stream));
+}
+
+mamba_status mamba_mxfp4_matmul_form(int64_t batch, int64_t M, int64_t N, int64_t K, unsigned flags, int *form,
+                                     int64_t *tiles, int *slots)
+{
+    if (!form || !tiles || !slots)
+        return MAMBA_ERR_NULL;
+    const mamba_status st = matmul_sizes(batch, M, N, K, flags);
+    if (st != MAMBA_OK || batch * M * N == 0 || K == 0) {
+        *form = -1;
+        *tiles = *slots = 0;
+        return st;
+    }
+    mamba::MxMatmulArgs args{};
+    args.batch = batch;
+    args.M = M;
+    args.N = N;
+    args.groups = mamba::mx_groups(K);
+    args.a_shared = (flags & MAMBA_MXFP4_SHARED_A) != 0;
+    args.b_shared = (flags & MAMBA_MXFP4_SHARED_B) != 0;
+    const mamba::MxMatmulForm f = mamba::mxfp4_matmul_form(args);
+    *form = f.form;
+    *tiles = f.tiles;
+    *slots = f.slots;
+    return MAMBA_OK;
 }
 
 }  // extern "C"

@@ -62,7 +62,7 @@ def test_dequantise_rejects(lib, kw, want):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(out_type=2), EDTYPE), (dict(batch=-1), ESHAPE), (dict(M=-1), ESHAPE), (dict(N=-1), ESHAPE), (dict(K=-1), ESHAPE),
-    (dict(K=(1 << 23) + 1), EUNSUP), (dict(flags=4), EUNSUP), (dict(batch=1, M=1 << 20, N=1 << 21), ESHAPE), (dict(a=None), ENULL),
+    (dict(K=(1 << 23) + 1), EUNSUP), (dict(flags=4), EUNSUP), (dict(batch=1, M=1 << 20, N=1 << 23), ESHAPE), (dict(a=None), ENULL),
     (dict(b=None), ENULL), (dict(sa=None), ENULL), (dict(sb=None), ENULL), (dict(out=None), ENULL), (dict(a=_p(4, 8)), EALIGN),
     (dict(b=_p(5, 4)), EALIGN), (dict(sa=_p(6, 4)), EALIGN), (dict(sb=_p(7, 1)), EALIGN), (dict(out=_p(8, 1)), EALIGN),
     (dict(out=A), EALIAS), (dict(out=B), EALIAS), (dict(out=SA), EALIAS), (dict(out=SB), EALIAS),
