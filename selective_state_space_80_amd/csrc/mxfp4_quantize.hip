@@ -5,7 +5,9 @@
 // format's conversion); rounding to nearest, ties to even, by the hardware's
 // conversion, which divides by the power of two exactly.
 //
-// All of it is bound by memory: 2 bytes in, 0.53 out (bf16).
+// All of it is bound by memory: 2 bytes in, 0.53 out (bf16).  8 x 5120 x 2048, inputs
+// from memory: bf16 token-major 39.5 us, channel-major 38.8 (5.4 TB/s; a large copy moves
+// 5.1), fp32 67.8 and 75.3, back to bf16 31.9.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -108,95 +110,183 @@ template <int ROWS, bool BF16> __global__ __launch_bounds__(256) void quantize_k
 }
 
 // ---- channel-major ---------------------------------------------------------------------
-// x [B, K, L] to rows (b, t) of K.  A workgroup takes one group of channels and 64
-// tokens; a wave takes one block of 32 channels, a lane a token, so that its loads run
-// along the tokens and a block's largest value needs no other lane.
+// x [B, K, L] to rows (b, t) of K.  A workgroup takes one group of channels and 128
+// tokens (bf16; 64 in fp32); a wave takes one block of 32 channels, a lane two tokens
+// (one), so that a load instruction takes 256 bytes of a channel and a block's largest
+// value needs no other lane.  The packed rows go out by way of LDS, whole lines of 128
+// bytes (chunk c of token t at c ^ (t / 2 % 8)), and so do the scales.
 template <bool BF16> __global__ __launch_bounds__(512) void quantize_channel_kernel(const MxQuantArgs p)
 {
     using T = typename Elem<BF16>::T;
-    constexpr int kTokens = 64;
+    constexpr int kEach = BF16 ? 2 : 1, kTokens = 64 * kEach;
+    __shared__ __attribute__((aligned(16))) uint8_t rows_out[kTokens * kMxGroupBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t scales_out[kTokens * kMxScales];
     const int64_t groups = mx_groups(p.K), rows = p.B * p.L, tiles = (p.L + kTokens - 1) / kTokens;
     const int64_t tile = blockIdx.x % tiles, g = blockIdx.x / tiles % groups, b = blockIdx.x / tiles / groups;
     const int lane = threadIdx.x & 63, block = threadIdx.x / 64;
-    const int64_t t = tile * kTokens + lane, k = g * kMxGroup + block * 32;
-    if (t >= p.L)
-        return;
+    const int64_t t = tile * kTokens + lane * kEach, k = g * kMxGroup + block * 32;
+    const int left = p.K - k < 32 ? (p.K > k ? (int)(p.K - k) : 0) : 32;  // channels of this block
     const T *x = (const T *)p.x + (b * p.K + k) * p.L + t;
-    float f[4][8];
+    uint32_t v[32];  // a channel each; bf16: two tokens, the first in the low half
+    if (t + kEach <= p.L) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-        f[j / 8][j % 8] = k + j < p.K ? Elem<BF16>::load(x + (int64_t)j * p.L) : 0.f;
-    uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        const uint32_t v = __float_as_uint(f[j / 8][j % 8]) & 0x7fffffffu;
-        top = top > v ? top : v;
-    }
-    const uint32_t code = scale_code(top);
-    const u32x4 w = {pack8(f[0], code), pack8(f[1], code), pack8(f[2], code), pack8(f[3], code)};
-    const int64_t row = b * p.L + t;
-    *(u32x4 *)(p.q + (row * groups + g) * kMxGroupBytes + block * 16) = w;
-    p.scale[(g * rows + row) * kMxScales + block] = (uint8_t)code;
-}
-
-// ---- back ------------------------------------------------------------------------------
-// A lane takes 8 elements; the product with the power of two is exact but where it
-// leaves the range of fp32.
-template <bool BF16> __global__ __launch_bounds__(256) void dequantize_kernel(const MxDequantArgs p)
-{
-    using T = typename Elem<BF16>::T;
-    const int64_t groups = mx_groups(p.K);
-    const int64_t g = blockIdx.x % groups, row = blockIdx.x / groups * 8 + threadIdx.x / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t k = g * kMxGroup + lane * 8;
-    if (row >= p.rows || k >= p.K)
-        return;
-    const uint32_t w = *(const uint32_t *)(p.q + (row * groups + g) * kMxGroupBytes + lane * 4);
-    const uint32_t code = p.scale[(g * p.rows + row) * kMxScales + lane / 4];
-    const float s = __uint_as_float(code == kExpNan ? 0x7fc00000u : (code ? code << 23 : 0x00400000u));
-    float f[8];
-    typedef float f32x2v __attribute__((ext_vector_type(2)));
-    const f32x2v a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.f, 1),
-                 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.f, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.f, 3);
-    f[0] = a[0] * s, f[1] = a[1] * s, f[2] = b[0] * s, f[3] = b[1] * s;
-    f[4] = c[0] * s, f[5] = c[1] * s, f[6] = d[0] * s, f[7] = d[1] * s;
-    T *o = (T *)p.out + row * p.K + k;
-    if (k + 8 <= p.K) {
-        if constexpr (BF16) {
-            const u32x4 v = {cvt2(f[0], f[1]), cvt2(f[2], f[3]), cvt2(f[4], f[5]), cvt2(f[6], f[7])};
-            __builtin_memcpy(o, &v, 16);
-        } else {
-            __builtin_memcpy(o, f, 32);
+        for (int j = 0; j < 32; ++j) {
+            v[j] = 0;
+            if (j < left)
+                __builtin_memcpy(&v[j], x + (int64_t)j * p.L, 4);
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 7; ++j)
-            if (k + j < p.K)
-                Elem<BF16>::store(o + j, f[j]);
+        for (int j = 0; j < 32; ++j)
+            v[j] = BF16 && t < p.L && j < left ? (uint32_t)x[(int64_t)j * p.L] : 0;
+    }
+    auto put = [&](int token, uint32_t code, u32x4 w) {
+        *(u32x4 *)(rows_out + token * kMxGroupBytes + (block ^ ((token >> 1) & 7)) * 16) = w;
+        scales_out[token * kMxScales + block] = (uint8_t)code;
+    };
+    if constexpr (BF16) {
+        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+        u16x2 top = {0, 0};  // without their signs, bf16 are in the order of their bits
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, v[j] & 0x7fff7fffu));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t code = scale_code((uint32_t)top[h] << 16);
+            const float s = __uint_as_float(code << 23);
+            u32x4 w = {0, 0, 0, 0};
+            auto pair = [&](int j) {  // this token's channels j and j + 1
+                return __builtin_bit_cast(bf16x2, __builtin_amdgcn_perm(v[j + 1], v[j], h ? 0x07060302u : 0x05040100u));
+            };
+            if (code != kExpNan) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t q = 0;
+                    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, pair(c * 8), s, 0);
+                    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, pair(c * 8 + 2), s, 1);
+                    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, pair(c * 8 + 4), s, 2);
+                    w[c] = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, pair(c * 8 + 6), s, 3);
+                }
+            }
+            put(lane * 2 + h, code, w);
+        }
+    } else {
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            top = top > (v[j] & 0x7fffffffu) ? top : v[j] & 0x7fffffffu;
+        const uint32_t code = scale_code(top);
+        u32x4 w;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                f[j] = __uint_as_float(v[c * 8 + j]);
+            w[c] = pack8(f, code);
+        }
+        put(lane, code, w);
+    }
+    __syncthreads();
+    const int64_t row0 = b * p.L + tile * kTokens;
+    const int tokens = p.L - tile * kTokens < kTokens ? (int)(p.L - tile * kTokens) : kTokens;
+#pragma unroll
+    for (int i = 0; i < kTokens / 64; ++i) {
+        const int token = i * 64 + threadIdx.x / 8, c = threadIdx.x & 7;
+        if (token < tokens)
+            *(u32x4 *)(p.q + ((row0 + token) * groups + g) * kMxGroupBytes + c * 16) =
+                *(const u32x4 *)(rows_out + token * kMxGroupBytes + (c ^ ((token >> 1) & 7)) * 16);
+    }
+    if (threadIdx.x < tokens)
+        *(u32x2 *)(p.scale + (g * rows + row0 + threadIdx.x) * kMxScales) =
+            *(const u32x2 *)(scales_out + threadIdx.x * kMxScales);
+}
+
+// ---- back ------------------------------------------------------------------------------
+// A lane takes what it stores in 16 bytes, 8 elements (bf16) or 4, so that a wave's store
+// is one piece (with 8 in fp32 it was two half-empty ones: 8 x 2048 x 5120 123 us), of
+// several rows.  The product with the power of two is exact but where it leaves the range
+// of the type.
+template <int ROWS, bool BF16> __global__ __launch_bounds__(256) void dequantize_kernel(const MxDequantArgs p)
+{
+    using T = typename Elem<BF16>::T;
+    constexpr int kEach = BF16 ? 8 : 4, kLanes = kMxGroup / kEach, kPass = 256 / kLanes, kUnits = ROWS / kPass;
+    const int64_t groups = mx_groups(p.K);
+    const int64_t g = blockIdx.x % groups, row0 = blockIdx.x / groups * ROWS + threadIdx.x / kLanes;
+    const int lane = threadIdx.x & (kLanes - 1);
+    const int64_t k = g * kMxGroup + lane * kEach;
+    if (k >= p.K)
+        return;
+    uint32_t w[kUnits], codes[kUnits];
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+        const int64_t row = row0 + u * kPass < p.rows ? row0 + u * kPass : p.rows - 1;
+        const uint8_t *q = p.q + (row * groups + g) * kMxGroupBytes + lane * kEach / 2;
+        w[u] = BF16 ? *(const uint32_t *)q : *(const uint16_t *)q;
+        codes[u] = p.scale[(g * p.rows + row) * kMxScales + lane * kEach / 32];
+    }
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+        const int64_t row = row0 + u * kPass;
+        if (row >= p.rows)
+            return;
+        const uint32_t code = codes[u];
+        const float s = __uint_as_float(code == kExpNan ? 0x7fc00000u : (code ? code << 23 : 0x00400000u));
+        typedef float f32x2v __attribute__((ext_vector_type(2)));
+        f32x2v v[kEach / 2];
+        v[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[u], 1.f, 0);
+        v[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[u], 1.f, 1);
+        if constexpr (BF16) {
+            v[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[u], 1.f, 2);
+            v[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[u], 1.f, 3);
+        }
+        float f[kEach];
+#pragma unroll
+        for (int j = 0; j < kEach; ++j)
+            f[j] = v[j / 2][j % 2] * s;
+        T *o = (T *)p.out + row * p.K + k;
+        if (k + kEach <= p.K) {
+            if constexpr (BF16) {
+                const u32x4 b = {cvt2(f[0], f[1]), cvt2(f[2], f[3]), cvt2(f[4], f[5]), cvt2(f[6], f[7])};
+                __builtin_memcpy(o, &b, 16);
+            } else {
+                __builtin_memcpy(o, f, 16);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kEach - 1; ++j)
+                if (k + j < p.K)
+                    Elem<BF16>::store(o + j, f[j]);
+        }
     }
 }
 
 }  // namespace
 
+// Units of 8 rows and a group: four a workgroup, whose loads are in flight together,
+// where that still leaves work for every CU.
+static bool four_units(int64_t rows, int64_t groups) { return rows * groups >= 32 * 1024; }
+
 hipError_t launch_quantize_mxfp4(const MxQuantArgs &a, hipStream_t s)
 {
     const int64_t rows = a.B * a.L, groups = mx_groups(a.K);
-    const bool few = rows * groups < 32 * 1024;
-    const dim3 grid((unsigned)(few ? (rows + 7) / 8 * groups : (rows + 31) / 32 * groups)), block(256);
-    if (a.bf16 && few)
-        quantize_kernel<8, true><<<grid, block, 0, s>>>(a);
-    else if (a.bf16)
+    const bool four = four_units(rows, groups);
+    const dim3 grid((unsigned)(four ? (rows + 31) / 32 * groups : (rows + 7) / 8 * groups)), block(256);
+    if (a.bf16 && four)
         quantize_kernel<32, true><<<grid, block, 0, s>>>(a);
-    else if (few)
-        quantize_kernel<8, false><<<grid, block, 0, s>>>(a);
-    else
+    else if (a.bf16)
+        quantize_kernel<8, true><<<grid, block, 0, s>>>(a);
+    else if (four)
         quantize_kernel<32, false><<<grid, block, 0, s>>>(a);
+    else
+        quantize_kernel<8, false><<<grid, block, 0, s>>>(a);
     return hipGetLastError();
 }
 
 hipError_t launch_quantize_mxfp4_channel_major(const MxQuantArgs &a, hipStream_t s)
 {
-    const dim3 grid((unsigned)((a.L + 63) / 64 * mx_groups(a.K) * a.B)), block(512);
+    const int64_t tokens = a.bf16 ? 128 : 64;
+    const dim3 grid((unsigned)((a.L + tokens - 1) / tokens * mx_groups(a.K) * a.B)), block(512);
     if (a.bf16)
         quantize_channel_kernel<true><<<grid, block, 0, s>>>(a);
     else
@@ -206,11 +296,17 @@ hipError_t launch_quantize_mxfp4_channel_major(const MxQuantArgs &a, hipStream_t
 
 hipError_t launch_dequantize_mxfp4(const MxDequantArgs &a, hipStream_t s)
 {
-    const dim3 grid((unsigned)((a.rows + 7) / 8 * mx_groups(a.K))), block(256);
-    if (a.bf16)
-        dequantize_kernel<true><<<grid, block, 0, s>>>(a);
+    const int64_t groups = mx_groups(a.K);
+    const bool four = four_units(a.rows, groups);
+    const dim3 grid((unsigned)(four ? (a.rows + 31) / 32 * groups : (a.rows + 7) / 8 * groups)), block(256);
+    if (a.bf16 && four)
+        dequantize_kernel<32, true><<<grid, block, 0, s>>>(a);
+    else if (a.bf16)
+        dequantize_kernel<8, true><<<grid, block, 0, s>>>(a);
+    else if (four)
+        dequantize_kernel<32, false><<<grid, block, 0, s>>>(a);
     else
-        dequantize_kernel<false><<<grid, block, 0, s>>>(a);
+        dequantize_kernel<8, false><<<grid, block, 0, s>>>(a);
     return hipGetLastError();
 }
 
