@@ -98,7 +98,7 @@ template <int N> struct ScaleLoads {
 // takes byte 2 r + lane / 32.  The one barrier of a step stands before its last round:
 // there every wave has read this stage (it may be overwritten) and the next stage has
 // arrived.
-constexpr int kStaging = 2048;  // of a wave's outputs: 32 rows of 64 bytes
+constexpr int kStaging = 2048;  // of a wave's outputs: 16 rows of 128 bytes
 constexpr int scale_loads(int rows, int waves) { return (rows + 32 * waves - 1) / (32 * waves); }
 constexpr int stage_bytes(int rows, int waves) { return rows * kStep + scale_loads(rows, waves) * waves * 256; }
 constexpr int tile_lds(int WM, int WN, int FM, int FN, int STAGES)
@@ -119,7 +119,9 @@ __global__ __launch_bounds__(64 * WM * WN, tile_waves(WM, WN, FM, FN, STAGES)) v
     constexpr int LA = TM / 8 / NW, LB = TN / 8 / NW;  // loads of a wave and stage
     constexpr int LS = scale_loads(TM + TN, NW), kLoads = LA + LB + LS;
     static_assert(TM % (32 * LS) == 0, "a wave's scales are of one operand");
-    constexpr int kStores = FM * FN * (BF16 ? 2 : 4);  // of a wave and a whole tile
+    constexpr int kWide = BF16 ? 2 : 1;                // blocks of 32 columns in 128 bytes
+    constexpr int kStores = FM * FN / kWide * 4;       // of a wave and a whole tile
+    static_assert(FN % kWide == 0, "a wave's columns fill whole lines");
     __shared__ __attribute__((aligned(16))) char smem[tile_lds(WM, WN, FM, FN, STAGES)];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -297,46 +299,65 @@ __global__ __launch_bounds__(64 * WM * WN, tile_waves(WM, WN, FM, FN, STAGES)) v
         step(std::true_type{});
         for (int s = 1; s < p.groups; ++s)
             step(std::false_type{});
-        // Round and store, 32 rows of 64 bytes at a time through the wave's own piece
-        // of LDS, so that a store instruction writes 16 whole pieces of memory traffic.
-        // Chunk c of row r lies at c ^ (r / 4 % 4).
+        // Round and store, 16 rows of 128 bytes at a time through the wave's own piece
+        // of LDS, so that a store instruction writes 8 whole lines (in pieces of 64
+        // bytes, stores past the caches reach 3.3 TB/s, by whole lines 5.3).  A pass
+        // takes half of the lanes' rows: 32 would not fit beside the scales.  In bf16
+        // lanes l and l + 32 first exchange, so that each has 8 neighbouring columns.
         using T = typename Elem<BF16>::T;
-        constexpr int kPerChunk = BF16 ? 8 : 4;   // elements in 16 bytes
-        constexpr int kParts = BF16 ? 1 : 2;      // of a block: 64 bytes wide
+        constexpr int kPerChunk = BF16 ? 8 : 4;  // elements in 16 bytes
         char *st = smem + STAGES * kStage + wave * kStaging;
+        int at = lane;
+        asm volatile("" : "+v"(at));  // addresses made anew for each tile: held over the steps, they spill
+        const int row16 = at & 15, low = at >> 4 & 1, upper = at >> 5;
         auto finish = [&](auto full) {
 #pragma unroll
-            for (int i = 0; i < FM; ++i)
+            for (int j0 = 0; j0 < FN; j0 += kWide) {
+                const int64_t n = t.n0 + (wn * FN + j0) * 32 + (at & 7) * kPerChunk;
 #pragma unroll
-                for (int j = 0; j < FN; ++j)
+                for (int i = 0; i < FM; ++i) {
+                    u32x4 w[4];  // chunks of 16 bytes of row fr
+                    if constexpr (BF16) {
 #pragma unroll
-                    for (int h = 0; h < kParts; ++h) {
+                        for (int c = 0; c < 4; ++c) {
+                            const f32x16 &v = acc[i][j0 + c / 2];
+                            const int e = c % 2 * 8;
 #pragma unroll
-                        for (int e = 0; e < 4 / kParts; ++e) {
-                            const int at = (h * 2 + e) * 4;
-                            if constexpr (BF16) {
-                                const u32x2 w = {cvt2(acc[i][j][e * 4], acc[i][j][e * 4 + 1]),
-                                                 cvt2(acc[i][j][e * 4 + 2], acc[i][j][e * 4 + 3])};
-                                *(u32x2 *)(st + fr * 64 + (e ^ ((fr >> 2) & 3)) * 16 + half * 8) = w;
-                            } else {
-                                const f32x4 w = {acc[i][j][at], acc[i][j][at + 1], acc[i][j][at + 2], acc[i][j][at + 3]};
-                                *(f32x4 *)(st + fr * 64 + ((e * 2 + half) ^ ((fr >> 2) & 3)) * 16) = w;
+                            for (int d = 0; d < 2; ++d) {
+                                const auto x = __builtin_amdgcn_permlane32_swap(
+                                    cvt2(v[e + d * 2], v[e + d * 2 + 1]), cvt2(v[e + 4 + d * 2], v[e + 5 + d * 2]), false, false);
+                                w[c][d] = x[0];
+                                w[c][2 + d] = x[1];
                             }
                         }
-                        const int64_t n = t.n0 + (wn * FN + j) * 32 + h * 16 + (lane & 3) * kPerChunk;
-                        const int64_t m = t.m0 + (wm * FM + i) * 32 + (lane >> 2);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int d = 0; d < 4; ++d)
+                                w[c][d] = __float_as_uint(acc[i][j0][c * 4 + d]);
+                    }
+#pragma unroll
+                    for (int pass = 0; pass < 2; ++pass) {
+                        if (low == pass) {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                *(u32x4 *)(st + row16 * 128 + place(row16, c * 2 + upper) * 16) = w[c];
+                        }
+                        asm volatile("" ::: "memory");  // what is read below other lanes have written
+                        const int64_t m = t.m0 + (wm * FM + i) * 32 + pass * 16 + (at >> 3);
                         T *o = (T *)p.out + (t.batch * p.M + m) * p.N + n;
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
-                            const int row = r * 16 + (lane >> 2);
-                            const u32x4 v = *(const u32x4 *)(st + row * 64 + ((lane & 3) ^ ((row >> 2) & 3)) * 16);
+                            const int row = r * 8 + (at >> 3);
+                            const u32x4 v = *(const u32x4 *)(st + row * 128 + place(row, at & 7) * 16);
                             typedef u32x4 __attribute__((aligned(2))) loose;  // rows start at any element
-                            T *to = o + (int64_t)(r * 16) * p.N;
+                            T *to = o + (int64_t)(r * 8) * p.N;
                             if constexpr (full && STREAM) {
                                 __builtin_nontemporal_store(v, (loose *)to);
                             } else if constexpr (full) {
                                 *(loose *)to = v;
-                            } else if (m + r * 16 < p.M) {
+                            } else if (m + r * 8 < p.M) {
                                 if (n + kPerChunk <= p.N) {
                                     *(loose *)to = v;
                                 } else {
@@ -352,6 +373,8 @@ __global__ __launch_bounds__(64 * WM * WN, tile_waves(WM, WN, FM, FN, STAGES)) v
                             }
                         }
                     }
+                }
+            }
         };
         stores_known = t.m0 + TM <= p.M && t.n0 + TN <= p.N;
         if (stores_known)
