@@ -534,20 +534,32 @@ template <bool BF16> __global__ __launch_bounds__(256) void zero_kernel(void *ou
 //   max(rounds * steps * alone, tiles / slots * steps * busy) + rounds * each + once
 // rounds: output tiles a workgroup slot takes after one another; alone: a step of one
 // group on an otherwise free card; busy: with every slot taken, where power and the
-// shared caches hold the rate; each: a tile's end.
+// shared caches hold the rate; each: a tile's end.  The constants are fitted to 1000
+// shapes drawn from 1 x 16 to 65536 x 8192 with 64 to 8192 of the inner axis, each timed
+// in every form; the form chosen takes 1.9 % more than the fastest on average, 5.3 % at
+// the ninetieth percentile, and 31 % at the worst (30044 x 4360 x 107: 78 us, 59).  Both
+// sides of some of the choices, in us:
+//   8 x 5120 x 2048 x 2560   256 x 256 tiles 110, 128 x 128 130
+//   16384 x 1536 x 768       128 x 128 tiles of two stages 19.9, 256 x 256 22.2, 128 x 64 35.6
+//   256 x 5120 x 2560        128 x 128 tiles of two stages 8.5, of four 8.9, rings of 48 x 64 9.4
+//   512 x 1536 x 768         rings of 64 x 48 4.4, of 48 x 64 6.4, 128 x 128 tiles 4.9
+//   256 x 2560 x 5120        rings of 64 x 48 6.8, of 64 x 64 7.7, 128 x 128 tiles 13.4
+//   64 x 2560 x 5120         rings of 32 x 32 4.4, of 32 x 64 5.3, of 16 x 16 6.0
+//   1 x 5120 x 2560          rings of 32 x 32 4.2, of 64 x 64 5.5, 128 x 128 tiles 8.1
 enum Form { kTile256, kTile128, kTile128Deep, kTile64, kRing44, kRing34, kRing43, kRing24, kRing42, kRing22, kRing12, kRing21, kRing11, kForms };
 struct FormCost {
     int tm, tn, slots;
     double alone, busy, each, once;
 };
+// A ring's loads bound it, alone or not.
 constexpr FormCost ring_cost(int tm, int tn)
 {
-    return FormCost{tm, tn, kCus, .00178 * (tm + tn), .00178 * (tm + tn), 1.04 + .00055 * tm * tn, 1.3};
+    return FormCost{tm, tn, kCus, .0014 * (tm + tn), .0014 * (tm + tn), 1.32 + .000135 * tm * tn, 2.17};
 }
-constexpr FormCost kCosts[kForms] = {{256, 256, kCus, 1.30, 1.50, 8.80, 1.30},
-                                     {128, 128, 2 * kCus, 0.80, 1.15, 2.50, 2.50},
-                                     {128, 128, kCus, 0.51, 0.69, 2.10, 2.60},
-                                     {128, 64, kCus, 0.41, 0.48, 1.75, 2.86},
+constexpr FormCost kCosts[kForms] = {{256, 256, kCus, 1.51, 1.54, 5.93, 2.63},
+                                     {128, 128, 2 * kCus, 0.63, 1.16, 2.62, 1.92},
+                                     {128, 128, kCus, 0.45, 0.64, 2.07, 2.35},
+                                     {128, 64, kCus, 0.49, 0.50, 1.49, 2.34},
                                      ring_cost(64, 64), ring_cost(48, 64), ring_cost(64, 48), ring_cost(32, 64), ring_cost(64, 32),
                                      ring_cost(32, 32), ring_cost(16, 32), ring_cost(32, 16), ring_cost(16, 16)};
 constexpr int64_t kMostRingTiles = 1 << 16;  // of 512 threads
