@@ -861,26 +861,27 @@ def int8_matmul_form(M, N, K, batch=1, aligned=True, flags=0):
 def _gated_arguments(x, r, i, lam, r_bias, i_bias, z, h0, reset):
     """Checks shared by the gated recurrence's calls; reset [B, L] for a scan."""
     torch = _torch()
-    shape, io_t, dev, index = x.shape, x.dtype, x.device, x.get_device()
-    f32 = torch.float32
-    D = shape[1]
+    shape, io_t, index, f32 = x.shape, x.dtype, x.get_device(), torch.float32
+    per = (shape[1],)
     if not (x.is_contiguous() and _is(r, shape, io_t, index) and _is(i, shape, io_t, index)
-            and _is(lam, (D,), f32, index)):
+            and _is(lam, per, f32, index) and (r_bias is None or _is(r_bias, per, f32, index))
+            and (i_bias is None or _is(i_bias, per, f32, index))
+            and (z is None or _is(z, shape, io_t, index))):
+        dev = x.device
         _check(x, "x", shape)
         _check(r, "r", shape, io_t, dev)
         _check(i, "i", shape, io_t, dev)
-        _check(lam, "lam", (D,), f32, dev)
-    for t, name in ((r_bias, "r_bias"), (i_bias, "i_bias")):
-        if t is not None and not _is(t, (D,), f32, index):
-            _check(t, name, (D,), f32, dev)
-    if z is not None and not _is(z, shape, io_t, index):
-        _check(z, "z", shape, io_t, dev)
+        _check(lam, "lam", per, f32, dev)
+        _check(r_bias, "r_bias", per, f32, dev, optional=True)
+        _check(i_bias, "i_bias", per, f32, dev, optional=True)
+        _check(z, "z", shape, io_t, dev, optional=True)
     if h0 is not None and not _is(h0, shape[:2], f32, index):
-        _check(h0, "h0", shape[:2], f32, dev)
+        _check(h0, "h0", shape[:2], f32, x.device)
     if reset is not None:
         if reset.dtype is not torch.bool and reset.dtype is not torch.uint8:
             raise TypeError(f"reset must be bool or uint8, got {reset.dtype}")
-        _check(reset, "reset", (shape[0], shape[2]), device=dev)
+        if not _is(reset, (shape[0], shape[2]), reset.dtype, index):
+            _check(reset, "reset", (shape[0], shape[2]), device=x.device)
 
 
 def gated_scan_fwd(x, r, i, lam, r_bias=None, i_bias=None, z=None, h0=None, reset=None, c=8.0,
@@ -936,12 +937,14 @@ def gated_scan_bwd(x, r, i, lam, dout, r_bias=None, i_bias=None, z=None, h0=None
     lib = load_library()
     B, D, L = x.shape
     _gated_arguments(x, r, i, lam, r_bias, i_bias, z, h0, reset)
-    dev = x.device
-    _check(dout, "dout", x.shape, x.dtype, dev)
-    _check(dh_last, "dh_last", (B, D), torch.float32, dev, optional=True)
+    dev, index, f32 = x.device, x.get_device(), torch.float32
+    if not _is(dout, x.shape, x.dtype, index):
+        _check(dout, "dout", x.shape, x.dtype, dev)
+    _check(dh_last, "dh_last", (B, D), f32, dev, optional=True)
     if checkpoints is not None:
-        _check(checkpoints, "checkpoints", (B, D, lib.mamba_gated_scan_checkpoints(L)),
-               torch.float32, dev)
+        kept = (B, D, lib.mamba_gated_scan_checkpoints(L))
+        if not _is(checkpoints, kept, f32, index):
+            _check(checkpoints, "checkpoints", kept, f32, dev)
     g = {"dx": torch.empty_like(x), "dr": torch.empty_like(x), "di": torch.empty_like(x),
          "dz": None if z is None else torch.empty_like(x), "dlam": torch.empty_like(lam),
          "dr_bias": torch.empty_like(lam), "di_bias": torch.empty_like(lam),
@@ -965,17 +968,19 @@ def gated_state_update(h, x, r, i, lam, r_bias=None, i_bias=None, z=None, c=8.0,
     the new state in h_out; x, r, i, z [B,D] f32/bf16.  Returns y [B,D] of x's dtype."""
     torch = _torch()
     lib = load_library()
-    B, D = x.shape
-    _check(h, "h", (B, D), torch.float32, x.device)
+    shape, index, f32 = x.shape, x.get_device(), torch.float32
+    B, D = shape
+    if h is None or not _is(h, shape, f32, index):
+        _check(h, "h", shape, f32, x.device)
     _gated_arguments(x, r, i, lam, r_bias, i_bias, z, None, None)
     if h_out is None:
         h_out = h
-    else:
-        _check(h_out, "h_out", (B, D), torch.float32, x.device)
+    elif not _is(h_out, shape, f32, index):
+        _check(h_out, "h_out", shape, f32, x.device)
     if out is None:
         out = torch.empty_like(x)
-    else:
-        _check(out, "out", x.shape, x.dtype, x.device)
+    elif not _is(out, shape, x.dtype, index):
+        _check(out, "out", shape, x.dtype, x.device)
     st = lib.mamba_gated_state_update(h.data_ptr(), h_out.data_ptr(), x.data_ptr(), r.data_ptr(),
                                       i.data_ptr(), lam.data_ptr(), _addr(r_bias), _addr(i_bias),
                                       _addr(z), out.data_ptr(), B, D, c, _io_dtype(x), _raw_stream(x))

@@ -240,10 +240,24 @@ template <int G, bool DROPS> __device__ __forceinline__ Span<DROPS> join_behind(
     return G == 64 || in < G - 1 ? e : none;
 }
 
-// Lanes a row of L steps takes, and how many waves share a row of more than a chunk.
+// Threads of a workgroup: one row where several waves share it, which meet in LDS.
+constexpr int gated_threads(int waves) { return waves == 1 ? 256 : 64 * waves; }
+
+// Lanes a row of L steps takes.
 inline int gated_group(int64_t L)
 {
     return L <= 4 * kLaneSteps ? 4 : (L <= 16 * kLaneSteps ? 16 : (L <= 32 * kLaneSteps ? 32 : 64));
+}
+
+// Waves that share a row: at most `most`, while there are fewer than about 12000 waves
+// in all and each has `least` chunks of the row or more (a power of two).
+inline int gated_waves(int64_t rows, int64_t L, int least, int most)
+{
+    const int64_t chunks = (L + 64 * kLaneSteps - 1) / (64 * kLaneSteps);
+    int waves = 1;
+    while (waves * 2 <= most && waves * 2 * rows <= 12288 && waves * 2 * least <= chunks)
+        waves *= 2;
+    return waves;
 }
 
 }  // namespace mamba

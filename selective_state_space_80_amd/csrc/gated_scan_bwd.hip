@@ -20,11 +20,11 @@ namespace mamba {
 namespace {
 
 template <int G, int WAVES, bool BF16, bool GATE, bool RESET>
-__global__ __launch_bounds__(256) void gated_bwd_kernel(const GatedScanBwdArgs p)
+__global__ __launch_bounds__(gated_threads(WAVES)) void gated_bwd_kernel(const GatedScanBwdArgs p)
 {
     using T = typename Elem<BF16>::T;
     using M = Span<RESET>;
-    constexpr int kRows = 256 / G / WAVES;  // of a workgroup
+    constexpr int kRows = gated_threads(WAVES) / G / WAVES;  // of a workgroup
     constexpr int kSpan = G * kLaneSteps * WAVES;
     __shared__ float2 maps[2][WAVES];
     __shared__ float sums[3][WAVES];
@@ -223,8 +223,8 @@ __global__ __launch_bounds__(256) void gated_sums_kernel(const GatedScanBwdArgs 
 
 template <int G, int WAVES> hipError_t launch(const GatedScanBwdArgs &a, hipStream_t s)
 {
-    constexpr int kRows = 256 / G / WAVES;
-    const dim3 grid((unsigned)((a.f.B * a.f.D + kRows - 1) / kRows)), block(256);
+    constexpr int kRows = gated_threads(WAVES) / G / WAVES;
+    const dim3 grid((unsigned)((a.f.B * a.f.D + kRows - 1) / kRows)), block(gated_threads(WAVES));
     auto with = [&](auto bf16, auto gate, auto reset) {
         gated_bwd_kernel<G, WAVES, bf16, gate, reset><<<grid, block, 0, s>>>(a);
     };
@@ -249,15 +249,27 @@ template <int G, int WAVES> hipError_t launch(const GatedScanBwdArgs &a, hipStre
 
 }  // namespace
 
+// Waves of a row, both sides measured (us, inputs from memory):
+//   8 x 5120 x 2048 bf16, gated  one 313, two 365, four 459
+//   2 x 1536 x 8192 fp32         one 162, two 140, four 152
+//   1 x 1536 x 131072 bf16       one 667, two 599, four 596, eight 562
+//   1 x 256 x 131072 bf16, gated one 462, two 233, four 130, eight 126
 hipError_t launch_gated_scan_bwd(const GatedScanBwdArgs &a, hipStream_t s)
 {
     hipError_t e = hipSuccess;
-    if (a.f.B > 0) {
+    const int64_t rows = a.f.B * a.f.D;
+    if (rows > 0) {
         switch (gated_group(a.f.L)) {
         case 4: e = launch<4, 1>(a, s); break;
         case 16: e = launch<16, 1>(a, s); break;
         case 32: e = launch<32, 1>(a, s); break;
-        default: e = a.f.L > kGatedChunk && a.f.B * a.f.D < 4096 ? launch<64, 4>(a, s) : launch<64, 1>(a, s);
+        default:
+            switch (gated_waves(rows, a.f.L, 8, 8)) {
+            case 1: e = launch<64, 1>(a, s); break;
+            case 2: e = launch<64, 2>(a, s); break;
+            case 4: e = launch<64, 4>(a, s); break;
+            default: e = launch<64, 8>(a, s);
+            }
         }
     }
     if (e != hipSuccess)

@@ -16,11 +16,11 @@ namespace mamba {
 namespace {
 
 template <int G, int WAVES, bool BF16, bool GATE, bool RESET>
-__global__ __launch_bounds__(256) void gated_fwd_kernel(const GatedScanArgs p)
+__global__ __launch_bounds__(gated_threads(WAVES)) void gated_fwd_kernel(const GatedScanArgs p)
 {
     using T = typename Elem<BF16>::T;
     using M = Span<RESET>;
-    constexpr int kRows = 256 / G / WAVES;  // of a workgroup
+    constexpr int kRows = gated_threads(WAVES) / G / WAVES;  // of a workgroup
     constexpr int kSpan = G * kLaneSteps * WAVES;
     __shared__ float2 maps[2][WAVES];
     const int lane = threadIdx.x & (G - 1), wave = threadIdx.x / G % WAVES;
@@ -113,8 +113,8 @@ __global__ __launch_bounds__(256) void gated_fwd_kernel(const GatedScanArgs p)
 
 template <int G, int WAVES> hipError_t launch(const GatedScanArgs &a, hipStream_t s)
 {
-    constexpr int kRows = 256 / G / WAVES;
-    const dim3 grid((unsigned)((a.B * a.D + kRows - 1) / kRows)), block(256);
+    constexpr int kRows = gated_threads(WAVES) / G / WAVES;
+    const dim3 grid((unsigned)((a.B * a.D + kRows - 1) / kRows)), block(gated_threads(WAVES));
     auto with = [&](auto bf16, auto gate, auto reset) {
         gated_fwd_kernel<G, WAVES, bf16, gate, reset><<<grid, block, 0, s>>>(a);
     };
@@ -159,13 +159,26 @@ template <bool BF16, bool GATE> __global__ __launch_bounds__(256) void gated_ste
 
 }  // namespace
 
+// Waves of a row, both sides measured (us, inputs from memory):
+//   8 x 5120 x 2048 bf16, gated  one 162, two 187, four 182
+//   2 x 1536 x 8192 fp32         one 81.6, four 79.3, eight 79.5, 16 92.5
+//   1 x 1536 x 131072 bf16       one 403, two 341, four 339, eight 323, 16 340
+//   1 x 256 x 131072 bf16, gated one 307, four 88, eight 76, 16 71
+//   3 x 771 x 1001 fp32, gated   one 15.1, two 15.6, four 18.6
 hipError_t launch_gated_scan_fwd(const GatedScanArgs &a, hipStream_t s)
 {
     switch (gated_group(a.L)) {
     case 4: return launch<4, 1>(a, s);
     case 16: return launch<16, 1>(a, s);
     case 32: return launch<32, 1>(a, s);
-    default: return a.L > kGatedChunk && a.B * a.D < 4096 ? launch<64, 4>(a, s) : launch<64, 1>(a, s);
+    }
+    const int64_t rows = a.B * a.D;
+    switch (gated_waves(rows, a.L, 4, rows <= 256 ? 16 : 8)) {
+    case 1: return launch<64, 1>(a, s);
+    case 2: return launch<64, 2>(a, s);
+    case 4: return launch<64, 4>(a, s);
+    case 8: return launch<64, 8>(a, s);
+    default: return launch<64, 16>(a, s);
     }
 }
 

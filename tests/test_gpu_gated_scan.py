@@ -255,3 +255,28 @@ def test_offsets_past_32_bits():
     assert not y[:2].any() and not y[2, 0, :-700].any()
     assert (y[2, 0, -700:].float() - want[0, 0].float()).abs().max() <= 2.0 ** -7 * want.float().abs().max()
     assert abs(last[2, 0] - want_last[0, 0]) <= 1e-5 * abs(want_last[0, 0])
+
+
+@pytest.mark.parametrize("io", [F32, BF16])
+@pytest.mark.parametrize("L", [3600, 8200, 17000, 33000])
+def test_waves_that_share_a_row(io, L):
+    """Two, four, eight and sixteen waves a row, the last round of chunks not full."""
+    say(f"gated scan L={L} {io}")
+    _check_both(C.make(1, 3, L, io, seed=L, gate=io == BF16, reset=1e-3 if L % 16 else 0.0), seed=L + 1)
+
+
+def test_many_rows_of_many_chunks():
+    """Eight waves a row, rows in more than one workgroup a CU."""
+    p = C.make(1, 600, 20000, F32, seed=40, gate=False)
+    q = C.gradient_inputs(p, 41)
+    y, kept = _forward(p, return_checkpoints=True)
+    got = _backward(p, q, checkpoints=kept)
+    rows = [0, 1, 255, 256, 299, 599]
+    some = {k: (None if v is None else (v[:, rows].contiguous() if v.dim() > 1 else v[rows])) for k, v in p.items()}
+    sq = {k: v[:, rows].contiguous() for k, v in q.items()}
+    f, want = C.forward(some), C.backward(some, sq)
+    assert C.worst(y[:, rows], f["y"], f["y_err"]) <= 1
+    for name in ("dx", "dr", "di", "dh0"):
+        assert C.worst(got[name][:, rows], want[name], want[name + "_err"]) <= 1, name
+    for name in ("dlam", "dr_bias", "di_bias"):
+        assert C.worst(got[name][rows], want[name], want[name + "_err"]) <= 1, name
