@@ -123,8 +123,27 @@ __device__ __forceinline__ float sigmoid_log2(float x, float bias2)
     return hw_rcp(1.f + hw_exp2(fmaf(x, -kLog2e, -bias2)));
 }
 
-// ln(1 + e^x), once a row and accurately: it scales every v of the row.
-__device__ __forceinline__ float softplus_row(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
+// ln(1 + e^x), which scales every v of a row: max(x, 0) + ln(1 + t), t = e^-|x|.  t by
+// 2^x of the fraction of |x| log2 e, which the split constant gives to within 2^-25; the
+// logarithm as 2 atanh(q), q = t / (2 + t) at most 1/3, whose series to q^15 is left off
+// below 1e-8 relative.
+__device__ __forceinline__ float softplus_row(float x)
+{
+    constexpr float kLog2eLow = (float)(1.44269504088896340736 - (double)kLog2e);
+    const float y = -fabsf(x), whole = __builtin_rintf(y * kLog2e);
+    const float part = fmaf(y, kLog2eLow, fmaf(y, kLog2e, -whole));
+    const float t = __builtin_amdgcn_ldexpf(hw_exp2(part), (int)fmaxf(whole, -1000.f));
+    const float q = t * hw_rcp(2.f + t), q2 = q * q;
+    float s = 1.f / 15.f;
+    s = fmaf(s, q2, 1.f / 13.f);
+    s = fmaf(s, q2, 1.f / 11.f);
+    s = fmaf(s, q2, 1.f / 9.f);
+    s = fmaf(s, q2, 1.f / 7.f);
+    s = fmaf(s, q2, 1.f / 5.f);
+    s = fmaf(s, q2, 1.f / 3.f);
+    s = fmaf(s, q2, 1.f);
+    return fmaxf(x, 0.f) + 2.f * q * s;
+}
 
 // 1 - 2^-u for u >= 0, given a = 2^-u.  Below 1/8 from the series of 1 - e^-v, v = u ln 2, whose
 // truncation stays below 2e-8 relative there; above, the subtraction loses at most

@@ -202,23 +202,24 @@ __global__ __launch_bounds__(gated_threads(WAVES)) void gated_bwd_kernel(const G
     }
 }
 
-// Sums over the batch, in its order.
-__global__ __launch_bounds__(256) void gated_sums_kernel(const GatedScanBwdArgs p)
+// Sums over the batch, in its order: a thread a channel and parameter.
+__global__ __launch_bounds__(64) void gated_sums_kernel(const GatedScanBwdArgs p)
 {
-    const int64_t d = (int64_t)blockIdx.x * 256 + threadIdx.x, rows = p.f.B * p.f.D;
+    const int64_t d = (int64_t)blockIdx.x * 64 + threadIdx.x, rows = p.f.B * p.f.D;
     if (d >= p.f.D)
         return;
-    float q = 0.f, r = 0.f, i = 0.f;
-    for (int64_t at = d; at < rows; at += p.f.D) {
-        q += p.partials[at];
-        r += p.partials[rows + at];
-        i += p.partials[2 * rows + at];
+    const float *from = p.partials + blockIdx.y * rows + d;
+    float sum = 0.f;
+#pragma unroll 8
+    for (int64_t b = 0; b < p.f.B; ++b)
+        sum += from[b * p.f.D];
+    if (blockIdx.y == 0) {
+        // sigmoid(lam) / softplus(lam), which goes to 1 where both go to 0
+        const float lam = p.f.lam[d], t = expf(-fabsf(lam)), s = (lam < 0.f ? t : 1.f) / (1.f + t);
+        p.dlam[d] = lam < -80.f ? sum : sum * (s / softplus_row(lam));
+    } else {
+        (blockIdx.y == 1 ? p.dr_bias : p.di_bias)[d] = sum;
     }
-    // sigmoid(lam) / softplus(lam), which goes to 1 where both go to 0
-    const float lam = p.f.lam[d], t = expf(-fabsf(lam)), s = (lam < 0.f ? t : 1.f) / (1.f + t);
-    p.dlam[d] = lam < -80.f ? q : q * (s / softplus_row(lam));
-    p.dr_bias[d] = r;
-    p.di_bias[d] = i;
 }
 
 template <int G, int WAVES> hipError_t launch(const GatedScanBwdArgs &a, hipStream_t s)
@@ -274,7 +275,7 @@ hipError_t launch_gated_scan_bwd(const GatedScanBwdArgs &a, hipStream_t s)
     }
     if (e != hipSuccess)
         return e;
-    gated_sums_kernel<<<dim3((unsigned)((a.f.D + 255) / 256)), dim3(256), 0, s>>>(a);
+    gated_sums_kernel<<<dim3((unsigned)((a.f.D + 63) / 64), 3), dim3(64), 0, s>>>(a);
     return hipGetLastError();
 }
 

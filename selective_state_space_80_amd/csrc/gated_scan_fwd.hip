@@ -138,23 +138,87 @@ template <int G, int WAVES> hipError_t launch(const GatedScanArgs &a, hipStream_
 }
 
 // ---- one step ----------------------------------------------------------------------------
-// A thread a state: the parameters of neighbouring channels are neighbours.  What bounds
-// it is the launch for a few sequences, the state's traffic (8 of 16 bytes in bf16) for many.
-template <bool BF16, bool GATE> __global__ __launch_bounds__(256) void gated_step_kernel(const GatedStepArgs p)
+// A thread takes EACH consecutive channels of one or two sequences (256 x 5120 bf16,
+// gated: 8.4 us, 11.8 with one state a thread).  What bounds it is the launch for a few
+// sequences, the state's traffic (8 of 18 bytes) and its latency for many.
+template <int EACH, bool BF16> struct Few;  // EACH consecutive elements
+template <int EACH> struct Few<EACH, true> {
+    uint16_t v[EACH];
+    __device__ __forceinline__ void load(const uint16_t *p) { __builtin_memcpy(v, p, sizeof(v)); }
+    __device__ __forceinline__ float get(int j) const { return bf16_bits_to_f32(v[j]); }
+    static __device__ __forceinline__ void store(uint16_t *p, const float (&f)[EACH])
+    {
+        if constexpr (EACH == 4) {
+            const uint32_t w[2] = {cvt2(f[0], f[1]), cvt2(f[2], f[3])};
+            __builtin_memcpy(p, w, 8);
+        } else {
+            Elem<true>::store(p, f[0]);
+        }
+    }
+};
+template <int EACH> struct Few<EACH, false> {
+    float v[EACH];
+    __device__ __forceinline__ void load(const float *p) { __builtin_memcpy(v, p, sizeof(v)); }
+    __device__ __forceinline__ float get(int j) const { return v[j]; }
+    static __device__ __forceinline__ void store(float *p, const float (&f)[EACH]) { __builtin_memcpy(p, f, sizeof(f)); }
+};
+
+template <int EACH, bool BF16, bool GATE>
+__global__ __launch_bounds__(256) void gated_step_kernel(const GatedStepArgs p, int64_t parts, int sequences)
 {
     using T = typename Elem<BF16>::T;
-    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (n >= p.B * p.D)
+    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;  // parts of EACH channels, then sequences
+    const int64_t d = n % parts * EACH, b0 = n / parts * sequences;
+    if (b0 >= p.B)
         return;
-    const int64_t d = n % p.D;
-    const float rb = p.r_bias ? p.r_bias[d] * kLog2e : 0.f, ib = p.i_bias ? p.i_bias[d] * kLog2e : 0.f;
-    const float u = p.c * softplus_row(p.lam[d]) * kLog2e * sigmoid_log2(Elem<BF16>::load((const T *)p.r + n), rb);
-    const float a = hw_exp2(-u), e = loss_of(u, a), in = sigmoid_log2(Elem<BF16>::load((const T *)p.i + n), ib) *
-                                     Elem<BF16>::load((const T *)p.x + n);
-    float h = p.h[n];
-    h = fmaf(a, h, __builtin_amdgcn_sqrtf(e * (2.f - e)) * in);
-    p.h_out[n] = h;
-    Elem<BF16>::store((T *)p.y + n, GATE ? h * silu_hw(Elem<BF16>::load((const T *)p.z + n)) : h);
+    float rate[EACH], rb[EACH], ib[EACH];
+#pragma unroll
+    for (int j = 0; j < EACH; ++j) {
+        rate[j] = p.c * softplus_row(p.lam[d + j]) * kLog2e;
+        rb[j] = p.r_bias ? p.r_bias[d + j] * kLog2e : 0.f;
+        ib[j] = p.i_bias ? p.i_bias[d + j] * kLog2e : 0.f;
+    }
+    const int64_t end = b0 + sequences < p.B ? b0 + sequences : p.B;
+#pragma unroll 2
+    for (int64_t b = b0; b < end; ++b) {
+        const int64_t at = b * p.D + d;
+        Few<EACH, BF16> x, r, i, z;
+        Few<EACH, false> h;
+        h.load(p.h + at);
+        x.load((const T *)p.x + at);
+        r.load((const T *)p.r + at);
+        i.load((const T *)p.i + at);
+        if constexpr (GATE)
+            z.load((const T *)p.z + at);
+        float state[EACH], y[EACH];
+#pragma unroll
+        for (int j = 0; j < EACH; ++j) {
+            const float u = rate[j] * sigmoid_log2(r.get(j), rb[j]), a = hw_exp2(-u), e = loss_of(u, a);
+            const float in = sigmoid_log2(i.get(j), ib[j]) * x.get(j);
+            state[j] = fmaf(a, h.get(j), __builtin_amdgcn_sqrtf(e * (2.f - e)) * in);
+            y[j] = GATE ? state[j] * silu_hw(z.get(j)) : state[j];
+        }
+        Few<EACH, false>::store(p.h_out + at, state);
+        Few<EACH, BF16>::store((T *)p.y + at, y);
+    }
+}
+
+template <int EACH> hipError_t launch_step(const GatedStepArgs &a, hipStream_t s)
+{
+    // two sequences a thread where that leaves every CU eight waves (256 x 5120 bf16,
+    // gated: one 9.3 us, two 8.4, four 9.6; 64 x 5120: one 4.8, two 4.6, four 6.1)
+    const int64_t parts = a.D / EACH;
+    const int sequences = parts * (a.B / 2) >= 256 * 8 * 64 ? 2 : 1;
+    const dim3 grid((unsigned)((parts * ((a.B + sequences - 1) / sequences) + 255) / 256)), block(256);
+    if (a.bf16 && a.z)
+        gated_step_kernel<EACH, true, true><<<grid, block, 0, s>>>(a, parts, sequences);
+    else if (a.bf16)
+        gated_step_kernel<EACH, true, false><<<grid, block, 0, s>>>(a, parts, sequences);
+    else if (a.z)
+        gated_step_kernel<EACH, false, true><<<grid, block, 0, s>>>(a, parts, sequences);
+    else
+        gated_step_kernel<EACH, false, false><<<grid, block, 0, s>>>(a, parts, sequences);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -184,16 +248,8 @@ hipError_t launch_gated_scan_fwd(const GatedScanArgs &a, hipStream_t s)
 
 hipError_t launch_gated_step(const GatedStepArgs &a, hipStream_t s)
 {
-    const dim3 grid((unsigned)((a.B * a.D + 255) / 256)), block(256);
-    if (a.bf16 && a.z)
-        gated_step_kernel<true, true><<<grid, block, 0, s>>>(a);
-    else if (a.bf16)
-        gated_step_kernel<true, false><<<grid, block, 0, s>>>(a);
-    else if (a.z)
-        gated_step_kernel<false, true><<<grid, block, 0, s>>>(a);
-    else
-        gated_step_kernel<false, false><<<grid, block, 0, s>>>(a);
-    return hipGetLastError();
+    // four channels a thread where there are enough of them
+    return a.D % 4 == 0 && a.B * a.D >= 4 * 256 * 64 ? launch_step<4>(a, s) : launch_step<1>(a, s);
 }
 
 }  // namespace mamba
