@@ -195,7 +195,7 @@ def test_gradient_against_differences():
 
 @pytest.mark.parametrize("io", [F32, BF16])
 @pytest.mark.parametrize("gate", [False, True])
-@pytest.mark.parametrize("B,D", [(1, 1), (1, 2560), (3, 771), (256, 130)])
+@pytest.mark.parametrize("B,D", [(1, 1), (1, 2560), (3, 771), (256, 130), (33, 4096), (257, 5120)])
 def test_step(io, gate, B, D):
     say(f"gated step {B} x {D} {io} gate={gate}")
     p = C.make(B, D, 1, io, seed=D, gate=gate)
