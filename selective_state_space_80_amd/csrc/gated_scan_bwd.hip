@@ -32,14 +32,14 @@ __global__ __launch_bounds__(gated_threads(WAVES)) void gated_bwd_kernel(const G
     const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / (G * WAVES);
     const int64_t rows = p.f.B * p.f.D;
     const bool live = row < rows;
-    const int64_t at = live ? row : 0, d = at % p.f.D, L = live ? p.f.L : 0, first_of = at * p.f.L;
+    const int64_t at = live ? row : 0, L = live ? p.f.L : 0, first_of = at * p.f.L;
+    const uint32_t d = (uint32_t)at % (uint32_t)p.f.D;  // rows are below 2^24
     const T *x = (const T *)p.f.x + first_of, *r = (const T *)p.f.r + first_of, *i = (const T *)p.f.i + first_of;
     const T *z = GATE ? (const T *)p.f.z + first_of : nullptr, *dout = (const T *)p.dout + first_of;
     T *dx = (T *)p.dx + first_of, *dr = (T *)p.dr + first_of, *di = (T *)p.di + first_of;
     T *dz = GATE ? (T *)p.dz + first_of : nullptr;
-    const uint8_t *reset = RESET ? p.f.reset + at / p.f.D * p.f.L : nullptr;
-    const float rate = p.f.c * softplus_row(p.f.lam[d]) * kLog2e;
-    const float rb = p.f.r_bias ? p.f.r_bias[d] * kLog2e : 0.f, ib = p.f.i_bias ? p.f.i_bias[d] * kLog2e : 0.f;
+    const uint8_t *reset = RESET ? p.f.reset + (int64_t)((uint32_t)at / (uint32_t)p.f.D) * p.f.L : nullptr;
+    const float lam = p.f.lam[d], r_bias = p.f.r_bias ? p.f.r_bias[d] : 0.f, i_bias = p.f.i_bias ? p.f.i_bias[d] : 0.f;
     const int64_t chunks = (p.f.L + kGatedChunk - 1) / kGatedChunk;
     float carry = p.dh_last ? p.dh_last[at] : 0.f;  // a g of the step behind
     float sum_q = 0.f, sum_r = 0.f, sum_i = 0.f;
@@ -64,6 +64,8 @@ __global__ __launch_bounds__(gated_threads(WAVES)) void gated_bwd_kernel(const G
     const int64_t mine = ((int64_t)wave * G + lane) * kLaneSteps;
     if (base >= 0)
         fetch(base + mine);
+    const float rate = p.f.c * softplus_row(lam) * kLog2e;
+    const float rb = r_bias * kLog2e, ib = i_bias * kLog2e;
     int turn = 0;
     for (; base >= 0; base -= kSpan) {
         const int64_t t = base + mine;

@@ -26,13 +26,13 @@ __global__ __launch_bounds__(gated_threads(WAVES)) void gated_fwd_kernel(const G
     const int lane = threadIdx.x & (G - 1), wave = threadIdx.x / G % WAVES;
     const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / (G * WAVES);
     const bool live = row < p.B * p.D;  // the others' lanes run along, with nothing to load or store
-    const int64_t at = live ? row : 0, d = at % p.D, L = live ? p.L : 0;
+    const int64_t at = live ? row : 0, L = live ? p.L : 0;
+    const uint32_t d = (uint32_t)at % (uint32_t)p.D;  // rows are below 2^24
     const T *x = (const T *)p.x + at * p.L, *r = (const T *)p.r + at * p.L, *i = (const T *)p.i + at * p.L;
     const T *z = GATE ? (const T *)p.z + at * p.L : nullptr;
     T *y = (T *)p.y + at * p.L;
-    const uint8_t *reset = RESET ? p.reset + at / p.D * p.L : nullptr;
-    const float rate = p.c * softplus_row(p.lam[d]) * kLog2e;  // of the exponents of 2
-    const float rb = p.r_bias ? p.r_bias[d] * kLog2e : 0.f, ib = p.i_bias ? p.i_bias[d] * kLog2e : 0.f;
+    const uint8_t *reset = RESET ? p.reset + (int64_t)((uint32_t)at / (uint32_t)p.D) * p.L : nullptr;
+    const float lam = p.lam[d], r_bias = p.r_bias ? p.r_bias[d] : 0.f, i_bias = p.i_bias ? p.i_bias[d] : 0.f;
     const int64_t chunks = (p.L + kGatedChunk - 1) / kGatedChunk;
     float carry = p.h0 ? p.h0[at] : 0.f;
 
@@ -50,6 +50,9 @@ __global__ __launch_bounds__(gated_threads(WAVES)) void gated_fwd_kernel(const G
     };
     int64_t t = ((int64_t)wave * G + lane) * kLaneSteps;
     fetch(t);
+    // worked out while the first loads are on their way
+    const float rate = p.c * softplus_row(lam) * kLog2e;  // of the exponents of 2
+    const float rb = r_bias * kLog2e, ib = i_bias * kLog2e;
     int turn = 0;
     for (int64_t base = 0; base < p.L; base += kSpan, t += kSpan) {
         const Eight<BF16> cx = nx, cr = nr, ci = ni, cz = nz;
