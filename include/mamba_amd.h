@@ -510,9 +510,9 @@ mamba_status mamba_gated_scan_fwd(const void *x, const void *r, const void *i, c
  *   dlam, dr_bias, di_bias : [D] float, required: sums over batch and steps, in a
  *                          fixed order
  *   dh0                  : [B, D] float, required
- *   workspace            : mamba_gated_scan_bwd_workspace_size(...) bytes, 256-byte
- *                          aligned, for checkpoints given (1) or not (0); scratch as
- *                          in the scan
+ *   workspace            : mamba_gated_scan_bwd_workspace_size(...) bytes (0 for one
+ *                          sequence with checkpoints), 256-byte aligned, for
+ *                          checkpoints given (1) or not (0); scratch as in the scan
  * Where a step keeps everything (v_t = 0), dr_t is zero.  With L = 0 or B = 0 the
  * parameters' gradients are zero, and dh0 = dh_last (or zeros).
  */

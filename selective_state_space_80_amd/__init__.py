@@ -949,15 +949,19 @@ def gated_scan_bwd(x, r, i, lam, dout, r_bias=None, i_bias=None, z=None, h0=None
          "dz": None if z is None else torch.empty_like(x), "dlam": torch.empty_like(lam),
          "dr_bias": torch.empty_like(lam), "di_bias": torch.empty_like(lam),
          "dh0": lam.new_empty((B, D))}
-    need = (lib.mamba_gated_scan_bwd_workspace_size(B, D, L, 0 if checkpoints is None else 1)
-            if workspace is None else 0)
-    workspace, workspace_bytes = _workspace(workspace, need, dev)
+    workspace_bytes = 0
+    if workspace is None:
+        need = lib.mamba_gated_scan_bwd_workspace_size(B, D, L, 0 if checkpoints is None else 1)
+        if need:
+            workspace, workspace_bytes = _workspace(None, need, dev)
+    else:
+        workspace, workspace_bytes = _workspace(workspace, 0, dev)
     st = lib.mamba_gated_scan_bwd(
         x.data_ptr(), r.data_ptr(), i.data_ptr(), lam.data_ptr(), _addr(r_bias), _addr(i_bias),
         _addr(z), _addr(h0), _addr(reset), _addr(checkpoints), dout.data_ptr(), _addr(dh_last),
         g["dx"].data_ptr(), g["dr"].data_ptr(), g["di"].data_ptr(), _addr(g["dz"]),
         g["dlam"].data_ptr(), g["dr_bias"].data_ptr(), g["di_bias"].data_ptr(), g["dh0"].data_ptr(),
-        workspace.data_ptr(), workspace_bytes, B, D, L, c, _io_dtype(x), _raw_stream(x))
+        _addr(workspace), workspace_bytes, B, D, L, c, _io_dtype(x), _raw_stream(x))
     if st:
         _raise(st, "mamba_gated_scan_bwd")
     return g

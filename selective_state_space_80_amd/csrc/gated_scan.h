@@ -30,7 +30,7 @@ struct GatedScanBwdArgs {
     const float *dh_last;           // [B, D] or NULL
     void *dx, *dr, *di, *dz;        // [B, D, L]; dz NULL without z
     float *dlam, *dr_bias, *di_bias, *dh0;  // [D], [D], [D], [B, D]
-    float *partials;                // [3, B, D]
+    float *partials;                // [3, B, D]; unused with B = 1
 };
 hipError_t launch_gated_scan_bwd(const GatedScanBwdArgs &a, hipStream_t s);
 

@@ -18,6 +18,8 @@ constexpr int64_t kMaxGatedRows = int64_t(1) << 24;
 
 int64_t chunks_of(int64_t L) { return (L + mamba::kGatedChunk - 1) / mamba::kGatedChunk; }
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+// Each row's part of the parameters' gradients, where more than one row has some.
+size_t sums_bytes(int64_t B, int64_t D) { return B > 1 ? up256((size_t)(B * D) * 3 * 4) : 0; }
 
 mamba_status gated_sizes(int64_t B, int64_t D, int64_t L, float c)
 {
@@ -101,7 +103,7 @@ size_t mamba_gated_scan_bwd_workspace_size(int64_t B, int64_t D, int64_t L, int 
     if (gated_sizes(B, D, L, 0.f) != MAMBA_OK)
         return 0;
     const size_t rows = (size_t)(B * D);
-    return up256(rows * 3 * 4) + (with_checkpoints ? 0 : up256(rows * (size_t)chunks_of(L) * 4));
+    return sums_bytes(B, D) + (with_checkpoints ? 0 : up256(rows * (size_t)chunks_of(L) * 4));
 }
 
 mamba_status mamba_gated_scan_bwd(const void *x, const void *r, const void *i, const float *lam, const float *r_bias,
@@ -150,7 +152,7 @@ mamba_status mamba_gated_scan_bwd(const void *x, const void *r, const void *i, c
     a.f = mamba::GatedScanArgs{x, r, i, z, lam, r_bias, i_bias, h0, reset, nullptr, nullptr,
                                const_cast<float *>(checkpoints), c, B, D, L, io == MAMBA_BF16};
     if (!checkpoints && rows * L > 0) {  // the forward pass again, for its states alone
-        a.f.checkpoints = (float *)((unsigned char *)workspace + up256(per_row * 3));
+        a.f.checkpoints = (float *)((unsigned char *)workspace + sums_bytes(B, D));
         st = launched(mamba::launch_gated_scan_fwd(a.f, (hipStream_t)stream));
         if (st != MAMBA_OK)
             return st;

@@ -19,6 +19,13 @@
 namespace mamba {
 namespace {
 
+// sigmoid(lam) / softplus(lam), which goes to 1 where both go to 0.
+__device__ __forceinline__ float lam_slope(float lam)
+{
+    const float t = expf(-fabsf(lam)), s = (lam < 0.f ? t : 1.f) / (1.f + t);
+    return lam < -80.f ? 1.f : s / softplus_row(lam);
+}
+
 template <int G, int WAVES, bool BF16, bool GATE, bool RESET>
 __global__ __launch_bounds__(gated_threads(WAVES)) void gated_bwd_kernel(const GatedScanBwdArgs p)
 {
@@ -198,9 +205,15 @@ __global__ __launch_bounds__(gated_threads(WAVES)) void gated_bwd_kernel(const G
         }
     }
     if (live && lane == 0 && wave == 0) {
-        p.partials[row] = sum_q;
-        p.partials[rows + row] = sum_r;
-        p.partials[2 * rows + row] = sum_i;
+        if (p.f.B == 1) {  // a row's sums are its channel's
+            p.dlam[row] = sum_q * lam_slope(lam);
+            p.dr_bias[row] = sum_r;
+            p.di_bias[row] = sum_i;
+        } else {
+            p.partials[row] = sum_q;
+            p.partials[rows + row] = sum_r;
+            p.partials[2 * rows + row] = sum_i;
+        }
     }
 }
 
@@ -216,9 +229,7 @@ __global__ __launch_bounds__(64) void gated_sums_kernel(const GatedScanBwdArgs p
     for (int64_t b = 0; b < p.f.B; ++b)
         sum += from[b * p.f.D];
     if (blockIdx.y == 0) {
-        // sigmoid(lam) / softplus(lam), which goes to 1 where both go to 0
-        const float lam = p.f.lam[d], t = expf(-fabsf(lam)), s = (lam < 0.f ? t : 1.f) / (1.f + t);
-        p.dlam[d] = lam < -80.f ? sum : sum * (s / softplus_row(lam));
+        p.dlam[d] = sum * lam_slope(p.f.lam[d]);
     } else {
         (blockIdx.y == 1 ? p.dr_bias : p.di_bias)[d] = sum;
     }
@@ -275,7 +286,7 @@ hipError_t launch_gated_scan_bwd(const GatedScanBwdArgs &a, hipStream_t s)
             }
         }
     }
-    if (e != hipSuccess)
+    if (e != hipSuccess || a.f.B == 1)
         return e;
     gated_sums_kernel<<<dim3((unsigned)((a.f.D + 63) / 64), 3), dim3(64), 0, s>>>(a);
     return hipGetLastError();

@@ -84,6 +84,7 @@ def test_sizes(lib):
     assert [lib.mamba_gated_scan_checkpoints(L) for L in (-1, 0, 1, 512, 513, 131072)] == [0, 0, 1, 1, 2, 256]
     size = lib.mamba_gated_scan_bwd_workspace_size
     assert size(2, 64, 600, 1) == 1536 and size(2, 64, 600, 0) == 1536 + 1024
+    assert size(1, 64, 600, 1) == 0 and size(1, 64, 600, 0) == 512
     assert size(-1, 64, 600, 1) == 0 and size(1, 1 << 24, 1, 1) == 0
 
 
