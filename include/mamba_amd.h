@@ -490,15 +490,20 @@ mamba_status mamba_int8_matmul_form(int64_t batch, int64_t M, int64_t N, int64_t
  *   h_last        : [B, D] float or NULL (not returned)
  *   checkpoints   : [B, D, mamba_gated_scan_checkpoints(L)] float or NULL: the
  *                   state before steps 0, 512, 1024, ..., for the backward call
+ *   workspace     : mamba_gated_scan_fwd_workspace_size(B, D, L) bytes, 256-byte
+ *                   aligned (0, and none needed, but for few rows of many steps);
+ *                   scratch as in the scan
  * c is finite and not negative.  A step with r = -infinity and a finite x leaves
  * the state as it is: padded tokens.  A state that becomes infinite is NaN from the
  * next step that decays it on.  B * D < 2^24.  With L = 0, h_last = h0 (or zeros).
  */
 int64_t mamba_gated_scan_checkpoints(int64_t L);
+size_t mamba_gated_scan_fwd_workspace_size(int64_t B, int64_t D, int64_t L);
 mamba_status mamba_gated_scan_fwd(const void *x, const void *r, const void *i, const float *lam, const float *r_bias,
                                   const float *i_bias, const void *z, const float *h0, const uint8_t *reset,
-                                  void *y, float *h_last, float *checkpoints, int64_t B, int64_t D, int64_t L,
-                                  float c, mamba_dtype io, void *stream);
+                                  void *y, float *h_last, float *checkpoints, void *workspace,
+                                  size_t workspace_bytes, int64_t B, int64_t D, int64_t L, float c, mamba_dtype io,
+                                  void *stream);
 
 /*
  * Gradients of sum(y * dout) + sum(h_last * dh_last) of mamba_gated_scan_fwd.
@@ -511,7 +516,7 @@ mamba_status mamba_gated_scan_fwd(const void *x, const void *r, const void *i, c
  *                          fixed order
  *   dh0                  : [B, D] float, required
  *   workspace            : mamba_gated_scan_bwd_workspace_size(...) bytes (0 for one
- *                          sequence with checkpoints), 256-byte aligned, for
+ *                          sequence of many channels with checkpoints), 256-byte aligned, for
  *                          checkpoints given (1) or not (0); scratch as in the scan
  * Where a step keeps everything (v_t = 0), dr_t is zero.  With L = 0 or B = 0 the
  * parameters' gradients are zero, and dh0 = dh_last (or zeros).

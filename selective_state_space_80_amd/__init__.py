@@ -31,6 +31,7 @@ Entry points (same names as the C ABI, without the ``mamba_`` prefix):
                  return_last_state=False, return_checkpoints=False, out=None, ...)
   gated_scan_bwd(x, r, i, lam, dout, r_bias=None, i_bias=None, z=None, h0=None, reset=None,
                  dh_last=None, c=8.0, checkpoints=None, workspace=None)
+  gated_scan_fwd_workspace_size(B, D, L)
   gated_scan_bwd_workspace_size(B, D, L, with_checkpoints=True)
   gated_state_update(h, x, r, i, lam, r_bias=None, i_bias=None, z=None, c=8.0, h_out=None, out=None)
   quantize_mxfp4(x, channel_major=False, out=None, scale=None)
@@ -72,7 +73,8 @@ EXPORTED = ["mamba_status_string", "mamba_abi_version", "mamba_conv1d_silu",
             "mamba_selective_scan_fwd_noalloc", "mamba_rms_norm", "mamba_rms_norm_int8",
             "mamba_rms_norm_bwd_workspace_size", "mamba_rms_norm_bwd", "mamba_quantize_int8",
             "mamba_int8_matmul", "mamba_int8_matmul_form",
-            "mamba_gated_scan_checkpoints", "mamba_gated_scan_fwd",
+            "mamba_gated_scan_checkpoints", "mamba_gated_scan_fwd_workspace_size",
+            "mamba_gated_scan_fwd",
             "mamba_gated_scan_bwd_workspace_size", "mamba_gated_scan_bwd",
             "mamba_gated_state_update", "mamba_quantize_mxfp4", "mamba_dequantize_mxfp4",
             "mamba_mxfp4_matmul", "mamba_mxfp4_matmul_form"]
@@ -159,7 +161,9 @@ def load_library(path: str = LIBRARY):
     lib.mamba_gated_scan_checkpoints.restype = I64
     lib.mamba_gated_scan_checkpoints.argtypes = [I64]
     lib.mamba_gated_scan_fwd.restype = I32
-    lib.mamba_gated_scan_fwd.argtypes = [P] * 12 + [I64, I64, I64, F, I32, P]
+    lib.mamba_gated_scan_fwd_workspace_size.restype = SZ
+    lib.mamba_gated_scan_fwd_workspace_size.argtypes = [I64, I64, I64]
+    lib.mamba_gated_scan_fwd.argtypes = [P] * 13 + [SZ, I64, I64, I64, F, I32, P]
     lib.mamba_gated_scan_bwd_workspace_size.restype = SZ
     lib.mamba_gated_scan_bwd_workspace_size.argtypes = [I64, I64, I64, I32]
     lib.mamba_gated_scan_bwd.restype = I32
@@ -886,7 +890,7 @@ def _gated_arguments(x, r, i, lam, r_bias, i_bias, z, h0, reset):
 
 def gated_scan_fwd(x, r, i, lam, r_bias=None, i_bias=None, z=None, h0=None, reset=None, c=8.0,
                    return_last_state=False, return_checkpoints=False, out=None, h_last=None,
-                   checkpoints=None):
+                   checkpoints=None, workspace=None):
     """Gated linear recurrence over [B, D, L]: with v = c softplus(lam) sigmoid(r + r_bias) and
     a = exp(-v), h_t = a_t h_(t-1) + sqrt(1 - a_t^2) sigmoid(i + i_bias) x, y = h or h SiLU(z).
     x, r, i, z [B,D,L] f32/bf16; lam, r_bias, i_bias [D] f32; h0 [B,D] f32; reset [B,L] bool or
@@ -913,15 +917,26 @@ def gated_scan_fwd(x, r, i, lam, r_bias=None, i_bias=None, z=None, h0=None, rese
             checkpoints = lam.new_empty(kept)
         else:
             _check(checkpoints, "checkpoints", kept, f32, x.device)
+    workspace_bytes = 0
+    if workspace is not None:
+        workspace, workspace_bytes = _workspace(workspace, 0, x.device)
+    else:
+        need = lib.mamba_gated_scan_fwd_workspace_size(B, D, L)
+        if need:
+            workspace, workspace_bytes = _workspace(None, need, x.device)
     st = lib.mamba_gated_scan_fwd(x.data_ptr(), r.data_ptr(), i.data_ptr(), lam.data_ptr(),
                                   _addr(r_bias), _addr(i_bias), _addr(z), _addr(h0), _addr(reset),
-                                  out.data_ptr(), _addr(h_last), _addr(checkpoints), B, D, L, c,
-                                  _io_dtype(x), _raw_stream(x))
+                                  out.data_ptr(), _addr(h_last), _addr(checkpoints), _addr(workspace),
+                                  workspace_bytes, B, D, L, c, _io_dtype(x), _raw_stream(x))
     if st:
         _raise(st, "mamba_gated_scan_fwd")
     got = (out,) + ((h_last,) if return_last_state else ()) + (
         (checkpoints,) if return_checkpoints else ())
     return out if len(got) == 1 else got
+
+
+def gated_scan_fwd_workspace_size(B, D, L) -> int:
+    return int(load_library().mamba_gated_scan_fwd_workspace_size(B, D, L))
 
 
 def gated_scan_bwd_workspace_size(B, D, L, with_checkpoints=True) -> int:

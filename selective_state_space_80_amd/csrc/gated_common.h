@@ -274,6 +274,20 @@ template <int G, bool DROPS> __device__ __forceinline__ Span<DROPS> join_behind(
     return G == 64 || in < G - 1 ? e : none;
 }
 
+// The map of a row's parts before this one (lane l holds part l's, or nothing), joined,
+// applied to the state that enters the first.
+template <bool DROPS> __device__ __forceinline__ float through_parts(const float2 *maps, int count, bool from_end, int parts, float s)
+{
+    const int lane = threadIdx.x & 63;
+    Span<DROPS> m{0.f, 0.f};
+    if (lane < count) {
+        const float2 f = maps[from_end ? parts - 1 - lane : lane];
+        m = Span<DROPS>{f.x, f.y};
+    }
+    join_before<64, DROPS>(m);
+    return read_span(m, 63).of(s);
+}
+
 // Threads of a workgroup: one row where several waves share it, which meet in LDS.
 constexpr int gated_threads(int waves) { return waves == 1 ? 256 : 64 * waves; }
 

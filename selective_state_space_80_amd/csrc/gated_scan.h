@@ -21,7 +21,19 @@ struct GatedScanArgs {
     float c;
     int64_t B, D, L;
     bool bf16;
+    // rows split into parts (gated_parts), whose maps are worked out first
+    float2 *maps;        // [B, D, parts]
+    int64_t part_steps;
+    int parts;
 };
+
+// Few rows of many steps: parts of a row that different workgroups take, at most 64
+// (a wave joins their maps), each of whole chunks.  One part: no split.
+struct GatedParts {
+    int parts;
+    int64_t steps;  // of a part
+};
+GatedParts gated_parts(int64_t rows, int64_t L);
 hipError_t launch_gated_scan_fwd(const GatedScanArgs &a, hipStream_t s);
 
 struct GatedScanBwdArgs {
@@ -30,7 +42,7 @@ struct GatedScanBwdArgs {
     const float *dh_last;           // [B, D] or NULL
     void *dx, *dr, *di, *dz;        // [B, D, L]; dz NULL without z
     float *dlam, *dr_bias, *di_bias, *dh0;  // [D], [D], [D], [B, D]
-    float *partials;                // [3, B, D]; unused with B = 1
+    float *partials;                // [3, parts, B, D]; unused with one row a channel
 };
 hipError_t launch_gated_scan_bwd(const GatedScanBwdArgs &a, hipStream_t s);
 

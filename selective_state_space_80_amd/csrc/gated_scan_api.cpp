@@ -18,8 +18,18 @@ constexpr int64_t kMaxGatedRows = int64_t(1) << 24;
 
 int64_t chunks_of(int64_t L) { return (L + mamba::kGatedChunk - 1) / mamba::kGatedChunk; }
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
-// Each row's part of the parameters' gradients, where more than one row has some.
-size_t sums_bytes(int64_t B, int64_t D) { return B > 1 ? up256((size_t)(B * D) * 3 * 4) : 0; }
+// Maps of the parts that rows are split into.
+size_t maps_bytes(int64_t B, int64_t D, int64_t L)
+{
+    const int parts = mamba::gated_parts(B * D, L).parts;
+    return parts > 1 ? up256((size_t)(B * D * parts) * sizeof(float2)) : 0;
+}
+// Each row's and part's share of the parameters' gradients, where a channel has several.
+size_t sums_bytes(int64_t B, int64_t D, int64_t L)
+{
+    const int parts = mamba::gated_parts(B * D, L).parts;
+    return B * parts > 1 ? up256((size_t)(B * D * parts) * 3 * 4) : 0;
+}
 
 mamba_status gated_sizes(int64_t B, int64_t D, int64_t L, float c)
 {
@@ -62,10 +72,16 @@ extern "C" {
 
 int64_t mamba_gated_scan_checkpoints(int64_t L) { return L > 0 && L <= kMaxElems ? chunks_of(L) : 0; }
 
+size_t mamba_gated_scan_fwd_workspace_size(int64_t B, int64_t D, int64_t L)
+{
+    return gated_sizes(B, D, L, 0.f) == MAMBA_OK ? maps_bytes(B, D, L) : 0;
+}
+
 mamba_status mamba_gated_scan_fwd(const void *x, const void *r, const void *i, const float *lam, const float *r_bias,
                                   const float *i_bias, const void *z, const float *h0, const uint8_t *reset,
-                                  void *y, float *h_last, float *checkpoints, int64_t B, int64_t D, int64_t L,
-                                  float c, mamba_dtype io, void *stream)
+                                  void *y, float *h_last, float *checkpoints, void *workspace,
+                                  size_t workspace_bytes, int64_t B, int64_t D, int64_t L, float c, mamba_dtype io,
+                                  void *stream)
 {
     if (!valid_dtype(io))
         return MAMBA_ERR_DTYPE;
@@ -82,19 +98,23 @@ mamba_status mamba_gated_scan_fwd(const void *x, const void *r, const void *i, c
     if (!inputs_aligned(in, es) || !aligned(h0, 4) || !aligned(y, es) || !aligned(h_last, 4) ||
         !aligned(checkpoints, 4))
         return MAMBA_ERR_ALIGN;
+    const size_t need = maps_bytes(B, D, L);
+    if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+        return MAMBA_ERR_WORKSPACE;
     const Range ins[] = {rng(x, n), rng(r, n), rng(i, n), optional(z, n), rng(lam, per_d), optional(r_bias, per_d),
                          optional(i_bias, per_d), optional(h0, (size_t)rows * 4),
                          optional(reset, (size_t)(B * L))};
     const Range outs[] = {rng(y, n), optional(h_last, (size_t)rows * 4),
-                          optional(checkpoints, (size_t)(rows * chunks_of(L)) * 4)};
-    mamba_status st = apart(outs, 3, ins, 9);
+                          optional(checkpoints, (size_t)(rows * chunks_of(L)) * 4), rng(workspace, need)};
+    mamba_status st = apart(outs, 4, ins, 9);
     if (st != MAMBA_OK)
         return st;
     st = device_ok();
     if (st != MAMBA_OK)
         return st;
+    const mamba::GatedParts split = mamba::gated_parts(rows, L);
     mamba::GatedScanArgs a{x, r, i, z, lam, r_bias, i_bias, h0, reset, y, h_last, checkpoints,
-                           c, B, D, L, io == MAMBA_BF16};
+                           c, B, D, L, io == MAMBA_BF16, (float2 *)workspace, split.steps, split.parts};
     return launched(mamba::launch_gated_scan_fwd(a, (hipStream_t)stream));
 }
 
@@ -103,7 +123,7 @@ size_t mamba_gated_scan_bwd_workspace_size(int64_t B, int64_t D, int64_t L, int 
     if (gated_sizes(B, D, L, 0.f) != MAMBA_OK)
         return 0;
     const size_t rows = (size_t)(B * D);
-    return sums_bytes(B, D) + (with_checkpoints ? 0 : up256(rows * (size_t)chunks_of(L) * 4));
+    return sums_bytes(B, D, L) + maps_bytes(B, D, L) + (with_checkpoints ? 0 : up256(rows * (size_t)chunks_of(L) * 4));
 }
 
 mamba_status mamba_gated_scan_bwd(const void *x, const void *r, const void *i, const float *lam, const float *r_bias,
@@ -149,10 +169,13 @@ mamba_status mamba_gated_scan_bwd(const void *x, const void *r, const void *i, c
     if (st != MAMBA_OK)
         return st;
     mamba::GatedScanBwdArgs a{};
+    const mamba::GatedParts split = mamba::gated_parts(rows, L);
+    unsigned char *ws = (unsigned char *)workspace, *maps = ws + sums_bytes(B, D, L);
     a.f = mamba::GatedScanArgs{x, r, i, z, lam, r_bias, i_bias, h0, reset, nullptr, nullptr,
-                               const_cast<float *>(checkpoints), c, B, D, L, io == MAMBA_BF16};
+                               const_cast<float *>(checkpoints), c, B, D, L, io == MAMBA_BF16, (float2 *)maps,
+                               split.steps, split.parts};
     if (!checkpoints && rows * L > 0) {  // the forward pass again, for its states alone
-        a.f.checkpoints = (float *)((unsigned char *)workspace + sums_bytes(B, D));
+        a.f.checkpoints = (float *)(maps + maps_bytes(B, D, L));
         st = launched(mamba::launch_gated_scan_fwd(a.f, (hipStream_t)stream));
         if (st != MAMBA_OK)
             return st;

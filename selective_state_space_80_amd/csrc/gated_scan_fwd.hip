@@ -4,7 +4,12 @@
 // from chunk to chunk of 512 steps.  Each lane joins its steps to one affine map, the
 // wave joins its lanes' maps by DPP, and every lane then runs its steps again from the
 // state that enters them.  WAVES waves of a workgroup take consecutive chunks of one
-// row, where rows are few.
+// row, where rows are few; where they are fewer than fill the CUs so, a row is split
+// into parts for different workgroups, whose maps a first kernel works out.
+//
+// What bounds it is memory, with the vector unit close behind (about 40 issue slots an
+// element, six of them transcendental at two slots): 8 x 5120 x 2048 bf16 129 us, 5.2
+// TB/s, gated 161, where a large copy moves 5.1 to 5.4 and the slots take 86 and 100.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -15,7 +20,32 @@
 namespace mamba {
 namespace {
 
-template <int G, int WAVES, bool BF16, bool GATE, bool RESET>
+// What a lane's eight steps come to, from its inputs as they lie in memory.
+template <bool BF16, bool RESET>
+__device__ __forceinline__ Span<RESET> lane_steps(const Eight<BF16> &x, const Eight<BF16> &r, const Eight<BF16> &i,
+                                                  uint32_t first, float rate, float rb, float ib,
+                                                  float (&a)[kLaneSteps], float (&b)[kLaneSteps])
+{
+    float sum = 0.f, h = 0.f;
+    bool dropped = false;
+#pragma unroll
+    for (int j = 0; j < kLaneSteps; ++j) {
+        const float u = rate * sigmoid_log2(r.get(j), rb);
+        const float in = sigmoid_log2(i.get(j), ib) * x.get(j);
+        a[j] = hw_exp2(-u);
+        const float e = loss_of(u, a[j]);
+        b[j] = __builtin_amdgcn_sqrtf(e * (2.f - e)) * in;
+        sum += u;
+        h = fmaf(a[j], h, b[j]);
+        if (RESET && (first >> j & 1)) {
+            h = b[j] = in;
+            dropped = true;
+        }
+    }
+    return {RESET && dropped ? __builtin_inff() : sum, h};
+}
+
+template <int G, int WAVES, bool BF16, bool GATE, bool RESET, bool PARTS>
 __global__ __launch_bounds__(gated_threads(WAVES)) void gated_fwd_kernel(const GatedScanArgs p)
 {
     using T = typename Elem<BF16>::T;
@@ -26,7 +56,9 @@ __global__ __launch_bounds__(gated_threads(WAVES)) void gated_fwd_kernel(const G
     const int lane = threadIdx.x & (G - 1), wave = threadIdx.x / G % WAVES;
     const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / (G * WAVES);
     const bool live = row < p.B * p.D;  // the others' lanes run along, with nothing to load or store
-    const int64_t at = live ? row : 0, L = live ? p.L : 0;
+    const int64_t from = PARTS ? blockIdx.y * p.part_steps : 0;
+    const int64_t stop = PARTS && from + p.part_steps < p.L ? from + p.part_steps : p.L;
+    const int64_t at = live ? row : 0, L = live ? stop : 0;
     const uint32_t d = (uint32_t)at % (uint32_t)p.D;  // rows are below 2^24
     const T *x = (const T *)p.x + at * p.L, *r = (const T *)p.r + at * p.L, *i = (const T *)p.i + at * p.L;
     const T *z = GATE ? (const T *)p.z + at * p.L : nullptr;
@@ -35,6 +67,8 @@ __global__ __launch_bounds__(gated_threads(WAVES)) void gated_fwd_kernel(const G
     const float lam = p.lam[d], r_bias = p.r_bias ? p.r_bias[d] : 0.f, i_bias = p.i_bias ? p.i_bias[d] : 0.f;
     const int64_t chunks = (p.L + kGatedChunk - 1) / kGatedChunk;
     float carry = p.h0 ? p.h0[at] : 0.f;
+    if constexpr (PARTS)
+        carry = through_parts<RESET>(p.maps + at * p.parts, blockIdx.y, false, p.parts, carry);
 
     Eight<BF16> nx, nr, ni, nz;
     uint32_t nreset = 0;
@@ -48,34 +82,19 @@ __global__ __launch_bounds__(gated_threads(WAVES)) void gated_fwd_kernel(const G
         if constexpr (RESET)
             nreset = load_resets(reset + t, n);
     };
-    int64_t t = ((int64_t)wave * G + lane) * kLaneSteps;
+    int64_t t = from + ((int64_t)wave * G + lane) * kLaneSteps;
     fetch(t);
     // worked out while the first loads are on their way
     const float rate = p.c * softplus_row(lam) * kLog2e;  // of the exponents of 2
     const float rb = r_bias * kLog2e, ib = i_bias * kLog2e;
     int turn = 0;
-    for (int64_t base = 0; base < p.L; base += kSpan, t += kSpan) {
+    for (int64_t base = from; base < stop; base += kSpan, t += kSpan) {
         const Eight<BF16> cx = nx, cr = nr, ci = ni, cz = nz;
         const uint32_t first = nreset;
-        if (base + kSpan < p.L)
+        if (base + kSpan < stop)
             fetch(t + kSpan);
-        float a[kLaneSteps], b[kLaneSteps], sum = 0.f, h = 0.f;
-        bool dropped = false;
-#pragma unroll
-        for (int j = 0; j < kLaneSteps; ++j) {
-            const float u = rate * sigmoid_log2(cr.get(j), rb);
-            const float in = sigmoid_log2(ci.get(j), ib) * cx.get(j);
-            a[j] = hw_exp2(-u);
-            const float e = loss_of(u, a[j]);
-            b[j] = __builtin_amdgcn_sqrtf(e * (2.f - e)) * in;
-            sum += u;
-            h = fmaf(a[j], h, b[j]);
-            if (RESET && (first >> j & 1)) {
-                h = b[j] = in;
-                dropped = true;
-            }
-        }
-        M m{RESET && dropped ? __builtin_inff() : sum, h};
+        float a[kLaneSteps], b[kLaneSteps];
+        M m = lane_steps<BF16, RESET>(cx, cr, ci, first, rate, rb, ib, a, b);
         const M before = join_before<G, RESET>(m);
         float enter = carry;
         if constexpr (WAVES > 1) {
@@ -95,7 +114,7 @@ __global__ __launch_bounds__(gated_threads(WAVES)) void gated_fwd_kernel(const G
         }
         if (p.checkpoints && lane == 0 && t < L)
             p.checkpoints[at * chunks + t / kGatedChunk] = enter;
-        h = before.of(enter);
+        float h = before.of(enter);
         float out[kLaneSteps];
 #pragma unroll
         for (int j = 0; j < kLaneSteps; ++j) {
@@ -107,19 +126,62 @@ __global__ __launch_bounds__(gated_threads(WAVES)) void gated_fwd_kernel(const G
         if (p.y)
             Eight<BF16>::store(y + t, out, steps_left(L, t));
         // the steps past the end have left the state as it was
-        if (p.h_last && live && base + kSpan >= p.L && lane == G - 1 && wave == WAVES - 1)
+        if (p.h_last && live && base + kSpan >= p.L && stop == p.L && lane == G - 1 && wave == WAVES - 1)
             p.h_last[row] = h;
     }
     if (p.L == 0 && p.h_last && live && lane == 0 && wave == 0)
         p.h_last[row] = carry;
 }
 
-template <int G, int WAVES> hipError_t launch(const GatedScanArgs &a, hipStream_t s)
+// The maps of a row's parts but the last, a wave each.
+template <bool BF16, bool RESET> __global__ __launch_bounds__(256) void gated_maps_kernel(const GatedScanArgs p)
+{
+    using T = typename Elem<BF16>::T;
+    constexpr int kSpan = 64 * kLaneSteps;
+    const int lane = threadIdx.x & 63;
+    const int64_t at = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
+    if (at >= p.B * p.D)
+        return;
+    const uint32_t d = (uint32_t)at % (uint32_t)p.D;
+    const T *x = (const T *)p.x + at * p.L, *r = (const T *)p.r + at * p.L, *i = (const T *)p.i + at * p.L;
+    const uint8_t *reset = RESET ? p.reset + (int64_t)((uint32_t)at / (uint32_t)p.D) * p.L : nullptr;
+    const float rate = p.c * softplus_row(p.lam[d]) * kLog2e;
+    const float rb = p.r_bias ? p.r_bias[d] * kLog2e : 0.f, ib = p.i_bias ? p.i_bias[d] * kLog2e : 0.f;
+    const int64_t from = blockIdx.y * p.part_steps;  // whole chunks, and none of them a row's last
+    const int64_t stop = from + p.part_steps;
+    Span<RESET> all{0.f, 0.f};
+    Eight<BF16> nx, nr, ni;
+    uint32_t nreset = 0;
+    auto fetch = [&](int64_t t) {
+        nr.load(r + t);
+        nx.load(x + t);
+        ni.load(i + t);
+        if constexpr (RESET)
+            nreset = load_resets(reset + t, kLaneSteps);
+    };
+    fetch(from + lane * kLaneSteps);
+    for (int64_t base = from; base < stop; base += kSpan) {
+        const Eight<BF16> cx = nx, cr = nr, ci = ni;
+        const uint32_t first = nreset;
+        if (base + kSpan < stop)
+            fetch(base + kSpan + lane * kLaneSteps);
+        float a[kLaneSteps], b[kLaneSteps];
+        Span<RESET> m = lane_steps<BF16, RESET>(cx, cr, ci, first, rate, rb, ib, a, b);
+        join_before<64, RESET>(m);
+        Span<RESET> chunk = read_span(m, 63);
+        chunk.after(all);
+        all = chunk;
+    }
+    if (lane == 0)
+        p.maps[at * p.parts + blockIdx.y] = float2{all.U, all.S};
+}
+
+template <int G, int WAVES, bool PARTS = false> hipError_t launch(const GatedScanArgs &a, hipStream_t s)
 {
     constexpr int kRows = gated_threads(WAVES) / G / WAVES;
-    const dim3 grid((unsigned)((a.B * a.D + kRows - 1) / kRows)), block(gated_threads(WAVES));
+    const dim3 grid((unsigned)((a.B * a.D + kRows - 1) / kRows), PARTS ? a.parts : 1), block(gated_threads(WAVES));
     auto with = [&](auto bf16, auto gate, auto reset) {
-        gated_fwd_kernel<G, WAVES, bf16, gate, reset><<<grid, block, 0, s>>>(a);
+        gated_fwd_kernel<G, WAVES, bf16, gate, reset, PARTS><<<grid, block, 0, s>>>(a);
     };
     auto on_reset = [&](auto bf16, auto gate) {
         if (a.reset)
@@ -226,6 +288,23 @@ template <int EACH> hipError_t launch_step(const GatedStepArgs &a, hipStream_t s
 
 }  // namespace
 
+// The inputs are then read twice, the second time mostly from the caches.  Both sides
+// measured, with eight or sixteen waves of one workgroup a row and in parts (us):
+//   1 x 64 x 131072 bf16         55 and 32, backward 85 and 46
+//   1 x 32 x 131072 fp32         59 and 29, backward 100 and 43
+//   1 x 128 x 131072 bf16, gated 64 and 57, backward 105 and 92 (129 rows, 128 rows)
+GatedParts gated_parts(int64_t rows, int64_t L)
+{
+    const int64_t chunks = (L + kGatedChunk - 1) / kGatedChunk;
+    if (rows == 0 || rows > 128 || chunks < 32)
+        return {1, L};
+    // about 4096 waves in all, four chunks a part or more
+    int64_t parts = 4096 / rows < chunks / 4 ? 4096 / rows : chunks / 4;
+    parts = parts < 64 ? parts : 64;
+    const int64_t each = (chunks + parts - 1) / parts;
+    return {(int)((chunks + each - 1) / each), each * kGatedChunk};
+}
+
 // Waves of a row, both sides measured (us, inputs from memory):
 //   8 x 5120 x 2048 bf16, gated  one 162, two 187, four 182
 //   2 x 1536 x 8192 fp32         one 81.6, four 79.3, eight 79.5, 16 92.5
@@ -240,6 +319,19 @@ hipError_t launch_gated_scan_fwd(const GatedScanArgs &a, hipStream_t s)
     case 32: return launch<32, 1>(a, s);
     }
     const int64_t rows = a.B * a.D;
+    if (a.parts > 1) {
+        const dim3 grid((unsigned)((rows + 3) / 4), a.parts - 1), block(256);
+        if (a.bf16 && a.reset)
+            gated_maps_kernel<true, true><<<grid, block, 0, s>>>(a);
+        else if (a.bf16)
+            gated_maps_kernel<true, false><<<grid, block, 0, s>>>(a);
+        else if (a.reset)
+            gated_maps_kernel<false, true><<<grid, block, 0, s>>>(a);
+        else
+            gated_maps_kernel<false, false><<<grid, block, 0, s>>>(a);
+        const hipError_t e = hipGetLastError();
+        return e == hipSuccess ? launch<64, 1, true>(a, s) : e;
+    }
     switch (gated_waves(rows, a.L, 4, rows <= 256 ? 16 : 8)) {
     case 1: return launch<64, 1>(a, s);
     case 2: return launch<64, 2>(a, s);

@@ -26,7 +26,7 @@ X, R, I, LAM, RB, IB, Z, H0, RESET, Y, HL, CK, DO, DHL, DX, DR, DI, DZ, DLAM, DR
 
 
 def fwd(lib, **kw):
-    a = dict(x=X, r=R, i=I, lam=LAM, rb=RB, ib=IB, z=Z, h0=H0, reset=RESET, y=Y, hl=HL, ck=CK, B=2, D=64, L=600, c=8.0,
+    a = dict(x=X, r=R, i=I, lam=LAM, rb=RB, ib=IB, z=Z, h0=H0, reset=RESET, y=Y, hl=HL, ck=CK, ws=WS, nws=1 << 20, B=2, D=64, L=600, c=8.0,
              io=BF16, stream=None)
     a.update(kw)
     return lib.mamba_gated_scan_fwd(*a.values())
@@ -55,7 +55,9 @@ COMMON = [(dict(io=2), EDTYPE), (dict(B=-1), ESHAPE), (dict(D=-1), ESHAPE), (dic
     (dict(L=-1), ESHAPE), (dict(D=1 << 23), ESHAPE), (dict(L=1 << 39), ESHAPE), (dict(y=None), ENULL), (dict(y=_p(10, 1)), EALIGN),
     (dict(hl=_p(11, 2)), EALIGN), (dict(ck=_p(12, 2)), EALIGN), (dict(y=X), EALIAS), (dict(y=Z), EALIAS), (dict(y=RESET), EALIAS),
     (dict(hl=H0), EALIAS), (dict(hl=Y), EALIAS), (dict(ck=HL), EALIAS), (dict(ck=LAM), EALIAS), (dict(y=RB), EALIAS),
-    (dict(y=_p(1, 2 * 64 * 600 * 2 - 2)), EALIAS), (dict(B=0), OK), (dict(D=0), OK), (dict(L=0, hl=None), OK)])
+    (dict(y=_p(1, 2 * 64 * 600 * 2 - 2)), EALIAS), (dict(B=0), OK), (dict(D=0), OK), (dict(L=0, hl=None), OK),
+    (dict(L=50000, ws=None), EWS), (dict(L=50000, nws=1024), EWS), (dict(L=50000, ws=_p(23, 128)), EWS),
+    (dict(L=50000, ws=X), EALIAS), (dict(L=50000, ws=Y), EALIAS)])
 def test_forward_rejects(lib, kw, want):
     assert fwd(lib, **kw) == want
 
@@ -85,6 +87,9 @@ def test_sizes(lib):
     size = lib.mamba_gated_scan_bwd_workspace_size
     assert size(2, 64, 600, 1) == 1536 and size(2, 64, 600, 0) == 1536 + 1024
     assert size(1, 64, 600, 1) == 0 and size(1, 64, 600, 0) == 512
+    assert size(1, 64, 50000, 1) == 20 * 64 * 12 + 20 * 64 * 8  # 98 chunks in 20 parts of five
+    assert lib.mamba_gated_scan_fwd_workspace_size(1, 64, 50000) == 20 * 64 * 8
+    assert lib.mamba_gated_scan_fwd_workspace_size(3, 64, 50000) == 0 and lib.mamba_gated_scan_fwd_workspace_size(1, 64, 15872) == 0
     assert size(-1, 64, 600, 1) == 0 and size(1, 1 << 24, 1, 1) == 0
 
 

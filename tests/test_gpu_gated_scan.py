@@ -258,20 +258,59 @@ def test_offsets_past_32_bits():
 
 
 @pytest.mark.parametrize("io", [F32, BF16])
-@pytest.mark.parametrize("L", [3600, 8200, 17000, 33000])
+@pytest.mark.parametrize("L", [3600, 8200, 15872])
 def test_waves_that_share_a_row(io, L):
-    """Two, four, eight and sixteen waves a row, the last round of chunks not full."""
+    """Two and four waves a row, the last round of chunks not full."""
     say(f"gated scan L={L} {io}")
     _check_both(C.make(1, 3, L, io, seed=L, gate=io == BF16, reset=1e-3 if L % 16 else 0.0), seed=L + 1)
 
 
-def test_many_rows_of_many_chunks():
-    """Eight waves a row, rows in more than one workgroup a CU."""
-    p = C.make(1, 600, 20000, F32, seed=40, gate=False)
+@pytest.mark.parametrize("io", [F32, BF16])
+@pytest.mark.parametrize("B,D,L,reset", [(1, 3, 15873, 0.0), (2, 2, 16400, 1e-3), (1, 5, 40000, 1e-4), (1, 1, 70001, 0.0)])
+def test_rows_in_parts(io, B, D, L, reset):
+    """Few rows of many steps: parts of a row on different workgroups, joined by their maps."""
+    assert _mamba().gated_scan_fwd_workspace_size(B, D, L) > 0
+    say(f"gated scan in parts {B} x {D} x {L} {io}")
+    p = C.make(B, D, L, io, seed=L, gate=io == F32, reset=reset, decay=(0.99, 0.99999))
+    _check_both(p, seed=L + 1)
+    q = C.gradient_inputs(p, 3)
+    a = _backward(p, q, checkpoints=_forward(p, return_checkpoints=True)[1])
+    b = _backward(p, q)
+    assert all(torch.equal(a[n], b[n]) for n in GRADS if a[n] is not None)
+
+
+def test_parts_keep_sequences_apart():
+    """NaN of one packed sequence, in the parts' maps and in the state that enters the row."""
+    L, lo, hi = 30000, 9001, 20003
+    p = C.make(1, 2, L, F32, seed=50)
+    q = C.gradient_inputs(p, 51)
+    p["reset"] = torch.zeros(1, L, dtype=torch.bool)
+    p["reset"][0, [0, lo, hi]] = True
+    p["h0"][:] = torch.nan
+    clean = {k: (v.clone() if v is not None else None) for k, v in p.items()}
+    p["x"][0, 0, lo + 5] = torch.nan
+    p["r"][0, 1, hi - 7000] = torch.nan
+    y, h_last, kept = _forward(p, return_last_state=True, return_checkpoints=True)
+    got = _backward(p, q, checkpoints=kept)
+    y0, last0, kept0 = _forward(clean, return_last_state=True, return_checkpoints=True)
+    got0 = _backward(clean, q, checkpoints=kept0)
+    outside = torch.ones(L, dtype=torch.bool)
+    outside[lo:hi] = False
+    assert torch.isfinite(y0).all() and torch.isnan(y[0, 0, lo + 5:hi]).all()
+    assert torch.equal(y[..., outside], y0[..., outside]) and torch.equal(h_last, last0)
+    for name in ("dx", "dr", "di", "dz"):
+        assert torch.equal(got[name][..., outside], got0[name][..., outside]), name
+
+
+@pytest.mark.parametrize("D,L", [(600, 20000), (200, 33000), (130, 9000)])
+def test_many_rows_of_many_chunks(D, L):
+    """Eight, sixteen and four waves a row, rows in more than one workgroup a CU."""
+    assert _mamba().gated_scan_fwd_workspace_size(1, D, L) == 0
+    p = C.make(1, D, L, F32, seed=40, gate=False)
     q = C.gradient_inputs(p, 41)
     y, kept = _forward(p, return_checkpoints=True)
     got = _backward(p, q, checkpoints=kept)
-    rows = [0, 1, 255, 256, 299, 599]
+    rows = [0, 1, 63, 64, 99, D - 1]
     some = {k: (None if v is None else (v[:, rows].contiguous() if v.dim() > 1 else v[rows])) for k, v in p.items()}
     sq = {k: v[:, rows].contiguous() for k, v in q.items()}
     f, want = C.forward(some), C.backward(some, sq)
