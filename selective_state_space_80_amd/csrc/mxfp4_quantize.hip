@@ -204,8 +204,8 @@ template <bool BF16> __global__ __launch_bounds__(512) void quantize_channel_ker
 
 // ---- back ------------------------------------------------------------------------------
 // A lane takes what it stores in 16 bytes, 8 elements (bf16) or 4, so that a wave's store
-// is one piece (with 8 in fp32 it was two half-empty ones: 8 x 2048 x 5120 123 us), of
-// several rows.  The product with the power of two is exact but where it leaves the range
+// is one piece, of several rows, and stores it past the caches (8 x 2048 x 5120 in fp32:
+// 55 us; by the caches 102, with 8 elements a lane and two half-empty stores 123; bf16 31).  The product with the power of two is exact but where it leaves the range
 // of the type.
 template <int ROWS, bool BF16> __global__ __launch_bounds__(256) void dequantize_kernel(const MxDequantArgs p)
 {
@@ -248,9 +248,11 @@ template <int ROWS, bool BF16> __global__ __launch_bounds__(256) void dequantize
         if (k + kEach <= p.K) {
             if constexpr (BF16) {
                 const u32x4 b = {cvt2(f[0], f[1]), cvt2(f[2], f[3]), cvt2(f[4], f[5]), cvt2(f[6], f[7])};
-                __builtin_memcpy(o, &b, 16);
+                typedef u32x4 __attribute__((aligned(2))) loose;
+                __builtin_nontemporal_store(b, (loose *)o);
             } else {
-                __builtin_memcpy(o, f, 16);
+                typedef f32x4 __attribute__((aligned(4))) loose;
+                __builtin_nontemporal_store(f32x4{f[0], f[1], f[2], f[3]}, (loose *)o);
             }
         } else {
 #pragma unroll
