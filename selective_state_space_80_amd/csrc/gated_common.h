@@ -44,10 +44,10 @@ template <> struct Eight<true> {
     // wave's whole piece of 1024 bytes gains from (8 x 5120 x 2048 forward 130 -> 125 us,
     // backward 232 -> 221; fp32's two stores of half lines lose, 1 x 1536 x 131072
     // backward 1084 -> 1251).
-    static __device__ __forceinline__ void store(uint16_t *p, const float (&f)[kLaneSteps], int n)
+    static __device__ __forceinline__ void store(uint16_t *p, const float (&f)[kLaneSteps], bool whole, int n)
     {
         const gated_u32x4 w = {cvt2(f[0], f[1]), cvt2(f[2], f[3]), cvt2(f[4], f[5]), cvt2(f[6], f[7])};
-        if (n >= kLaneSteps) {
+        if (whole || n >= kLaneSteps) {
             typedef gated_u32x4 __attribute__((aligned(2))) loose;
             __builtin_nontemporal_store(w, (loose *)p);
         } else {
@@ -69,9 +69,9 @@ template <> struct Eight<false> {
     }
     __device__ __forceinline__ float raw(int j) const { return get(j); }
     __device__ __forceinline__ void set_raw(int j, float f) { v[j >> 2][j & 3] = f; }
-    static __device__ __forceinline__ void store(float *p, const float (&f)[kLaneSteps], int n)
+    static __device__ __forceinline__ void store(float *p, const float (&f)[kLaneSteps], bool whole, int n)
     {
-        if (n >= kLaneSteps) {
+        if (whole || n >= kLaneSteps) {
             __builtin_memcpy(p, f, 32);
         } else {
 #pragma unroll
@@ -82,21 +82,33 @@ template <> struct Eight<false> {
     }
 };
 
-// Of a lane's eight steps from t on, those before L.
-__device__ __forceinline__ int steps_left(int64_t L, int64_t t)
+// Steps of a group's 8 G from `from` on that lie before L.
+template <int G> __device__ __forceinline__ int steps_left(int64_t L, int64_t from)
 {
-    const int64_t left = L - t;
-    return left <= 0 ? 0 : (left < kLaneSteps ? (int)left : kLaneSteps);
+    const int64_t left = L - from;
+    return left <= 0 ? 0 : (left < G * kLaneSteps ? (int)left : G * kLaneSteps);
+}
+// A lane's share of them: its eight start at `off`.
+__device__ __forceinline__ int lane_share(int left, uint32_t off)
+{
+    const int n = left - (int)off;
+    return n <= 0 ? 0 : (n < kLaneSteps ? n : kLaneSteps);
+}
+// The same for every lane of a wave, which then takes what hangs on it by scalar means.
+template <bool WHOLE_WAVE> __device__ __forceinline__ int uniform(int v)
+{
+    return WHOLE_WAVE ? __builtin_amdgcn_readfirstlane(v) : v;
 }
 
-// The first n (at most 8) elements from p on; the others are `rest`.  At a row's end
+// The first n (at most 8) elements from p on; the others are `rest`.  whole: every lane
+// of the wave has all eight.  At a row's end
 // the elements are loaded one by one, but all at once: those past the end repeat the
 // last (with a branch for each, a row's end cost as many round trips to memory:
 // 8 x 5120 x 300 bf16 56 us).
 template <bool BF16>
-__device__ __forceinline__ void load_some(Eight<BF16> &to, const typename Elem<BF16>::T *p, int n, float rest)
+__device__ __forceinline__ void load_some(Eight<BF16> &to, const typename Elem<BF16>::T *p, bool whole, int n, float rest)
 {
-    if (n >= kLaneSteps) {
+    if (whole || n >= kLaneSteps) {
         to.load(p);
         return;
     }
@@ -113,10 +125,10 @@ __device__ __forceinline__ void load_some(Eight<BF16> &to, const typename Elem<B
 }
 
 // Bit j: step j of the lane's starts a sequence.
-__device__ __forceinline__ uint32_t load_resets(const uint8_t *p, int n)
+__device__ __forceinline__ uint32_t load_resets(const uint8_t *p, bool whole, int n)
 {
     uint32_t bits = 0;
-    if (n >= kLaneSteps) {
+    if (whole || n >= kLaneSteps) {
         uint32_t w[2];
         __builtin_memcpy(w, p, 8);
 #pragma unroll

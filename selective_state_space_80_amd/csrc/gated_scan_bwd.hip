@@ -36,9 +36,8 @@ __global__ __launch_bounds__(gated_threads(WAVES)) void gated_bwd_kernel(const G
     constexpr int kSpan = G * kLaneSteps * WAVES;
     __shared__ float2 maps[2][WAVES];
     __shared__ float sums[3][WAVES];
-    const int lane = threadIdx.x & (G - 1), wave = threadIdx.x / G % WAVES;
-    const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / (G * WAVES);
-    const int64_t rows = p.f.B * p.f.D;
+    const int lane = threadIdx.x & (G - 1), wave = uniform<G == 64>(threadIdx.x / G % WAVES);
+    const int rows = (int)(p.f.B * p.f.D), row = uniform<G == 64>(blockIdx.x * kRows + threadIdx.x / (G * WAVES));
     const bool live = row < rows;
     const int64_t start = PARTS ? blockIdx.y * p.f.part_steps : 0;
     const int64_t stop = PARTS && start + p.f.part_steps < p.f.L ? start + p.f.part_steps : p.f.L;
@@ -59,21 +58,23 @@ __global__ __launch_bounds__(gated_threads(WAVES)) void gated_bwd_kernel(const G
     Eight<BF16> nx, nr, ni, nz, nd;
     uint32_t nreset = 0;
     float nstate = 0.f;
+    const uint32_t off = lane * kLaneSteps;
     auto fetch = [&](int64_t t) {
-        const int n = steps_left(L, t);
-        load_some<BF16>(nr, r + t, n, -__builtin_inff());  // past the end: steps that change nothing
-        load_some<BF16>(nx, x + t, n, 0.f);
-        load_some<BF16>(ni, i + t, n, 0.f);
-        load_some<BF16>(nd, dout + t, n, 0.f);
+        const int left = steps_left<G>(L, t), n = lane_share(left, off);
+        const bool whole = G == 64 && left == G * kLaneSteps;
+        load_some<BF16>(nr, r + t + off, whole, n, -__builtin_inff());  // past the end: steps that change nothing
+        load_some<BF16>(nx, x + t + off, whole, n, 0.f);
+        load_some<BF16>(ni, i + t + off, whole, n, 0.f);
+        load_some<BF16>(nd, dout + t + off, whole, n, 0.f);
         if constexpr (GATE)
-            load_some<BF16>(nz, z + t, n, 0.f);
+            load_some<BF16>(nz, z + t + off, whole, n, 0.f);
         if constexpr (RESET)
-            nreset = load_resets(reset + t, n);
+            nreset = load_resets(reset + t + off, whole, n);
         const int64_t chunk = t / kGatedChunk;
         nstate = p.f.checkpoints[at * chunks + (chunk < chunks ? chunk : chunks - 1)];
     };
     int64_t base = p.f.L > 0 ? start + (stop - 1 - start) / kSpan * kSpan : -1;
-    const int64_t mine = ((int64_t)wave * G + lane) * kLaneSteps;
+    const int64_t mine = wave * (G * kLaneSteps);  // of the wave
     if (base >= 0)
         fetch(base + mine);
     const float rate = p.f.c * softplus_row(lam) * kLog2e;
@@ -174,13 +175,14 @@ __global__ __launch_bounds__(gated_threads(WAVES)) void gated_bwd_kernel(const G
             sum_r += orr[j];
             sum_i += oi[j];
         }
-        const int n = steps_left(L, t);
-        Eight<BF16>::store(dx + t, ox, n);
-        Eight<BF16>::store(dr + t, orr, n);
-        Eight<BF16>::store(di + t, oi, n);
+        const int left = steps_left<G>(L, t), n = lane_share(left, off);
+        const bool whole = G == 64 && left == G * kLaneSteps;
+        Eight<BF16>::store(dx + t + off, ox, whole, n);
+        Eight<BF16>::store(dr + t + off, orr, whole, n);
+        Eight<BF16>::store(di + t + off, oi, whole, n);
         if constexpr (GATE)
-            Eight<BF16>::store(dz + t, dgate, n);
-        if (live && t == 0)
+            Eight<BF16>::store(dz + t + off, dgate, whole, n);
+        if (live && t == 0 && lane == 0)
             p.dh0[row] = behind;
     }
     if (p.f.L == 0 && live && lane == 0 && wave == 0)
@@ -215,8 +217,8 @@ __global__ __launch_bounds__(gated_threads(WAVES)) void gated_bwd_kernel(const G
             p.dr_bias[row] = sum_r;
             p.di_bias[row] = sum_i;
         } else {
-            const int64_t all = PARTS ? p.f.parts * rows : rows;
-            float *sum = p.partials + (PARTS ? blockIdx.y * rows : 0) + row;
+            const int64_t all = (int64_t)(PARTS ? p.f.parts : 1) * rows;
+            float *sum = p.partials + (PARTS ? (int64_t)blockIdx.y * rows : 0) + row;
             sum[0] = sum_q;
             sum[all] = sum_r;
             sum[2 * all] = sum_i;
@@ -249,7 +251,7 @@ __global__ __launch_bounds__(256) void gated_back_maps_kernel(const GatedScanBwd
     using T = typename Elem<BF16>::T;
     constexpr int kSpan = 64 * kLaneSteps;
     const int lane = threadIdx.x & 63, part = blockIdx.y + 1;
-    const int64_t at = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
+    const int64_t at = uniform<true>(blockIdx.x * 4 + threadIdx.x / 64);
     if (at >= p.f.B * p.f.D)
         return;
     const uint32_t d = (uint32_t)at % (uint32_t)p.f.D;
@@ -262,22 +264,24 @@ __global__ __launch_bounds__(256) void gated_back_maps_kernel(const GatedScanBwd
     Span<RESET> all{0.f, 0.f};
     Eight<BF16> nr, nd, nz;
     uint32_t nreset = 0;
+    const uint32_t off = lane * kLaneSteps;
     auto fetch = [&](int64_t t) {
-        const int n = steps_left(stop, t);
-        load_some<BF16>(nr, r + t, n, -__builtin_inff());
-        load_some<BF16>(nd, dout + t, n, 0.f);
+        const int left = steps_left<64>(stop, t), n = lane_share(left, off);
+        const bool whole = left == kSpan;
+        load_some<BF16>(nr, r + t + off, whole, n, -__builtin_inff());
+        load_some<BF16>(nd, dout + t + off, whole, n, 0.f);
         if constexpr (GATE)
-            load_some<BF16>(nz, z + t, n, 0.f);
+            load_some<BF16>(nz, z + t + off, whole, n, 0.f);
         if constexpr (RESET)
-            nreset = load_resets(reset + t, n);
+            nreset = load_resets(reset + t + off, whole, n);
     };
     int64_t base = start + (stop - 1 - start) / kSpan * kSpan;
-    fetch(base + lane * kLaneSteps);
+    fetch(base);
     for (; base >= start; base -= kSpan) {
         const Eight<BF16> cr = nr, cd = nd, cz = nz;
         const uint32_t first = nreset;
         if (base > start)
-            fetch(base - kSpan + lane * kLaneSteps);
+            fetch(base - kSpan);
         float sum = 0.f, behind = 0.f;
 #pragma unroll
         for (int j = kLaneSteps - 1; j >= 0; --j) {

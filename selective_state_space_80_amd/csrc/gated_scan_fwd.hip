@@ -53,9 +53,9 @@ __global__ __launch_bounds__(gated_threads(WAVES)) void gated_fwd_kernel(const G
     constexpr int kRows = gated_threads(WAVES) / G / WAVES;  // of a workgroup
     constexpr int kSpan = G * kLaneSteps * WAVES;
     __shared__ float2 maps[2][WAVES];
-    const int lane = threadIdx.x & (G - 1), wave = threadIdx.x / G % WAVES;
-    const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / (G * WAVES);
-    const bool live = row < p.B * p.D;  // the others' lanes run along, with nothing to load or store
+    const int lane = threadIdx.x & (G - 1), wave = uniform<G == 64>(threadIdx.x / G % WAVES);
+    const int rows = (int)(p.B * p.D), row = uniform<G == 64>(blockIdx.x * kRows + threadIdx.x / (G * WAVES));
+    const bool live = row < rows;  // the others' lanes run along, with nothing to load or store
     const int64_t from = PARTS ? blockIdx.y * p.part_steps : 0;
     const int64_t stop = PARTS && from + p.part_steps < p.L ? from + p.part_steps : p.L;
     const int64_t at = live ? row : 0, L = live ? stop : 0;
@@ -72,17 +72,19 @@ __global__ __launch_bounds__(gated_threads(WAVES)) void gated_fwd_kernel(const G
 
     Eight<BF16> nx, nr, ni, nz;
     uint32_t nreset = 0;
+    const uint32_t off = lane * kLaneSteps;
     auto fetch = [&](int64_t t) {
-        const int n = steps_left(L, t);
-        load_some<BF16>(nr, r + t, n, -__builtin_inff());  // past the end: steps that change nothing
-        load_some<BF16>(nx, x + t, n, 0.f);
-        load_some<BF16>(ni, i + t, n, 0.f);
+        const int left = steps_left<G>(L, t), n = lane_share(left, off);
+        const bool whole = G == 64 && left == G * kLaneSteps;
+        load_some<BF16>(nr, r + t + off, whole, n, -__builtin_inff());  // past the end: steps that change nothing
+        load_some<BF16>(nx, x + t + off, whole, n, 0.f);
+        load_some<BF16>(ni, i + t + off, whole, n, 0.f);
         if constexpr (GATE)
-            load_some<BF16>(nz, z + t, n, 0.f);
+            load_some<BF16>(nz, z + t + off, whole, n, 0.f);
         if constexpr (RESET)
-            nreset = load_resets(reset + t, n);
+            nreset = load_resets(reset + t + off, whole, n);
     };
-    int64_t t = from + ((int64_t)wave * G + lane) * kLaneSteps;
+    int64_t t = from + wave * (G * kLaneSteps);  // of the wave
     fetch(t);
     // worked out while the first loads are on their way
     const float rate = p.c * softplus_row(lam) * kLog2e;  // of the exponents of 2
@@ -124,7 +126,8 @@ __global__ __launch_bounds__(gated_threads(WAVES)) void gated_fwd_kernel(const G
             out[j] = GATE ? h * silu_hw(cz.get(j)) : h;
         }
         if (p.y)
-            Eight<BF16>::store(y + t, out, steps_left(L, t));
+            Eight<BF16>::store(y + t + off, out, G == 64 && steps_left<G>(L, t) == G * kLaneSteps,
+                               lane_share(steps_left<G>(L, t), off));
         // the steps past the end have left the state as it was
         if (p.h_last && live && base + kSpan >= p.L && stop == p.L && lane == G - 1 && wave == WAVES - 1)
             p.h_last[row] = h;
@@ -139,7 +142,7 @@ template <bool BF16, bool RESET> __global__ __launch_bounds__(256) void gated_ma
     using T = typename Elem<BF16>::T;
     constexpr int kSpan = 64 * kLaneSteps;
     const int lane = threadIdx.x & 63;
-    const int64_t at = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
+    const int64_t at = uniform<true>(blockIdx.x * 4 + threadIdx.x / 64);
     if (at >= p.B * p.D)
         return;
     const uint32_t d = (uint32_t)at % (uint32_t)p.D;
@@ -152,19 +155,20 @@ template <bool BF16, bool RESET> __global__ __launch_bounds__(256) void gated_ma
     Span<RESET> all{0.f, 0.f};
     Eight<BF16> nx, nr, ni;
     uint32_t nreset = 0;
+    const uint32_t off = lane * kLaneSteps;
     auto fetch = [&](int64_t t) {
-        nr.load(r + t);
-        nx.load(x + t);
-        ni.load(i + t);
+        nr.load(r + t + off);
+        nx.load(x + t + off);
+        ni.load(i + t + off);
         if constexpr (RESET)
-            nreset = load_resets(reset + t, kLaneSteps);
+            nreset = load_resets(reset + t + off, true, kLaneSteps);
     };
-    fetch(from + lane * kLaneSteps);
+    fetch(from);
     for (int64_t base = from; base < stop; base += kSpan) {
         const Eight<BF16> cx = nx, cr = nr, ci = ni;
         const uint32_t first = nreset;
         if (base + kSpan < stop)
-            fetch(base + kSpan + lane * kLaneSteps);
+            fetch(base + kSpan);
         float a[kLaneSteps], b[kLaneSteps];
         Span<RESET> m = lane_steps<BF16, RESET>(cx, cr, ci, first, rate, rb, ib, a, b);
         join_before<64, RESET>(m);
