@@ -314,12 +314,12 @@ inline int gated_group(int64_t L)
 }
 
 // Waves that share a row: at most `most`, while there are fewer than about 12000 waves
-// in all and each has `least` chunks of the row or more (a power of two).
-inline int gated_waves(int64_t rows, int64_t L, int least, int most)
+// in all and each has four chunks of the row or more (a power of two).
+inline int gated_waves(int64_t rows, int64_t L, int most)
 {
     const int64_t chunks = (L + 64 * kLaneSteps - 1) / (64 * kLaneSteps);
     int waves = 1;
-    while (waves * 2 <= most && waves * 2 * rows <= 12288 && waves * 2 * least <= chunks)
+    while (waves * 2 <= most && waves * 2 * rows <= 12288 && waves * 2 * 4 <= chunks)
         waves *= 2;
     return waves;
 }

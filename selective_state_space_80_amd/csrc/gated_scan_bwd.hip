@@ -9,7 +9,7 @@
 // come from the forward call's checkpoints, one a chunk, and the steps after it run
 // again; so a chunk needs nothing from its neighbours but the gradient that enters it
 // from behind, a_(t+1) g_(t+1), and the inputs are read once.  Bound by memory: 8 x 5120
-// x 2048 bf16 229 us, 5.1 TB/s, gated 291 to 313.
+// x 2048 bf16 215 us, 5.5 TB/s, gated 260 to 278.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -163,7 +163,8 @@ __global__ __launch_bounds__(gated_threads(WAVES)) void gated_bwd_kernel(const G
             behind = a[j] * g;
             float m1 = m2[j] * rm[j];
             const float in = gate[j] * cx.get(j);
-            float q = g * (u[j] * kLn2) * a[j] * fmaf(a[j] * rm[j], in, -before[j]);
+            const float va = u[j] * kLn2 * a[j];  // first: v / m stays small where 1 / m does not
+            float q = g * fmaf(va * a[j] * rm[j], in, -va * before[j]);
             if (RESET && (first >> j & 1)) {
                 behind = q = 0.f;
                 m1 = 1.f;
@@ -341,10 +342,11 @@ template <int G, int WAVES, bool PARTS = false> hipError_t launch(const GatedSca
 }  // namespace
 
 // Waves of a row, both sides measured (us, inputs from memory):
-//   8 x 5120 x 2048 bf16, gated  one 313, two 365, four 459
-//   2 x 1536 x 8192 fp32         one 162, two 140, four 152
-//   1 x 1536 x 131072 bf16       one 667, two 599, four 596, eight 562
-//   1 x 256 x 131072 bf16, gated one 462, two 233, four 130, eight 126
+//   8 x 5120 x 2048 bf16, gated  one 278, two 334, four 324
+//   2 x 1536 x 8192 fp32         one 156, two 150, four 141, eight 155
+//   1 x 512 x 32768 bf16         one 102, two 84, four 48, eight 53
+//   1 x 1536 x 131072 bf16       one 664, two 634, four 588, eight 544
+//   1 x 256 x 131072 bf16, gated one 436, two 231, four 128, eight 119
 hipError_t launch_gated_scan_bwd(const GatedScanBwdArgs &a, hipStream_t s)
 {
     hipError_t e = hipSuccess;
@@ -359,7 +361,7 @@ hipError_t launch_gated_scan_bwd(const GatedScanBwdArgs &a, hipStream_t s)
                 e = launch<64, 1, true>(a, s);
                 break;
             }
-            switch (gated_waves(rows, a.f.L, 8, 8)) {
+            switch (gated_waves(rows, a.f.L, a.f.L >= 128 * kGatedChunk ? 8 : 4)) {
             case 1: e = launch<64, 1>(a, s); break;
             case 2: e = launch<64, 2>(a, s); break;
             case 4: e = launch<64, 4>(a, s); break;

@@ -8,8 +8,8 @@
 // into parts for different workgroups, whose maps a first kernel works out.
 //
 // What bounds it is memory, with the vector unit close behind (about 40 issue slots an
-// element, six of them transcendental at two slots): 8 x 5120 x 2048 bf16 129 us, 5.2
-// TB/s, gated 161, where a large copy moves 5.1 to 5.4 and the slots take 86 and 100.
+// element, six of them transcendental at two slots): 8 x 5120 x 2048 bf16 123 us, 5.45
+// TB/s, gated 150 with 86 % of the vector unit's slots taken; a large copy moves 5.1 to 5.4.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -293,7 +293,7 @@ template <int EACH> hipError_t launch_step(const GatedStepArgs &a, hipStream_t s
 }  // namespace
 
 // The inputs are then read twice, the second time mostly from the caches.  Both sides
-// measured, with eight or sixteen waves of one workgroup a row and in parts (us):
+// measured, with waves of one workgroup and in parts (us):
 //   1 x 64 x 131072 bf16         55 and 32, backward 85 and 46
 //   1 x 32 x 131072 fp32         59 and 29, backward 100 and 43
 //   1 x 128 x 131072 bf16, gated 64 and 57, backward 105 and 92 (129 rows, 128 rows)
@@ -310,11 +310,11 @@ GatedParts gated_parts(int64_t rows, int64_t L)
 }
 
 // Waves of a row, both sides measured (us, inputs from memory):
-//   8 x 5120 x 2048 bf16, gated  one 162, two 187, four 182
-//   2 x 1536 x 8192 fp32         one 81.6, four 79.3, eight 79.5, 16 92.5
-//   1 x 1536 x 131072 bf16       one 403, two 341, four 339, eight 323, 16 340
-//   1 x 256 x 131072 bf16, gated one 307, four 88, eight 76, 16 71
-//   3 x 771 x 1001 fp32, gated   one 15.1, two 15.6, four 18.6
+//   8 x 5120 x 2048 bf16, gated  one 156, two 196, four 182
+//   2 x 1536 x 8192 fp32         one 80.3, two 79.9, four 75.8, eight 75.0, 16 83.7
+//   1 x 1536 x 131072 bf16       one 401, two 366, four 339, eight 318, 16 365
+//   1 x 256 x 131072 bf16, gated one 336, four 89, eight 69, 16 76
+//   3 x 771 x 1001 fp32, gated   one 16.4, two 17.0, four 20.0
 hipError_t launch_gated_scan_fwd(const GatedScanArgs &a, hipStream_t s)
 {
     switch (gated_group(a.L)) {
@@ -336,12 +336,11 @@ hipError_t launch_gated_scan_fwd(const GatedScanArgs &a, hipStream_t s)
         const hipError_t e = hipGetLastError();
         return e == hipSuccess ? launch<64, 1, true>(a, s) : e;
     }
-    switch (gated_waves(rows, a.L, 4, rows <= 256 ? 16 : 8)) {
+    switch (gated_waves(rows, a.L, 8)) {
     case 1: return launch<64, 1>(a, s);
     case 2: return launch<64, 2>(a, s);
     case 4: return launch<64, 4>(a, s);
-    case 8: return launch<64, 8>(a, s);
-    default: return launch<64, 16>(a, s);
+    default: return launch<64, 8>(a, s);
     }
 }
 

@@ -6,8 +6,8 @@
 // conversion, which divides by the power of two exactly.
 //
 // All of it is bound by memory: 2 bytes in, 0.53 out (bf16).  8 x 5120 x 2048, inputs
-// from memory: bf16 token-major 39.5 us, channel-major 38.8 (5.4 TB/s; a large copy moves
-// 5.1), fp32 67.8 and 75.3, back to bf16 31.9.
+// from memory: bf16 token-major 39.5 us, channel-major 38.0 (5.6 TB/s; a large copy moves
+// 5.1 to 5.4), fp32 67.8 and 75.3, back to bf16 31, to fp32 55.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

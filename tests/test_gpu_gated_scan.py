@@ -99,13 +99,17 @@ def test_lam(lam, c):
 
 
 @pytest.mark.parametrize("io", [F32, BF16])
-def test_padded_tokens_leave_the_state(io):
-    """r = -inf: the state, its gradient and everything behind are as without the token."""
+@pytest.mark.parametrize("padding", [None, 3e38])
+def test_padded_tokens_leave_the_state(io, padding):
+    """r = -inf: the state, its gradient and everything behind are as without the token,
+    whatever finite input it has."""
     p = C.make(2, 6, 300, io, seed=11)
     q = C.gradient_inputs(p, 12)
     lengths = (300, 137)
     for b, n in enumerate(lengths):
         p["r"][b, :, n:] = -torch.inf
+        if padding:
+            p["x"][b, :, n:] = padding
     y, h_last, kept = _forward(p, return_last_state=True, return_checkpoints=True)
     got = _backward(p, q, checkpoints=kept)
     n = lengths[1]
@@ -302,9 +306,9 @@ def test_parts_keep_sequences_apart():
         assert torch.equal(got[name][..., outside], got0[name][..., outside]), name
 
 
-@pytest.mark.parametrize("D,L", [(600, 20000), (200, 33000), (130, 9000)])
+@pytest.mark.parametrize("D,L", [(600, 20000), (200, 33000), (130, 9000), (130, 66000)])
 def test_many_rows_of_many_chunks(D, L):
-    """Eight, sixteen and four waves a row, rows in more than one workgroup a CU."""
+    """Four and eight waves a row, forward and backward, rows in more than one workgroup a CU."""
     assert _mamba().gated_scan_fwd_workspace_size(1, D, L) == 0
     p = C.make(1, D, L, F32, seed=40, gate=False)
     q = C.gradient_inputs(p, 41)
