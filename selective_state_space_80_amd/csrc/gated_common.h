@@ -5,8 +5,8 @@
 //   h <- a h + m sigmoid(i) x
 //
 // Two things are kept from losing their digits where a is next to 1 (long memories).
-// 1 - a^2 is e (2 - e) with the loss e = 1 - a from its series.  And spans of steps are
-// joined with the sum of their exponents, not the product of their a: a's rounding
+// 1 - a^2 comes from a polynomial in the exponent there, not from a.  And spans of steps
+// are joined with the sum of their exponents, not the product of their a: a's rounding
 // there (6e-8) would add up over the steps of a sequence, as it is it adds up over a
 // lane's eight.
 #pragma once
@@ -176,18 +176,17 @@ __device__ __forceinline__ float softplus_row(float x)
     return fmaxf(x, 0.f) + 2.f * q * s;
 }
 
-// 1 - 2^-u for u >= 0, given a = 2^-u.  Below 1/8 from the series of 1 - e^-v, v = u ln 2, whose
-// truncation stays below 2e-8 relative there; above, the subtraction loses at most
-// three bits of e.
-__device__ __forceinline__ float loss_of(float u, float a)
+// 1 - a^2 for a = 2^-u, u >= 0.  Below 1/8 by a polynomial in u (through (1 - 2^-2u) / u at
+// the interval's Chebyshev points; off by 1e-8 relative at most); above, the subtraction
+// keeps all but three bits.
+__device__ __forceinline__ float square_of(float u, float a)
 {
-    constexpr float l = kLn2, l2 = l * l, l3 = l2 * l, l4 = l3 * l, l5 = l4 * l;
-    float p = l5 / 120.f;
-    p = fmaf(p, u, -l4 / 24.f);
-    p = fmaf(p, u, l3 / 6.f);
-    p = fmaf(p, u, -l2 / 2.f);
-    p = fmaf(p, u, l);
-    return u < 0.125f ? u * p : 1.f - a;
+    float p = 0.0397070758f;
+    p = fmaf(p, u, -0.153570428f);
+    p = fmaf(p, u, 0.444018692f);
+    p = fmaf(p, u, -0.96090579f);
+    p = fmaf(p, u, 1.38629436f);
+    return u < 0.125f ? u * p : fmaf(-a, a, 1.f);
 }
 
 // The value of the lane that the DPP control names, 0 where there is none or the row

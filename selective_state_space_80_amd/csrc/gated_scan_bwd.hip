@@ -97,8 +97,7 @@ __global__ __launch_bounds__(gated_threads(WAVES)) void gated_bwd_kernel(const G
             u[j] = rate * s;
             gate[j] = sigmoid_log2(ci.get(j), ib);
             a[j] = hw_exp2(-u[j]);
-            const float e = loss_of(u[j], a[j]);
-            m2[j] = e * (2.f - e);
+            m2[j] = square_of(u[j], a[j]);
             // 1 / m; a step that loses nothing (m = 0) has v = 0, which the floor keeps from 0 / 0
             rm[j] = __builtin_amdgcn_rsqf(fmaxf(m2[j], 1e-37f));
             const float in = gate[j] * cx.get(j);

@@ -33,8 +33,7 @@ __device__ __forceinline__ Span<RESET> lane_steps(const Eight<BF16> &x, const Ei
         const float u = rate * sigmoid_log2(r.get(j), rb);
         const float in = sigmoid_log2(i.get(j), ib) * x.get(j);
         a[j] = hw_exp2(-u);
-        const float e = loss_of(u, a[j]);
-        b[j] = __builtin_amdgcn_sqrtf(e * (2.f - e)) * in;
+        b[j] = __builtin_amdgcn_sqrtf(square_of(u, a[j])) * in;
         sum += u;
         h = fmaf(a[j], h, b[j]);
         if (RESET && (first >> j & 1)) {
@@ -262,9 +261,9 @@ __global__ __launch_bounds__(256) void gated_step_kernel(const GatedStepArgs p, 
         float state[EACH], y[EACH];
 #pragma unroll
         for (int j = 0; j < EACH; ++j) {
-            const float u = rate[j] * sigmoid_log2(r.get(j), rb[j]), a = hw_exp2(-u), e = loss_of(u, a);
+            const float u = rate[j] * sigmoid_log2(r.get(j), rb[j]), a = hw_exp2(-u);
             const float in = sigmoid_log2(i.get(j), ib[j]) * x.get(j);
-            state[j] = fmaf(a, h.get(j), __builtin_amdgcn_sqrtf(e * (2.f - e)) * in);
+            state[j] = fmaf(a, h.get(j), __builtin_amdgcn_sqrtf(square_of(u, a)) * in);
             y[j] = GATE ? state[j] * silu_hw(z.get(j)) : state[j];
         }
         Few<EACH, false>::store(p.h_out + at, state);

@@ -6,11 +6,12 @@ Units u = 2^-24 (half a step of fp32), relative unless said otherwise.  The hard
   sigmoid  argument of up to 10 log2 e = 14.4 rounded (14.4 ln2 u), 2^x (2 u), 1 + p (u),
            reciprocal (2 u): below 16 u
   v        the rate (6 u: ln(1 + e^x) and two products), sigmoid, product: below 24 u
-  m        half of e's error (v's, and 8 u where 1 - a is taken directly) and the
-           root: below 20 u
-  input    m, sigmoid, two products: below 40 u of |b|
+  m        half of the error of 1 - a^2 (v's; where it is taken from a, from 2^-v = 0.917
+           down, twice a's 2 u of a^2 = 0.84 over 0.16: 22 u) and the root: below 26 u
+  input    m, sigmoid, two products: below 44 u of |b|
   a        2^-v: v 24 u absolute from v's error, 3 u of its own
-A step's error is then a times the last one's, 40 u |b|, and (24 v + 4) u a |h|, where h
+  v dm/dv  v, a^2 (twice a's), 1 / m, sigmoid, products: below (76 + 48 v) u
+A step's error is then a times the last one's, 44 u |b|, and (24 v + 4) u a |h|, where h
 stands for the recurrence of the absolute values.  Joining spans costs a rounding of its
 sums for each of about 20 joins every 8 steps: 3 u a step more.  2^x gives 0 below the normal range, so a is also
 off by up to TINY = 2^-126 absolutely, whatever its size."""
@@ -84,7 +85,7 @@ def forward(p, c=8.0):
     h = _run(a, b, h0, first)
     size = _run(a, b.abs(), h0.abs(), first)
     before = torch.cat([h0.abs()[..., None], size[..., :-1]], -1)
-    err = _run(a, 40 * U * b.abs() + ((24 * v + 7) * U * a + TINY) * before, torch.zeros_like(h0), first)
+    err = _run(a, 44 * U * b.abs() + ((24 * v + 7) * U * a + TINY) * before, torch.zeros_like(h0), first)
     y, y_err = h, err
     if p["z"] is not None:
         z = _d(p["z"])
@@ -129,13 +130,13 @@ def backward(p, q, c=8.0):
     behind = torch.cat([size[..., 1:], end.abs()[..., None]], -1)
     g_err = _run(a_next, 20 * U * grad.abs() + ((24 * v_next + 7) * U * a_next + TINY) * behind, zero, drop_next, reverse=True)
     out["dx"], out["di"] = g * m * si, g * m * x * si * (1 - si)
-    out["dx_err"] = g_err * m * si + 40 * U * out["dx"].abs()
-    out["di_err"] = g_err * (m * x * si * (1 - si)).abs() + (g * m * x).abs() * si * (44 * U)
+    out["dx_err"] = g_err * m * si + 44 * U * out["dx"].abs()
+    out["di_err"] = g_err * (m * x * si * (1 - si)).abs() + (g * m * x).abs() * si * (48 * U)
     ratio = torch.where(m > 0, v * a * a / m.clamp_min(1e-300), 0.0)  # v dm/dv, to 0 with v
     dv_m, dv_a = ratio * si * x, v * a * before
     dq = g * (dv_m - dv_a)
     dq_err = (g_err * (dv_m.abs() + dv_a.abs()) + g.abs() * v * a * before_err +
-              g.abs() * (dv_m.abs() + dv_a.abs()) * ((60 + 24 * v) * U) +
+              g.abs() * (dv_m.abs() + dv_a.abs()) * ((76 + 48 * v) * U) +
               g.abs() * v * TINY * ((si * x).abs() + before.abs()))
     if first is not None:
         dq, dq_err = torch.where(first, 0.0, dq), torch.where(first, 0.0, dq_err)
@@ -149,7 +150,7 @@ def backward(p, q, c=8.0):
     depth = (L // 64 + 24 + B) * U  # roundings on a term's way through a lane, its wave and the batch
     total = lambda t: t.sum(dim=(0, 2))  # noqa: E731
     unrounded = {"dr": dq_err * (1 - sr) + dq.abs() * 18 * U, "di": g_err * (m * x * si * (1 - si)).abs() +
-                 (g * m * x).abs() * si * (44 * U)}
+                 (g * m * x).abs() * si * (48 * U)}
     out["dlam"] = total(dq) * scale
     out["dlam_err"] = (total(dq_err) + depth * total(dq.abs())) * scale + 16 * U * out["dlam"].abs() + 1e-37
     for name, of in (("dr_bias", "dr"), ("di_bias", "di")):
