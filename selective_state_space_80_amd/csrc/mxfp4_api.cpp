@@ -42,7 +42,7 @@ mamba_status matmul_sizes(int64_t batch, int64_t M, int64_t N, int64_t K, unsign
     if (!sizes_ok(a_shared ? 1 : batch, M, padded) || !sizes_ok(b_shared ? 1 : batch, N, padded))
         return MAMBA_ERR_SHAPE;
     // The kernels number a batch's tiles, of 128 x 64 outputs at least where there
-    // are many, in 32 bits, twice a row of them included.
+    // are many, in 32 bits.
     const int64_t rows = b_shared && !a_shared ? batch * M : M;  // batches of one right operand are one
     return (rows + 127) / 128 * ((N + 63) / 64) < int64_t(1) << 30 ? MAMBA_OK : MAMBA_ERR_SHAPE;
 }

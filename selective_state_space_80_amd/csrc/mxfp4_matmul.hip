@@ -39,6 +39,7 @@ struct MxParams {
     int64_t a_batch, b_batch;              // rows between batches: 0 = shared
     int64_t a_scale_group, b_scale_group;  // bytes between groups of scales
     int tiles_m, tiles_n;
+    int band;                              // tile rows that are walked together
     int64_t tiles;                         // of all batches
 };
 
@@ -139,9 +140,9 @@ __global__ __launch_bounds__(64 * WM * WN, tile_waves(WM, WN, FM, FN, STAGES)) v
     const Share share = xcd_share(p.tiles, xcd);
     if (slot >= share.count)
         return;
-    // Bands of two tile rows, walked along n: 32 neighbouring tiles (an XCD's)
-    // then read 2 + 16 operand tiles.
-    constexpr int kBand = 2;
+    // Bands of six tile rows, walked along n: 32 neighbouring tiles (an XCD's) then read
+    // 6 + 6 operand tiles.  Bands of two (2 + 16) take 4 % more at 8192^3, 8 % more at 5120
+    // x 16384 x 2560; one, 16 % more there with 128 x 128 outputs.
     struct Tile {
         int64_t batch, m0, n0;
     };
@@ -149,9 +150,9 @@ __global__ __launch_bounds__(64 * WM * WN, tile_waves(WM, WN, FM, FN, STAGES)) v
         const int64_t id = share.first + i, per = (int64_t)p.tiles_m * p.tiles_n;
         Tile t;
         t.batch = id / per;
-        const int rest = (int)(id % per), band = rest / (kBand * p.tiles_n), in = rest % (kBand * p.tiles_n);
-        const int left = p.tiles_m - band * kBand, rows = left < kBand ? left : kBand;
-        t.m0 = (int64_t)(band * kBand + in % rows) * TM;
+        const int rest = (int)(id % per), band = rest / (p.band * p.tiles_n), in = rest % (p.band * p.tiles_n);
+        const int left = p.tiles_m - band * p.band, rows = left < p.band ? left : p.band;
+        t.m0 = (int64_t)(band * p.band + in % rows) * TM;
         t.n0 = (int64_t)(in / rows) * TN;
         return t;
     };
@@ -669,6 +670,7 @@ hipError_t launch_mxfp4_matmul(const MxMatmulArgs &a, hipStream_t s)
     p.b_scale_group = (a.b_shared ? a.N : a.batch * a.N) * kMxScales;
     p.tiles_m = (int)((f.M + f.tile_m - 1) / f.tile_m);
     p.tiles_n = (int)((a.N + f.tile_n - 1) / f.tile_n);
+    p.band = p.tiles_m < 6 ? p.tiles_m : 6;
     p.tiles = f.tiles;
     switch (f.form) {
     case kTile256: return tile<2, 4, 4, 2, 2>(p, f.slots, a.bf16, s);
