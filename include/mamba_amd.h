@@ -555,8 +555,8 @@ mamba_status mamba_gated_state_update(const float *h, float *h_out, const void *
  * from it is NaN.
  *   channel_major 0 : x [B, L, K] of `io`
  *   channel_major 1 : x [B, K, L] of `io`, as the scans write their output
- * rows = B * L in both.  K at most 2^23; ceil(rows / 8) * G < 2^23, channel-major
- * B * ceil(L / 64) * G too.
+ * rows = B * L in both.  K at most 2^23; ceil(rows / 32) * G < 2^24, channel-major
+ * B * ceil(L / 64) * G < 2^23.
  */
 mamba_status mamba_quantize_mxfp4(const void *x, uint8_t *q, uint8_t *scale, int64_t B, int64_t L, int64_t K,
                                   int channel_major, mamba_dtype io, void *stream);

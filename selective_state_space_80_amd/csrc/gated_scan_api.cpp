@@ -35,7 +35,7 @@ mamba_status gated_sizes(int64_t B, int64_t D, int64_t L, float c)
 {
     if (!sizes_ok(B, D, L) || !(c >= 0.f) || std::isinf(c))
         return MAMBA_ERR_SHAPE;
-    return B * D >= kMaxGatedRows ? MAMBA_ERR_SHAPE : MAMBA_OK;
+    return B * D >= kMaxGatedRows || D >= kMaxGatedRows ? MAMBA_ERR_SHAPE : MAMBA_OK;  // D alone with B = 0
 }
 
 // What the forward call and the backward one read alike.

@@ -11,7 +11,7 @@
 
 namespace {
 
-constexpr int64_t kMaxBlocks = int64_t(1) << 23;  // of 512 threads below 2^32 work-items
+constexpr int64_t kMaxBlocks = int64_t(1) << 24;  // of 256 threads below 2^32 work-items
 
 size_t packed_bytes(int64_t rows, int64_t K) { return (size_t)(rows * mamba::mx_groups(K)) * mamba::kMxGroupBytes; }
 size_t scale_bytes(int64_t rows, int64_t K) { return (size_t)(rows * mamba::mx_groups(K)) * mamba::kMxScales; }
@@ -24,7 +24,7 @@ mamba_status row_sizes(int64_t B, int64_t L, int64_t K)
     if (K > mamba::kMaxMxInner)
         return MAMBA_ERR_UNSUPPORTED;
     const int64_t groups = mamba::mx_groups(K);
-    if (!sizes_ok(B, L, groups * mamba::kMxGroup) || (B * L + 7) / 8 * groups >= kMaxBlocks)
+    if (!sizes_ok(B, L, groups * mamba::kMxGroup) || (B * L + 31) / 32 * groups >= kMaxBlocks)
         return MAMBA_ERR_SHAPE;
     return MAMBA_OK;
 }
@@ -62,7 +62,7 @@ mamba_status mamba_quantize_mxfp4(const void *x, uint8_t *q, uint8_t *scale, int
     if (channel_major != 0 && channel_major != 1)
         return MAMBA_ERR_UNSUPPORTED;
     const int64_t rows = B * L;
-    if (channel_major && B * ((L + 63) / 64) * mamba::mx_groups(K) >= kMaxBlocks)
+    if (channel_major && B * ((L + 63) / 64) * mamba::mx_groups(K) >= kMaxBlocks / 2)  // of 512 threads
         return MAMBA_ERR_SHAPE;
     if (rows * K == 0)
         return MAMBA_OK;

@@ -64,7 +64,8 @@ template <int ROWS, bool BF16> __global__ __launch_bounds__(256) void quantize_k
     constexpr int kUnits = ROWS / 8;
     __shared__ uint32_t codes[ROWS * kMxScales / 4];
     const int64_t groups = mx_groups(p.K), rows = p.B * p.L;
-    const int64_t g = blockIdx.x % groups, row0 = blockIdx.x / groups * ROWS;
+    const uint32_t n_groups = (uint32_t)groups, g = blockIdx.x % n_groups;  // blocks are below 2^24
+    const int64_t row0 = (int64_t)(blockIdx.x / n_groups) * ROWS;
     const int lane = threadIdx.x & 31;
     const int64_t k = g * kMxGroup + lane * 8;
     float f[kUnits][8];
@@ -122,7 +123,8 @@ template <bool BF16> __global__ __launch_bounds__(512) void quantize_channel_ker
     __shared__ __attribute__((aligned(16))) uint8_t rows_out[kTokens * kMxGroupBytes];
     __shared__ __attribute__((aligned(16))) uint8_t scales_out[kTokens * kMxScales];
     const int64_t groups = mx_groups(p.K), rows = p.B * p.L, tiles = (p.L + kTokens - 1) / kTokens;
-    const int64_t tile = blockIdx.x % tiles, g = blockIdx.x / tiles % groups, b = blockIdx.x / tiles / groups;
+    const uint32_t n_tiles = (uint32_t)tiles, n_groups = (uint32_t)groups;  // blocks are below 2^23
+    const int64_t tile = blockIdx.x % n_tiles, g = blockIdx.x / n_tiles % n_groups, b = blockIdx.x / n_tiles / n_groups;
     const int lane = threadIdx.x & 63, block = threadIdx.x / 64;
     const int64_t t = tile * kTokens + lane * kEach, k = g * kMxGroup + block * 32;
     const int left = p.K - k < 32 ? (p.K > k ? (int)(p.K - k) : 0) : 32;  // channels of this block
@@ -212,7 +214,8 @@ template <int ROWS, bool BF16> __global__ __launch_bounds__(256) void dequantize
     using T = typename Elem<BF16>::T;
     constexpr int kEach = BF16 ? 8 : 4, kLanes = kMxGroup / kEach, kPass = 256 / kLanes, kUnits = ROWS / kPass;
     const int64_t groups = mx_groups(p.K);
-    const int64_t g = blockIdx.x % groups, row0 = blockIdx.x / groups * ROWS + threadIdx.x / kLanes;
+    const uint32_t n_groups = (uint32_t)groups, g = blockIdx.x % n_groups;
+    const int64_t row0 = (int64_t)(blockIdx.x / n_groups) * ROWS + threadIdx.x / kLanes;
     const int lane = threadIdx.x & (kLanes - 1);
     const int64_t k = g * kMxGroup + lane * kEach;
     if (k >= p.K)

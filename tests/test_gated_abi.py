@@ -69,7 +69,8 @@ def test_forward_rejects(lib, kw, want):
     (dict(dx=_p(15, 1)), EALIGN), (dict(dh0=_p(22, 2)), EALIGN), (dict(ck=_p(12, 2)), EALIGN), (dict(ws=None), EWS),
     (dict(nws=255), EWS), (dict(ws=_p(23, 128)), EWS), (dict(ck=None, nws=2 * 64 * 3 * 4), EWS), (dict(dx=DO), EALIAS),
     (dict(dx=X), EALIAS), (dict(dr=DX), EALIAS), (dict(dz=DI), EALIAS), (dict(dlam=LAM), EALIAS), (dict(dh0=DHL), EALIAS),
-    (dict(ws=X), EALIAS), (dict(ws=CK), EALIAS), (dict(dh0=H0), EALIAS), (dict(D=0), OK)])
+    (dict(ws=X), EALIAS), (dict(ws=CK), EALIAS), (dict(dh0=H0), EALIAS), (dict(D=0), OK),
+    (dict(B=0, D=1 << 24), ESHAPE)])
 def test_backward_rejects(lib, kw, want):
     assert bwd(lib, **kw) == want
 

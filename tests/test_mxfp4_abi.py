@@ -53,7 +53,7 @@ def test_quantise_rejects(lib, cm, kw, want):
 
 
 @pytest.mark.parametrize("kw,want", [
-    (dict(io=2), EDTYPE), (dict(rows=-1), ESHAPE), (dict(K=-1), ESHAPE), (dict(K=(1 << 23) + 1), EUNSUP), (dict(rows=1 << 27), ESHAPE),
+    (dict(io=2), EDTYPE), (dict(rows=-1), ESHAPE), (dict(K=-1), ESHAPE), (dict(K=(1 << 23) + 1), EUNSUP), (dict(rows=1 << 28), ESHAPE),
     (dict(q=None), ENULL), (dict(s=None), ENULL), (dict(out=None), ENULL), (dict(q=_p(2, 8)), EALIGN), (dict(s=_p(3, 4)), EALIGN),
     (dict(out=_p(8, 1)), EALIGN), (dict(out=Q), EALIAS), (dict(out=S), EALIAS), (dict(rows=0), OK), (dict(K=0), OK)])
 def test_dequantise_rejects(lib, kw, want):
