@@ -1054,15 +1054,15 @@ def quantize_mxfp4(x, channel_major=False, out=None, scale=None):
 
 def _mxfp4_operand(q, scale, name, index):
     """Checks a packed operand and its scales; returns its number of groups."""
-    torch = _torch()
-    shape, u8 = q.shape, torch.uint8
+    shape, u8 = q.shape, _torch().uint8
     if not shape or shape[-1] % 128:
         raise ValueError(f"{name} has rows of whole groups of 128 bytes, got {tuple(shape)}")
     groups = shape[-1] // 128
-    if not (q.dtype is u8 and q.get_device() == index and q.is_contiguous()
-            and _is(scale, (groups, *shape[:-1], 8), u8, index)):
+    want = (groups, shape[0], 8) if len(shape) == 2 else (groups, *shape[:-1], 8)
+    if not (q.dtype is u8 and q.is_contiguous() and q.get_device() == index
+            and _is(scale, want, u8, index)):
         _check(q, name, shape, u8)
-        _check(scale, f"{name}_scale", (groups, *shape[:-1], 8), u8, q.device)
+        _check(scale, f"{name}_scale", want, u8, q.device)
         raise ValueError(f"{name} is on {q.device}, expected another device")
     return groups
 

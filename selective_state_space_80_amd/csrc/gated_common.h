@@ -291,7 +291,8 @@ template <int G, bool DROPS> __device__ __forceinline__ Span<DROPS> join_behind(
 
 // The map of a row's parts before this one (lane l holds part l's, or nothing), joined,
 // applied to the state that enters the first.
-template <bool DROPS> __device__ __forceinline__ float through_parts(const float2 *maps, int count, bool from_end, int parts, float s)
+template <bool DROPS>
+__device__ __forceinline__ float through_parts(const float2 *maps, int count, bool from_end, int parts, float s)
 {
     const int lane = threadIdx.x & 63;
     Span<DROPS> m{0.f, 0.f};

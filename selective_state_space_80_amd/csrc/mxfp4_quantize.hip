@@ -207,8 +207,8 @@ template <bool BF16> __global__ __launch_bounds__(512) void quantize_channel_ker
 // ---- back ------------------------------------------------------------------------------
 // A lane takes what it stores in 16 bytes, 8 elements (bf16) or 4, so that a wave's store
 // is one piece, of several rows, and stores it past the caches (8 x 2048 x 5120 in fp32:
-// 55 us; by the caches 102, with 8 elements a lane and two half-empty stores 123; bf16 31).  The product with the power of two is exact but where it leaves the range
-// of the type.
+// 55 us; by the caches 102, with 8 elements a lane and two half-empty stores 123; bf16
+// 31).  The product with the power of two is exact but where it leaves the type's range.
 template <int ROWS, bool BF16> __global__ __launch_bounds__(256) void dequantize_kernel(const MxDequantArgs p)
 {
     using T = typename Elem<BF16>::T;
