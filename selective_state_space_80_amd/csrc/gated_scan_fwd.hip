@@ -9,7 +9,7 @@
 //
 // What bounds it is memory, with the vector unit close behind (about 40 issue slots an
 // element, six of them transcendental at two slots): 8 x 5120 x 2048 bf16 123 us, 5.45
-// TB/s, gated 150 with 86 % of the vector unit's slots taken; a large copy moves 5.1 to 5.4.
+// TB/s, gated 148 with 85 % of the vector unit's slots taken; a large copy moves 5.1 to 5.4.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
