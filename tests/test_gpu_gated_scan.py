@@ -323,3 +323,29 @@ def test_many_rows_of_many_chunks(D, L):
         assert C.worst(got[name][:, rows], want[name], want[name + "_err"]) <= 1, name
     for name in ("dlam", "dr_bias", "di_bias"):
         assert C.worst(got[name][rows], want[name], want[name + "_err"]) <= 1, name
+
+
+@pytest.mark.parametrize("B,D,L", [(2, 5, 90), (1, 3, 20000)])
+def test_the_callers_own_buffers(B, D, L):
+    """Outputs, workspaces and resets (any non-zero byte) that the caller brings."""
+    mamba = _mamba()
+    p = C.make(B, D, L, BF16, seed=60, reset=0.01)
+    q = C.gradient_inputs(p, 61)
+    y, last, kept = _forward(p, return_last_state=True, return_checkpoints=True)
+    got = _backward(p, q, checkpoints=kept)
+    marks = (p["reset"].to(torch.uint8) * torch.arange(1, L + 1) % 256).to(torch.uint8)
+    own = {**p, "reset": torch.where(p["reset"] & (marks == 0), 7, marks).to(torch.uint8)}
+    out, h_last, ck = torch.full_like(y, 9.0), torch.full_like(last, 9.0), torch.full_like(kept, 9.0)
+    for spare in (0, 512):
+        need = mamba.gated_scan_fwd_workspace_size(B, D, L) + spare
+        ws = torch.full((max(need, 1),), 255, dtype=torch.uint8, device="cuda")
+        same = _forward(own, out=out, h_last=h_last, checkpoints=ck, workspace=ws)
+        assert same is out
+        assert torch.equal(out, y) and torch.equal(h_last, last) and torch.equal(ck, kept)
+        need = mamba.gated_scan_bwd_workspace_size(B, D, L) + spare
+        ws = torch.full((max(need, 1),), 255, dtype=torch.uint8, device="cuda")
+        again = _backward(own, q, checkpoints=ck, workspace=ws)
+        assert all(torch.equal(got[n], again[n]) for n in GRADS)
+    if mamba.gated_scan_bwd_workspace_size(B, D, L):
+        with pytest.raises(mamba.MambaError):
+            _backward(own, q, checkpoints=ck, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))

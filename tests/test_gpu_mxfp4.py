@@ -230,3 +230,22 @@ def test_offsets_past_32_bits():
     want = mamba.mxfp4_matmul(q1, w, s1, sw)
     assert torch.equal(mamba.mxfp4_matmul(q, w, s, sw)[-64:], want)
     assert torch.equal(mamba.mxfp4_matmul(w, q, sw, s)[:, -64:], want.t())
+
+
+def test_one_row_and_the_callers_own_buffers():
+    mamba = _mamba()
+    x = _normal((700,), F32, 8)
+    q, s = mamba.quantize_mxfp4(x)
+    assert q.shape == (384,) and s.shape == (3, 8)
+    q2, s2 = mamba.quantize_mxfp4(x[None], out=torch.full((1, 384), 9, dtype=torch.uint8, device="cuda"),
+                                  scale=torch.full((3, 1, 8), 9, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(q2[0], q) and torch.equal(s2[:, 0], s)
+    back = mamba.dequantize_mxfp4(q, s, dtype=F32)
+    assert back.shape == (768,) and not back[700:].any()
+    assert torch.equal(back[:700].cpu().double(), C.values(q, s)[:700])
+    out = torch.full((1, 700), 9.0, device="cuda")
+    assert mamba.dequantize_mxfp4(q2, s2, 700, dtype=F32, out=out) is out and torch.equal(out[0], back[:700])
+    prod = torch.full((1, 1), 9.0, device="cuda")
+    assert mamba.mxfp4_matmul(q2, q2, s2, s2, out_dtype=F32, out=prod) is prod
+    v = C.values(q2, s2)
+    assert ((prod.cpu().double() - v @ v.t()).abs() <= C.product_bound(v, v, v @ v.t(), C.U)).all()
