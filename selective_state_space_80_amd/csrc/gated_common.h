@@ -157,11 +157,13 @@ __device__ __forceinline__ float sigmoid_log2(float x, float bias2)
 // ln(1 + e^x), which scales every v of a row: max(x, 0) + ln(1 + t), t = e^-|x|.  t by
 // 2^x of the fraction of |x| log2 e, which the split constant gives to within 2^-25; the
 // logarithm as 2 atanh(q), q = t / (2 + t) at most 1/3, whose series to q^15 is left off
-// below 1e-8 relative.
+// below 1e-8 relative.  |x| is held at 200, where t is 0 in fp32: of a larger one the
+// product with log2 e is off by more than a fraction's range (of an infinite one there is
+// none).  By a comparison, which lets a NaN through.
 __device__ __forceinline__ float softplus_row(float x)
 {
     constexpr float kLog2eLow = (float)(1.44269504088896340736 - (double)kLog2e);
-    const float y = -fabsf(x), whole = __builtin_rintf(y * kLog2e);
+    const float y = fabsf(x) > 200.f ? -200.f : -fabsf(x), whole = __builtin_rintf(y * kLog2e);
     const float part = fmaf(y, kLog2eLow, fmaf(y, kLog2e, -whole));
     const float t = __builtin_amdgcn_ldexpf(hw_exp2(part), (int)fmaxf(whole, -1000.f));
     const float q = t * hw_rcp(2.f + t), q2 = q * q;

@@ -1,0 +1,113 @@
+"""The gated recurrence at the ends of its parameters' range, against 64 bits with the
+bounds of gated_check.py.  Those know no underflow of v, whose root m = sqrt(2 v) is: below
+lam = -104 softplus(lam) < 2^-149 is 0 in fp32, and m with it, where 64 bits still have m =
+7e-24.  There, and where a parameter is infinite, the 64-bit side takes a finite value whose
+gates are the same in fp32 and far past it: softplus(-700) = 1e-304, m below 1e-151, and a decay of
+1e38 leaves nothing of a state, as one of infinity does."""
+import pytest
+import torch
+
+import gated_check as C
+from scan_check import say
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+INF = float("inf")
+GRADS = ("dx", "dr", "di", "dz", "dlam", "dr_bias", "di_bias", "dh0")
+PARAMETERS = ("lam", "r_bias", "i_bias")
+
+
+def _mamba():
+    import selective_state_space_80_amd as mamba
+    return mamba
+
+
+def _call(p, which, *more, **kw):
+    g = {k: None if v is None else v.cuda() for k, v in p.items()}
+    return getattr(_mamba(), which)(g["x"], g["r"], g["i"], g["lam"], *more, r_bias=g["r_bias"], i_bias=g["i_bias"],
+                                    z=g["z"], h0=g["h0"], reset=g["reset"], **kw)
+
+
+def _step(p, c):
+    """The first step of p by the single-step call: (y, state)."""
+    g = {k: (v[..., 0].contiguous() if v is not None and v.dim() == 3 else v) for k, v in p.items()}
+    g = {k: None if v is None else v.cuda() for k, v in g.items()}
+    h = torch.empty_like(g["h0"])
+    y = _mamba().gated_state_update(g["h0"], g["x"], g["r"], g["i"], g["lam"], r_bias=g["r_bias"], i_bias=g["i_bias"],
+                                    z=g["z"], c=c, h_out=h)
+    return y, h
+
+
+def _far(p):
+    """p with finite parameters that mean the same."""
+    out = dict(p, lam=torch.where(p["lam"] < -104.0, -700.0, p["lam"].clamp(max=3e38)))
+    for name in ("r_bias", "i_bias"):
+        if p[name] is not None:
+            out[name] = p[name].clamp(-700.0, 700.0)
+    return out
+
+
+def _check(p, seed, c=8.0, forgets=()):
+    """Forward, gradient and single step; forgets: channels whose every step has v above 1e4, so
+    that a is 0 (to any number of bits that fp32 has) and dr and dlam are 0."""
+    far = _far(p)
+    f, q = C.forward(far, c), C.gradient_inputs(p, seed)
+    want = C.backward(far, q, c)
+    y, h_last, kept = _call(p, "gated_scan_fwd", c=c, return_last_state=True, return_checkpoints=True)
+    parts = {"y": C.worst(y, f["y"], f["y_err"]), "h_last": C.worst(h_last, f["h_last"], f["h_last_err"])}
+    forgets = torch.tensor(sorted(forgets), dtype=torch.long)
+    for kw in (dict(checkpoints=kept), {}):
+        got = _call(p, "gated_scan_bwd", q["dout"].cuda(), dh_last=q["dh_last"].cuda(), c=c, **kw)
+        for name in GRADS:
+            if name not in want:
+                assert got[name] is None
+                continue
+            part = C.worst(got[name], want[name], want[name + "_err"])
+            parts[name] = max(part, parts.get(name, 0.0))
+        assert not got["dr"][:, forgets].any() and not got["dlam"][forgets].any()
+    first = {k: (v[..., :1].contiguous() if v is not None and v.dim() == 3 else v) for k, v in p.items()}
+    first["reset"] = None
+    f1 = C.forward(_far(first), c)
+    y1, h1 = _step(first, c)
+    parts["step"] = max(C.worst(y1, f1["y"][..., 0], f1["y_err"][..., 0]), C.worst(h1, f1["h_last"], f1["h_last_err"]))
+    say("  parts of the bounds: " + ", ".join(f"{k} {v:.2f}" for k, v in parts.items()))
+    assert max(parts.values()) <= 1.0, parts
+
+
+# lengths that fill the lanes of every kind of row: groups of 4, 16, 32 and 64 lanes, two and
+# four waves a row, and parts of a row (from 15873 steps on)
+WHOLE = [32, 128, 256, 1024, 4096, 8192, 16384]
+# not between 709 and 1e4, where the 64-bit side's e^lam is infinite
+LARGE = [s * v for v in (1.5e2, 2.5e2, 6e2, 2e4, 3e9, 1e10, 3.3e10, 1e12, 1e20, 1e30, 1e37) for s in (1, -1)] + [-3e38, -INF]
+
+
+@pytest.mark.parametrize("io,reset", [(F32, 0.0), (BF16, 0.01)])
+@pytest.mark.parametrize("L", WHOLE)
+def test_large_lam(L, io, reset):
+    """lam of any size: a channel that keeps its state, or one that forgets it."""
+    say(f"gated scan large lam L={L} {io}")
+    p = C.make(1, len(LARGE), L, io, seed=L, gate=io == BF16, reset=reset)
+    p["lam"] = torch.tensor(LARGE)
+    _check(p, L + 1, forgets=[k for k, v in enumerate(LARGE) if v > 1e8])
+
+
+@pytest.mark.parametrize("size", [1e9, 1e10, 1e20, 1e30])
+def test_large_lam_and_small_c(size):
+    """c softplus(lam) between 0.1 and 4: ordinary decays."""
+    say(f"gated scan lam {size}, c {1 / size}")
+    p = C.make(2, 24, 1024, F32, seed=3)
+    p["lam"] = torch.linspace(0.1, 4.0, 24) * size
+    _check(p, 4, c=float(torch.tensor(1 / size)))
+
+
+def test_nan_lam_stays_in_its_channel():
+    p = C.make(2, 4, 512, F32, seed=5)
+    clean = _call(p, "gated_scan_fwd")
+    lam = p["lam"].clone()
+    lam[1] = torch.nan
+    y = _call(dict(p, lam=lam), "gated_scan_fwd")
+    others = torch.tensor([0, 2, 3])
+    assert torch.isnan(y[:, 1]).all() and torch.equal(y[:, others], clean[:, others])
+    y1, h1 = _step(dict(p, lam=lam), 8.0)
+    assert torch.isnan(y1[:, 1]).all() and torch.isnan(h1[:, 1]).all() and torch.isfinite(h1[:, others]).all()
