@@ -493,8 +493,10 @@ mamba_status mamba_int8_matmul_form(int64_t batch, int64_t M, int64_t N, int64_t
  *   workspace     : mamba_gated_scan_fwd_workspace_size(B, D, L) bytes, 256-byte
  *                   aligned (0, and none needed, but for few rows of many steps);
  *                   scratch as in the scan
- * c is finite and not negative.  A step with r = -infinity and a finite x leaves
- * the state as it is: padded tokens.  A state that becomes infinite is NaN from the
+ * c is finite and not negative.  lam and the biases may be infinite: a channel of lam =
+ * -infinity keeps its state, one of +infinity forgets it; c softplus(lam) and r_bias
+ * past the largest float count as that.  A step with r = -infinity and a finite x leaves
+ * the state as it is, whatever they are: padded tokens.  A state that becomes infinite is NaN from the
  * next step that decays it on.  B * D < 2^24.  With L = 0, h_last = h0 (or zeros).
  */
 int64_t mamba_gated_scan_checkpoints(int64_t L);

@@ -178,6 +178,18 @@ __device__ __forceinline__ float softplus_row(float x)
     return fmaxf(x, 0.f) + 2.f * q * s;
 }
 
+// A row's v = rate * sigmoid(r + r_bias) and the bias of a gate, in exponents of 2.  An infinite
+// one counts as the largest float, so that r = -infinity, which the steps past a row's end
+// have too, makes v 0 whatever they are (0 * infinity and infinity - infinity are NaN).  By
+// a comparison, which lets a NaN through.
+__device__ __forceinline__ float held(float v)
+{
+    constexpr float kMost = 3.402823466e38f;
+    return fabsf(v) > kMost ? copysignf(kMost, v) : v;
+}
+__device__ __forceinline__ float row_rate(float c, float lam) { return held(c * softplus_row(lam) * kLog2e); }
+__device__ __forceinline__ float row_bias(float bias) { return held(bias * kLog2e); }
+
 // 1 - a^2 for a = 2^-u, u >= 0.  Below 1/8 by a polynomial in u (through (1 - 2^-2u) / u at
 // the interval's Chebyshev points; off by 1e-8 relative at most); above, the subtraction
 // keeps all but three bits.

@@ -77,8 +77,8 @@ __global__ __launch_bounds__(gated_threads(WAVES)) void gated_bwd_kernel(const G
     const int64_t mine = wave * (G * kLaneSteps);  // of the wave
     if (base >= 0)
         fetch(base + mine);
-    const float rate = p.f.c * softplus_row(lam) * kLog2e;
-    const float rb = r_bias * kLog2e, ib = i_bias * kLog2e;
+    const float rate = row_rate(p.f.c, lam);
+    const float rb = row_bias(r_bias), ib = i_bias * kLog2e;
     int turn = 0;
     for (; base >= start; base -= kSpan) {
         const int64_t t = base + mine;
@@ -258,8 +258,8 @@ __global__ __launch_bounds__(256) void gated_back_maps_kernel(const GatedScanBwd
     const T *r = (const T *)p.f.r + at * p.f.L, *dout = (const T *)p.dout + at * p.f.L;
     const T *z = GATE ? (const T *)p.f.z + at * p.f.L : nullptr;
     const uint8_t *reset = RESET ? p.f.reset + (int64_t)((uint32_t)at / (uint32_t)p.f.D) * p.f.L : nullptr;
-    const float rate = p.f.c * softplus_row(p.f.lam[d]) * kLog2e;
-    const float rb = p.f.r_bias ? p.f.r_bias[d] * kLog2e : 0.f;
+    const float rate = row_rate(p.f.c, p.f.lam[d]);
+    const float rb = p.f.r_bias ? row_bias(p.f.r_bias[d]) : 0.f;
     const int64_t start = part * p.f.part_steps, stop = start + p.f.part_steps < p.f.L ? start + p.f.part_steps : p.f.L;
     Span<RESET> all{0.f, 0.f};
     Eight<BF16> nr, nd, nz;

@@ -86,8 +86,8 @@ __global__ __launch_bounds__(gated_threads(WAVES)) void gated_fwd_kernel(const G
     int64_t t = from + wave * (G * kLaneSteps);  // of the wave
     fetch(t);
     // worked out while the first loads are on their way
-    const float rate = p.c * softplus_row(lam) * kLog2e;  // of the exponents of 2
-    const float rb = r_bias * kLog2e, ib = i_bias * kLog2e;
+    const float rate = row_rate(p.c, lam);  // of the exponents of 2
+    const float rb = row_bias(r_bias), ib = i_bias * kLog2e;
     int turn = 0;
     for (int64_t base = from; base < stop; base += kSpan, t += kSpan) {
         const Eight<BF16> cx = nx, cr = nr, ci = ni, cz = nz;
@@ -147,8 +147,8 @@ template <bool BF16, bool RESET> __global__ __launch_bounds__(256) void gated_ma
     const uint32_t d = (uint32_t)at % (uint32_t)p.D;
     const T *x = (const T *)p.x + at * p.L, *r = (const T *)p.r + at * p.L, *i = (const T *)p.i + at * p.L;
     const uint8_t *reset = RESET ? p.reset + (int64_t)((uint32_t)at / (uint32_t)p.D) * p.L : nullptr;
-    const float rate = p.c * softplus_row(p.lam[d]) * kLog2e;
-    const float rb = p.r_bias ? p.r_bias[d] * kLog2e : 0.f, ib = p.i_bias ? p.i_bias[d] * kLog2e : 0.f;
+    const float rate = row_rate(p.c, p.lam[d]);
+    const float rb = p.r_bias ? row_bias(p.r_bias[d]) : 0.f, ib = p.i_bias ? p.i_bias[d] * kLog2e : 0.f;
     const int64_t from = blockIdx.y * p.part_steps;  // whole chunks, and none of them a row's last
     const int64_t stop = from + p.part_steps;
     Span<RESET> all{0.f, 0.f};
@@ -242,8 +242,8 @@ __global__ __launch_bounds__(256) void gated_step_kernel(const GatedStepArgs p, 
     float rate[EACH], rb[EACH], ib[EACH];
 #pragma unroll
     for (int j = 0; j < EACH; ++j) {
-        rate[j] = p.c * softplus_row(p.lam[d + j]) * kLog2e;
-        rb[j] = p.r_bias ? p.r_bias[d + j] * kLog2e : 0.f;
+        rate[j] = row_rate(p.c, p.lam[d + j]);
+        rb[j] = p.r_bias ? row_bias(p.r_bias[d + j]) : 0.f;
         ib[j] = p.i_bias ? p.i_bias[d + j] * kLog2e : 0.f;
     }
     const int64_t end = b0 + sequences < p.B ? b0 + sequences : p.B;

@@ -111,3 +111,49 @@ def test_nan_lam_stays_in_its_channel():
     assert torch.isnan(y[:, 1]).all() and torch.equal(y[:, others], clean[:, others])
     y1, h1 = _step(dict(p, lam=lam), 8.0)
     assert torch.isnan(y1[:, 1]).all() and torch.isnan(h1[:, 1]).all() and torch.isfinite(h1[:, others]).all()
+
+
+# (lam, r_bias, i_bias): gates that are always open or shut, rates past the largest float
+ENDS = [(-3.0, INF, 0.5), (-3.0, -INF, 0.5), (-3.0, 3e38, 0.5), (-3.0, -3e38, 0.5), (INF, 0.3, -0.2), (3e38, 0.3, -0.2),
+        (INF, INF, 0.1), (INF, -INF, 0.1), (-INF, INF, 0.1), (-3.0, 0.2, INF), (-3.0, 0.2, -INF), (INF, INF, INF), (-2.0, 0.1, 0.4)]
+FORGETS = [4, 5, 6, 11]  # channels of those
+# one step, and lengths that leave a part of a lane, of its group, of a chunk, of the waves of a row and of a row's last part
+ODD = [1, 5, 30, 32, 100, 200, 257, 300, 511, 700, 1024, 3600, 8200, 16400]
+
+
+@pytest.mark.parametrize("io,reset", [(F32, 0.0), (BF16, 0.02)])
+@pytest.mark.parametrize("L", ODD)
+def test_infinite_parameters(L, io, reset):
+    """Infinite parameters give the same at every length, and r = -inf leaves the state beside them too."""
+    say(f"gated scan infinite parameters L={L} {io}")
+    p = C.make(2, len(ENDS), L, io, seed=L, gate=io == BF16, reset=reset)
+    for k, name in enumerate(PARAMETERS):
+        p[name] = torch.tensor([e[k] for e in ENDS])
+    p["r"][1, :, 2 * L // 3:] = -INF
+    _check(p, L + 1, forgets=FORGETS)
+
+
+@pytest.mark.parametrize("c,lam", [(3e38, 5.0), (1e30, 1e20), (1e-30, INF)])
+def test_rates_past_the_largest_float(c, lam):
+    say(f"gated scan c={c} lam={lam}")
+    p = C.make(1, 3, 700, F32, seed=9, reset=0.01)
+    p["lam"] = torch.tensor([lam, lam, -INF])
+    _check(p, 10, c=c, forgets=[0, 1])
+
+
+@pytest.mark.parametrize("name", PARAMETERS)
+def test_nan_parameters_stay_in_their_channel(name):
+    for L in (20, 700):
+        p = C.make(2, 4, L, F32, seed=12, reset=0.02)
+        q = C.gradient_inputs(p, 13)
+        clean, clean_last = _call(p, "gated_scan_fwd", return_last_state=True)
+        bad = dict(p, **{name: p[name].clone()})
+        bad[name][2] = torch.nan
+        y, last = _call(bad, "gated_scan_fwd", return_last_state=True)
+        others = torch.tensor([0, 1, 3])
+        assert torch.isnan(y[:, 2]).all() or name != "i_bias" and torch.isnan(y[:, 2]).any()
+        assert torch.equal(y[:, others], clean[:, others]) and torch.equal(last[:, others], clean_last[:, others])
+        a, b = (_call(t, "gated_scan_bwd", q["dout"].cuda()) for t in (p, bad))
+        for g in GRADS:
+            across = (lambda t: t[others]) if g in ("dlam", "dr_bias", "di_bias") else (lambda t: t[:, others])
+            assert torch.equal(across(a[g]), across(b[g])), g
