@@ -218,7 +218,8 @@ __device__ __forceinline__ float read_lane(float v, int lane)
 }
 
 // A span's map s -> 2^-U s + S.  `after`: this one behind another.  With DROPS a map
-// of U = infinity (a reset) drops even a NaN or an infinity of what lies before it.
+// of U = infinity (a reset) drops even a NaN or an infinity of what lies before it.  The
+// exponents of a lane's steps are held at 1e30, so that no sum of them comes to that.
 template <bool DROPS> struct Span {
     float U, S;
     __device__ __forceinline__ float of(float s) const
@@ -232,6 +233,13 @@ template <bool DROPS> struct Span {
         U = DROPS && U == __builtin_inff() ? U : U + before.U;
     }
 };
+
+template <bool DROPS> __device__ __forceinline__ Span<DROPS> lane_span(float U, bool reset, float S)
+{
+    if constexpr (DROPS)
+        U = reset ? __builtin_inff() : fminf(U, 1e30f);  // of a NaN too: S is one then
+    return {U, S};
+}
 
 template <int CTRL, int ROWS = 0xf, bool DROPS>
 __device__ __forceinline__ Span<DROPS> span_of_lane(const Span<DROPS> &m)

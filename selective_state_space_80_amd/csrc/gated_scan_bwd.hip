@@ -108,9 +108,7 @@ __global__ __launch_bounds__(gated_threads(WAVES)) void gated_bwd_kernel(const G
                 dropped = true;
             }
         }
-        if (RESET && dropped)
-            sum = __builtin_inff();
-        M m{sum, h};
+        M m = lane_span<RESET>(sum, dropped, h);
         h = join_before<G, RESET>(m).of(state);
         // h before each step; the output's gradient, through the gate
         float before[kLaneSteps], grad[kLaneSteps], dgate[kLaneSteps];
@@ -136,7 +134,7 @@ __global__ __launch_bounds__(gated_threads(WAVES)) void gated_bwd_kernel(const G
             if (RESET && (first >> j & 1))
                 behind = 0.f;
         }
-        M back{sum, behind};
+        M back = lane_span<RESET>(sum, dropped, behind);
         const M from = join_behind<G, RESET>(back);
         float enter = carry;
         if constexpr (WAVES > 1) {
@@ -294,7 +292,7 @@ __global__ __launch_bounds__(256) void gated_back_maps_kernel(const GatedScanBwd
             if (RESET && (first >> j & 1))
                 behind = 0.f;
         }
-        Span<RESET> m{RESET && first != 0 ? __builtin_inff() : sum, behind};
+        Span<RESET> m = lane_span<RESET>(sum, first != 0, behind);
         join_behind<64, RESET>(m);
         Span<RESET> chunk = read_span(m, 0);
         chunk.after(all);

@@ -41,7 +41,7 @@ __device__ __forceinline__ Span<RESET> lane_steps(const Eight<BF16> &x, const Ei
             dropped = true;
         }
     }
-    return {RESET && dropped ? __builtin_inff() : sum, h};
+    return lane_span<RESET>(sum, dropped, h);
 }
 
 template <int G, int WAVES, bool BF16, bool GATE, bool RESET, bool PARTS>

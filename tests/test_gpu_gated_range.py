@@ -157,3 +157,16 @@ def test_nan_parameters_stay_in_their_channel(name):
         for g in GRADS:
             across = (lambda t: t[others]) if g in ("dlam", "dr_bias", "di_bias") else (lambda t: t[:, others])
             assert torch.equal(across(a[g]), across(b[g])), g
+
+
+@pytest.mark.parametrize("L", [40, 700, 3600, 16400])
+def test_nan_meets_a_channel_that_forgets(L):
+    """0 times NaN: a decay to nothing is no reset, and drops no NaN; a reset behind it does."""
+    p = C.make(1, 2, L, F32, seed=14)
+    p["lam"] = torch.tensor([INF, 3e38])
+    p["reset"] = torch.zeros(1, L, dtype=torch.bool)
+    p["reset"][0, L // 2] = True
+    p["x"][0, :, 3] = torch.nan
+    y, last = _call(p, "gated_scan_fwd", return_last_state=True)
+    assert torch.isnan(y[..., 3:L // 2]).all() and torch.isfinite(y[..., :3]).all()
+    assert torch.isfinite(y[..., L // 2:]).all() and torch.isfinite(last).all()
