@@ -496,8 +496,10 @@ mamba_status mamba_int8_matmul_form(int64_t batch, int64_t M, int64_t N, int64_t
  * c is finite and not negative.  lam and the biases may be infinite: a channel of lam =
  * -infinity keeps its state, one of +infinity forgets it; c softplus(lam) and r_bias
  * past the largest float count as that.  A step with r = -infinity and a finite x leaves
- * the state as it is, whatever they are: padded tokens.  A state that becomes infinite is NaN from the
- * next step that decays it on.  B * D < 2^24.  With L = 0, h_last = h0 (or zeros).
+ * the state as it is, whatever they are: padded tokens.  A state that becomes infinite
+ * is not finite again before a reset: it stays infinite, or is NaN from where the decay
+ * leaves the fp32 range (v above 87) on, that of one step or, in the scan, which joins
+ * steps, of several together.  B * D < 2^24.  With L = 0, h_last = h0 (or zeros).
  */
 int64_t mamba_gated_scan_checkpoints(int64_t L);
 size_t mamba_gated_scan_fwd_workspace_size(int64_t B, int64_t D, int64_t L);

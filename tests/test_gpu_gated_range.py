@@ -170,3 +170,34 @@ def test_nan_meets_a_channel_that_forgets(L):
     y, last = _call(p, "gated_scan_fwd", return_last_state=True)
     assert torch.isnan(y[..., 3:L // 2]).all() and torch.isfinite(y[..., :3]).all()
     assert torch.isfinite(y[..., L // 2:]).all() and torch.isfinite(last).all()
+
+
+@pytest.mark.parametrize("L", [20, 300, 700, 3600, 16400])
+def test_an_infinite_state(L):
+    """It is infinite, then from where a decay over several steps leaves fp32's range NaN, and
+    never finite again without a reset; what is before it and beside it stays as it is."""
+    p = C.make(1, 3, L, F32, seed=15, gate=False, reset=1e-9)  # no reset: the variant that has them
+    assert not p["reset"].any()
+    clean, clean_last = _call(p, "gated_scan_fwd", return_last_state=True)
+    at = L // 3
+    bad = dict(p, x=p["x"].clone(), h0=p["h0"].clone())
+    bad["x"][0, 1, at] = INF
+    bad["h0"][0, 2] = -INF
+    for reset in (p["reset"], None):
+        y, last = _call(dict(bad, reset=reset), "gated_scan_fwd", return_last_state=True)
+        assert torch.equal(y[0, 0], clean[0, 0]) and torch.equal(y[0, 1, :at], clean[0, 1, :at])
+        assert y[0, 1, at] == INF and y[0, 2, 0] == -INF
+        for t in (y[0, 1, at:], y[0, 2], last[0, 1:]):
+            assert not torch.isfinite(t).any()
+        assert not (y[0, 1] == -INF).any() and not (y[0, 2] == INF).any()
+
+
+def test_an_infinite_state_step_by_step():
+    """As long as a step's own decay is in fp32's range, it stays infinite."""
+    p = C.make(1, 3, 400, F32, seed=16, gate=False, biases=False)
+    g = {k: None if v is None else v.cuda() for k, v in p.items()}
+    h = torch.tensor([[INF, -INF, 1.0]], device="cuda")
+    for t in range(400):
+        y = _mamba().gated_state_update(h, *(g[n][..., t].contiguous() for n in ("x", "r", "i")), g["lam"])
+        assert torch.equal(y, h)
+    assert h[0, 0] == INF and h[0, 1] == -INF and torch.isfinite(h[0, 2])
