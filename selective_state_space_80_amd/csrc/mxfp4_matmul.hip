@@ -103,9 +103,11 @@ template <int N> struct ScaleLoads {
 // What bounds it is the card's power, then the rate at which lines reach LDS: 256 x 256
 // outputs by 8 waves keep the matrix units busy for 59 % of the cycles at 8192^3 on random
 // bytes, at 1.6 GHz (4.2 to 4.4 PFLOP/s); with zeros as data 5.8, which takes 52 bytes a
-// ns and CU of the 60 that the caches give all of them.  At 8 x 5120 x 2048 x 2560 (110 us,
-// 45 % busy; zeros 94) the tiles' ends add to it: a tile's stores and the loads behind them
-// are counted by one counter, in order, so a step after the next waits for the stores.
+// ns and CU of the 60 that the caches give all of them.  At 8 x 5120 x 2048 x 2560 (109 to
+// 121 us from one card to the next, 45 % busy) power is the smaller part: with zeros as data
+// it takes 94 to 99, 4.3 to 4.6 PFLOP/s.  The rest are the tiles' ends, of ten steps each: a
+// tile's stores and the loads behind them are counted by one counter, in order, so a step
+// after the next waits for the stores.
 constexpr int kStaging = 2048;  // of a wave's outputs: 16 rows of 128 bytes
 constexpr int scale_loads(int rows, int waves) { return (rows + 32 * waves - 1) / (32 * waves); }
 constexpr int stage_bytes(int rows, int waves) { return rows * kStep + scale_loads(rows, waves) * waves * 256; }
@@ -544,16 +546,18 @@ template <bool BF16> __global__ __launch_bounds__(256) void zero_kernel(void *ou
 // group on an otherwise free card; busy: with every slot taken, where power and the
 // shared caches hold the rate; each: a tile's end.  The constants are fitted to 1000
 // shapes drawn from 1 x 16 to 65536 x 8192 with 64 to 8192 of the inner axis, each timed
-// in every form; the form chosen takes 1.9 % more than the fastest on average, 5.3 % at
-// the ninetieth percentile, and 31 % at the worst (30044 x 4360 x 107: 78 us, 59).  Both
-// sides of some of the choices, in us:
-//   8 x 5120 x 2048 x 2560   256 x 256 tiles 110, 128 x 128 130
-//   16384 x 1536 x 768       128 x 128 tiles of two stages 19.9, 256 x 256 22.2, 128 x 64 35.6
-//   256 x 5120 x 2560        128 x 128 tiles of two stages 8.5, of four 8.9, rings of 48 x 64 9.4
-//   512 x 1536 x 768         rings of 64 x 48 4.4, of 48 x 64 6.4, 128 x 128 tiles 4.9
-//   256 x 2560 x 5120        rings of 64 x 48 6.8, of 64 x 64 7.7, 128 x 128 tiles 13.4
-//   64 x 2560 x 5120         rings of 32 x 32 4.4, of 32 x 64 5.3, of 16 x 16 6.0
-//   1 x 5120 x 2560          rings of 32 x 32 4.2, of 64 x 64 5.5, 128 x 128 tiles 8.1
+// in every form, when tiles were walked in bands of two rows.  Bands of six made the large
+// products 4 to 8 % faster; of 1000 other shapes timed with them the form chosen takes 1.7 %
+// more than the fastest on average, 4.6 % at the ninetieth percentile, and 35 % at the worst
+// (8121 x 25236 x 107: 145 us, 108 by 128 x 128 tiles of four stages).  Both sides of some
+// of the choices, in us:
+//   8 x 5120 x 2048 x 2560   256 x 256 tiles 116, 128 x 128 146
+//   16384 x 1536 x 768       128 x 128 tiles of two stages 18.7, 256 x 256 20.5, 128 x 64 40.5
+//   256 x 5120 x 2560        128 x 128 tiles of two stages 9.3, of four 9.6, rings of 48 x 64 9.9
+//   512 x 1536 x 768         rings of 64 x 48 4.5, of 48 x 64 6.4, 128 x 128 tiles 5.4
+//   256 x 2560 x 5120        rings of 64 x 48 7.1, of 64 x 64 7.9, 128 x 128 tiles 13.9
+//   64 x 2560 x 5120         rings of 32 x 32 4.7, of 32 x 64 5.6, of 16 x 16 6.3
+//   1 x 5120 x 2560          rings of 16 x 32 3.7, of 32 x 32 4.3, of 64 x 64 5.7, 128 x 128 tiles 8.9
 enum Form { kTile256, kTile128, kTile128Deep, kTile64, kRing44, kRing34, kRing43, kRing24, kRing42, kRing22, kRing12, kRing21, kRing11, kForms };
 struct FormCost {
     int tm, tn, slots;
